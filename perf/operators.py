@@ -42,13 +42,13 @@ def listed():
              fmt="mxfp4"),
         # one token through a down projection
         dict(name="product_one_token", op="product", M=1, N=2688, K=1856, a="mxfp8", w="mxfp4",
-             out="f32"),
-        # a decode batch through an up projection
-        dict(name="product_decode", op="product", M=64, N=1856, K=2688, a="mxfp4", w="mxfp4",
              out="bf16"),
+        # a decode batch through an up projection, fp32 results for a sum outside
+        dict(name="product_decode", op="product", M=64, N=1856, K=2688, a="mxfp4", w="mxfp4",
+             out="f32"),
         # a ragged batch through a projection of the LatentMoE width, 8 bits on both sides
         dict(name="product_ragged", op="product", M=1999, N=1040, K=4096, a="mxfp8", w="mxfp8",
-             out="f32"),
+             out="bf16"),
         # a prefill batch through the shared expert's up projection, 4 bits on both sides
         dict(name="product_prefill", op="product", M=8192, N=3712, K=2688, a="mxfp4", w="mxfp4",
              out="bf16"),
@@ -79,9 +79,9 @@ def draw(rng):
                     dt=rng.choice(["bf16", "f32"]), fmt=rng.choice(["mxfp4", "mxfp8"]))
     if op == "product":
         N, K = 16 * _log(rng, 1, 256), BLOCK * _log(rng, 1, 128)
+        a, w = rng.choice(["mxfp4", "mxfp8"]), rng.choice(["mxfp4", "mxfp8"])
         return dict(op=op, M=_log(rng, 1, min(8192, 8192 * 3712 * 2688 // (N * K))), N=N, K=K,
-                    a=rng.choice(["mxfp4", "mxfp8"]), w=rng.choice(["mxfp4", "mxfp8"]),
-                    out=rng.choice(["bf16", "f32"]))
+                    a=a, w=w, out=rng.choice(["bf16", "f32"]) if a == w == "mxfp4" else "bf16")
     if op == "experts":
         shape = rng.choice(["nano", "latent", "small"])
         return dict(op=op, T=_log(rng, 17, 8192 if shape != "latent" else 4096),
