@@ -6,9 +6,9 @@ The layer runs in hand-written HIP kernels behind the C ABI declared in include/
 is its thin Python binding: torch provides device memory and streams.
 """
 from .binding import (Backward, Layer, MoeError, alloc_routing, backward_from, bias_update,
-                      dispatch, layer_forward, layer_from, lib, route, status_str, to_device,
-                      workspace_size)
+                      dispatch, layer_forward, layer_from, lib, mx_dequantize, mx_gemm,
+                      mx_quantize, route, status_str, to_device, workspace_size)
 
 __all__ = ["Backward", "Layer", "MoeError", "alloc_routing", "backward_from", "bias_update",
-           "dispatch", "layer_forward", "layer_from", "lib", "route", "status_str", "to_device",
-           "workspace_size"]
+           "dispatch", "layer_forward", "layer_from", "lib", "mx_dequantize", "mx_gemm",
+           "mx_quantize", "route", "status_str", "to_device", "workspace_size"]

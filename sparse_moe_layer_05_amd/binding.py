@@ -19,13 +19,18 @@ _EXPERT_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "e4m3": MOE_FP8_E4M3, "mxfp4
                   "mxfp8": MOE_MXFP8}
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
 PATH_AUTO, PATH_GROUPED, PATH_STREAM, ROUTING_GIVEN, SAVED_IN_WORKSPACE = 0, 1, 2, 4, 8
-WGRAD_BF16 = 16
-_PATHS = {"auto": PATH_AUTO, "grouped": PATH_GROUPED, "stream": PATH_STREAM}
+WGRAD_BF16, MX_GROUPED = 16, 32
+# "grouped_mx": matrix-core tiles for MXFP4 / MXFP8 experts (many tokens)
+_PATHS = {"auto": PATH_AUTO, "grouped": PATH_GROUPED, "stream": PATH_STREAM,
+          "grouped_mx": MX_GROUPED}
+_MX_FORMATS = {"mxfp4": MOE_MXFP4, "mxfp8": MOE_MXFP8}
+MX_BLOCK = 32
 
 EXPORTS = ("moe_workspace_size", "moe_layer_forward", "latent_moe_forward", "moe_route",
            "moe_dispatch_workspace_size", "moe_dispatch", "moe_bias_update",
            "moe_backward_workspace_size", "moe_layer_forward_train", "moe_layer_backward",
-           "moe_layer_forward_static", "moe_status_str",
+           "moe_layer_forward_static", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
+           "moe_status_str",
            "moe_trace_enable",
            "moe_trace_count", "moe_trace_read", "moe_trace_reset")
 
@@ -86,6 +91,9 @@ def lib() -> C.CDLL:
                                              C.POINTER(MoeGrads), vp, sz, vp]
             L.moe_layer_forward_train.argtypes = [C.POINTER(MoeDesc), C.POINTER(MoeWeights), vp,
                                                   vp, sz, vp]
+            L.moe_mx_quantize.argtypes = [vp, i32, C.c_int64, i32, i32, vp, vp, vp]
+            L.moe_mx_dequantize.argtypes = [vp, vp, i32, C.c_int64, i32, vp, i32, vp]
+            L.moe_mx_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp]
             L.moe_status_str.argtypes = [i32]
             L.moe_trace_enable.argtypes = [i32, C.c_char_p]
             L.moe_trace_count.argtypes = []
@@ -398,6 +406,101 @@ def bias_update(counts, b, gamma: float, target=None, stream=None) -> None:
     rc = lib().moe_bias_update(_p(counts), _p(target) if target is not None else None, E,
                                float(gamma), _p(b), _stream(stream))
     _check(rc, "moe_bias_update")
+
+
+def _float_code(dtype: torch.dtype) -> int:
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype {dtype} is neither float32 nor bfloat16")
+    return MOE_F32 if dtype == torch.float32 else MOE_BF16
+
+
+def _on_gpu(t, what):
+    """The device that a call runs on: that of its first tensor, whatever device is current."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} is on {t.device}, expected a GPU")
+    return torch.cuda.device(t.device)
+
+
+def _mx_format(codes, scales, what):
+    """(moe_dtype_t, element columns) of a block-scaled matrix, read off its shapes: one scale per
+    32 columns, two MXFP4 elements or one MXFP8 element per byte."""
+    for t, n in ((codes, what), (scales, f"the scales of {what}")):
+        if t is None or t.dtype != torch.uint8:
+            raise ValueError(f"{n} must be a uint8 tensor")
+    if codes.dim() < 1 or scales.shape[:-1] != codes.shape[:-1] or scales.device != codes.device:
+        raise ValueError(f"{what} {tuple(codes.shape)} on {codes.device} and its scales "
+                         f"{tuple(scales.shape)} on {scales.device} do not belong together")
+    cols = MX_BLOCK * scales.shape[-1]
+    if cols and codes.shape[-1] * 2 == cols:
+        return MOE_MXFP4, cols
+    if cols and codes.shape[-1] == cols:
+        return MOE_MXFP8, cols
+    raise ValueError(f"{what}: {codes.shape[-1]} bytes and {scales.shape[-1]} scales a row are "
+                     "neither MXFP4 nor MXFP8")
+
+
+def mx_quantize(x, fmt="mxfp4", *, codes=None, scales=None, stream=None):
+    """(codes, scales) of x [.., cols] (float32 or bfloat16, contiguous) in the OCP microscaling
+    format ``fmt``, laid out as block-scaled expert weights are: codes [.., cols / 2] ("mxfp4")
+    or [.., cols] ("mxfp8"), scales [.., cols / 32], both uint8. See moe_mx_quantize in moe.h."""
+    if fmt not in _MX_FORMATS:
+        raise ValueError(f"fmt {fmt!r} is not one of {sorted(_MX_FORMATS)}")
+    dt = _float_code(x.dtype)
+    if x.dim() < 1 or x.shape[-1] % MX_BLOCK or not x.shape[-1]:
+        raise ValueError(f"x {tuple(x.shape)}: the last dimension is not a multiple of {MX_BLOCK}")
+    cols, lead = x.shape[-1], tuple(x.shape[:-1])
+    u8 = dict(dtype=torch.uint8, device=x.device)
+    per = 2 if fmt == "mxfp4" else 1
+    with _on_gpu(x, "x"):
+        made = [t is None for t in (codes, scales)]
+        codes = torch.empty(lead + (cols // per,), **u8) if codes is None else codes
+        scales = torch.empty(lead + (cols // MX_BLOCK,), **u8) if scales is None else scales
+        _need(codes, lead + (cols // per,), "codes", torch.uint8, x.device)
+        _need(scales, lead + (cols // MX_BLOCK,), "scales", torch.uint8, x.device)
+        rc = lib().moe_mx_quantize(_p(x), dt, x.numel() // cols, cols, _MX_FORMATS[fmt], _p(codes),
+                                   _p(scales), _stream(stream))
+        _check(rc, "moe_mx_quantize")
+        _used_on(stream, codes if made[0] else None, scales if made[1] else None)
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, *, dtype=torch.float32, out=None, stream=None):
+    """The values [.., cols] (float32 or bfloat16) that MXFP4 / MXFP8 codes and scales stand for;
+    the format is read off the shapes. See moe_mx_dequantize in moe.h."""
+    fmt, cols = _mx_format(codes, scales, "codes")
+    dt = _float_code(dtype)
+    shape = tuple(codes.shape[:-1]) + (cols,)
+    with _on_gpu(codes, "codes"):
+        made = out is None
+        out = torch.empty(shape, dtype=dtype, device=codes.device) if made else out
+        _need(out, shape, "out", dtype, codes.device)
+        rc = lib().moe_mx_dequantize(_p(codes), _p(scales), fmt, out.numel() // cols, cols, _p(out),
+                                     dt, _stream(stream))
+        _check(rc, "moe_mx_dequantize")
+        _used_on(stream, out if made else None)
+    return out
+
+
+def mx_gemm(a, a_scales, w, w_scales, *, out_dtype=torch.bfloat16, out=None, stream=None):
+    """C [M, N] = A [M, K] W [N, K]^T of two block-scaled matrices (each MXFP4 or MXFP8, read off
+    the shapes), fp32 accumulation, as bfloat16, or float32 for two MXFP4 operands. See
+    moe_mx_gemm in moe.h."""
+    fa, K = _mx_format(a, a_scales, "a")
+    fw, kw = _mx_format(w, w_scales, "w")
+    if a.dim() != 2 or w.dim() != 2 or K != kw or a.device != w.device:
+        raise ValueError(f"a {tuple(a.shape)} ({K} columns, {a.device}) and w {tuple(w.shape)} "
+                         f"({kw} columns, {w.device}) do not multiply")
+    dt = _float_code(out_dtype)
+    shape = (a.shape[0], w.shape[0])
+    with _on_gpu(a, "a"):
+        made = out is None
+        out = torch.empty(shape, dtype=out_dtype, device=a.device) if made else out
+        _need(out, shape, "out", out_dtype, a.device)
+        rc = lib().moe_mx_gemm(_p(a), _p(a_scales), fa, _p(w), _p(w_scales), fw, shape[0], shape[1],
+                               K, _p(out), dt, _stream(stream))
+        _check(rc, "moe_mx_gemm")
+        _used_on(stream, out if made else None)
+    return out
 
 
 def trace_enable(capacity: int, prefix: str = "") -> None:

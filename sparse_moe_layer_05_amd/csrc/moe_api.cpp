@@ -11,6 +11,7 @@
 #include "backward.hpp"
 #include "gemm_kt.hpp"
 #include "kernels.hpp"
+#include "mx.hpp"
 
 using namespace moe;
 
@@ -54,7 +55,10 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
   // block-scaled rows are whole 32-element blocks, in both projections
   const int64_t Dw = L ? L : H;
   if (mx && (Dw % 32 || I % 32)) return MOE_ERR_INVALID_ARG;
-  if (d->flags & ~(MOE_PATH_MASK | MOE_ROUTING_GIVEN)) return MOE_ERR_INVALID_ARG;
+  if (d->flags & ~(MOE_PATH_MASK | MOE_ROUTING_GIVEN | MOE_MX_GROUPED)) return MOE_ERR_INVALID_ARG;
+  const bool mx_grouped = d->flags & MOE_MX_GROUPED;
+  if (mx_grouped && (d->flags & MOE_PATH_MASK) != MOE_PATH_AUTO) return MOE_ERR_INVALID_ARG;
+  if (mx_grouped && !mx) return MOE_ERR_UNSUPPORTED;
   Plan p;
   p.act = d->act_dtype == MOE_F32 ? Elt::F32 : Elt::BF16;
   p.ex = fp8 ? Elt::FP8
@@ -63,9 +67,12 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
   p.T = (int)T; p.H = (int)H; p.E = (int)E; p.k = (int)k; p.I = (int)I; p.Is = (int)Is;
   p.L = (int)L; p.D = L ? (int)L : (int)H; p.P = (int)(T * k);
   const uint32_t path = d->flags & MOE_PATH_MASK;
-  // the decode path streams bf16, e4m3 and block-scaled experts (the last have no other path)
+  // the decode path streams bf16, e4m3 and block-scaled experts (which leave it only when
+  // MOE_MX_GROUPED asks for their matrix-core tiles)
   const bool stream_ok = p.act == Elt::BF16 && (p.ex == Elt::BF16 || fp8 || mx);
-  if (path == MOE_PATH_AUTO)
+  if (mx_grouped)
+    p.path = MOE_PATH_GROUPED;
+  else if (path == MOE_PATH_AUTO)
     p.path = (stream_ok && ((int64_t)p.P <= 8 * E || mx)) ? MOE_PATH_STREAM : MOE_PATH_GROUPED;
   else if (path == MOE_PATH_STREAM)
     p.path = stream_ok ? MOE_PATH_STREAM : -1;
@@ -495,7 +502,39 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
     dn.B = w->W_down; dn.ldb = I; dn.b_gstride = (int64_t)D * I;
     dn.C = Y; dn.ldc = D; dn.N = D; dn.K = I;
     dn.offs = offsets; dn.mt_start = mt_start; dn.G = E; dn.bm = pl.bm;
-    if (pl.ex == Elt::FP8) {
+    if (pl.ex == Elt::MXFP4 || pl.ex == Elt::MXFP8) {
+      // block-scaled expert weights: rows quantised per row to e4m3 as on the decode path, both
+      // projections on the block-scaled matrix cores
+      const bool f4 = pl.ex == Elt::MXFP4;
+      uint8_t* xq = base + pl.xq;
+      float* sx = (float*)(base + pl.sx);
+      uint8_t* hq = base + pl.hq;
+      float* sh = (float*)(base + pl.sh);
+      {
+        MOE_SPAN("quant_rows:x");
+        MOE_TRY(launch_quant_rows((const uint16_t*)xin, D, T, D, xq, sx, s));
+      }
+      MxGemmParams m;
+      m.offs = offsets; m.mt_start = mt_start; m.G = E;
+      m.A = xq; m.a_row = sx; m.a_rows = T; m.a_gather = perm;
+      m.W = (const uint8_t*)w->W_up; m.w_mx = (const uint8_t*)w->s_up;
+      m.C = h; m.M = P; m.N = I; m.K = D; m.sqrelu = 1;
+      {
+        MOE_SPAN(f4 ? "gemm_mxfp4_sqrelu:routed_up" : "gemm_mxfp8_sqrelu:routed_up");
+        MOE_TRY(launch_mx_gemm(Elt::FP8, pl.ex, m, max_mt, s));
+      }
+      {
+        MOE_SPAN("quant_rows:h");
+        MOE_TRY(launch_quant_rows((const uint16_t*)h, I, P, I, hq, sh, s));
+      }
+      m.A = hq; m.a_row = sh; m.a_rows = P; m.a_gather = nullptr;
+      m.W = (const uint8_t*)w->W_down; m.w_mx = (const uint8_t*)w->s_down;
+      m.C = Y; m.N = D; m.K = I; m.sqrelu = 0;
+      {
+        MOE_SPAN(f4 ? "gemm_mxfp4_store:routed_down" : "gemm_mxfp8_store:routed_down");
+        MOE_TRY(launch_mx_gemm(Elt::FP8, pl.ex, m, max_mt, s));
+      }
+    } else if (pl.ex == Elt::FP8) {
       // e4m3 expert weights: the expert input rows and the h rows are quantised per row to
       // e4m3 (scale = row amax / 448) and both projections run on fp8 matrix cores.
       uint8_t* xq = base + pl.xq;
@@ -1076,6 +1115,60 @@ int32_t moe_bias_update(const int32_t* counts, const float* target, int32_t E, f
                         float* b, void* stream) {
   if (E < 1 || !counts || !b) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_bias_update(counts, target, E, gamma, b, (hipStream_t)stream));
+}
+
+// rows * cols elements of whole blocks, few enough for one launch
+static bool mx_shape_ok(int64_t rows, int32_t cols) {
+  return rows >= 0 && cols >= kMxBlockElts && cols % kMxBlockElts == 0 && rows <= kMxMaxElts / cols;
+}
+static bool mx_format(moe_dtype_t f) { return f == MOE_MXFP4 || f == MOE_MXFP8; }
+
+int32_t moe_mx_quantize(const void* x, moe_dtype_t dt, int64_t rows, int32_t cols,
+                        moe_dtype_t fmt, void* codes, uint8_t* scales, void* stream) {
+  if (!mx_shape_ok(rows, cols)) return MOE_ERR_INVALID_ARG;
+  if (!mx_format(fmt) || (dt != MOE_F32 && dt != MOE_BF16)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_mx_quantize(x, dt == MOE_F32 ? Elt::F32 : Elt::BF16, rows * cols,
+                                       fmt == MOE_MXFP4 ? Elt::MXFP4 : Elt::MXFP8,
+                                       (uint8_t*)codes, scales, (hipStream_t)stream));
+}
+
+int32_t moe_mx_dequantize(const void* codes, const uint8_t* scales, moe_dtype_t fmt, int64_t rows,
+                          int32_t cols, void* x, moe_dtype_t dt, void* stream) {
+  if (!mx_shape_ok(rows, cols)) return MOE_ERR_INVALID_ARG;
+  if (!mx_format(fmt) || (dt != MOE_F32 && dt != MOE_BF16)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_mx_dequantize((const uint8_t*)codes, scales,
+                                         fmt == MOE_MXFP4 ? Elt::MXFP4 : Elt::MXFP8, rows * cols,
+                                         x, dt == MOE_F32 ? Elt::F32 : Elt::BF16,
+                                         (hipStream_t)stream));
+}
+
+int32_t moe_mx_gemm(const void* A, const uint8_t* a_scales, moe_dtype_t a_fmt, const void* W,
+                    const uint8_t* w_scales, moe_dtype_t w_fmt, int32_t M, int32_t N, int32_t K,
+                    void* C, moe_dtype_t c_dt, void* stream) {
+  if (M < 0 || N < 16 || N % 16 || K < kMxBlockElts || K % kMxBlockElts) return MOE_ERR_INVALID_ARG;
+  if (!mx_format(a_fmt) || !mx_format(w_fmt) || (c_dt != MOE_F32 && c_dt != MOE_BF16))
+    return MOE_ERR_UNSUPPORTED;
+  // fp32 results only where the matrix core's sums hold fp32 (see mx_gemm.hip)
+  if (c_dt == MOE_F32 && (a_fmt != MOE_MXFP4 || w_fmt != MOE_MXFP4)) return MOE_ERR_UNSUPPORTED;
+  // 32-bit operand offsets: A and W each span less than 2 GiB
+  constexpr int64_t kOp = ((int64_t)1 << 31) - 1;
+  if ((int64_t)M * K / (a_fmt == MOE_MXFP4 ? 2 : 1) > kOp ||
+      (int64_t)N * K / (w_fmt == MOE_MXFP4 ? 2 : 1) > kOp)
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!A || !a_scales || !W || !w_scales || !C || !aligned16(A) || !aligned16(W) || !aligned16(C))
+    return MOE_ERR_INVALID_ARG;
+  hipStream_t s = (hipStream_t)stream;
+  MxGemmParams p;
+  p.A = (const uint8_t*)A; p.a_mx = a_scales; p.a_rows = M;
+  p.W = (const uint8_t*)W; p.w_mx = w_scales;
+  p.C = C; p.M = M; p.N = N; p.K = K; p.out_f32 = c_dt == MOE_F32;
+  return hip_status(launch_mx_gemm(a_fmt == MOE_MXFP4 ? Elt::MXFP4 : Elt::MXFP8,
+                                   w_fmt == MOE_MXFP4 ? Elt::MXFP4 : Elt::MXFP8, p, 0, s));
 }
 
 int32_t moe_trace_enable(int32_t capacity, const char* filter) {

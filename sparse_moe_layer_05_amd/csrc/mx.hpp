@@ -1,0 +1,44 @@
+// Launchers of the block-scaled (OCP microscaling, MX v1.0) kernels: conversion of rows to and
+// from MXFP4 / MXFP8, and products of block-scaled matrices.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm.hpp"
+
+namespace moe {
+
+constexpr int kMxBlockElts = 32;  // elements that share one E8M0 scale
+// Elements one conversion launch takes: a grid's threads (32 elements each) stay below 2^32.
+constexpr int64_t kMxMaxElts = (int64_t)1 << 36;
+
+// n elements (whole blocks, contiguous) of bf16 / fp32 -> codes and one E8M0 scale per block.
+hipError_t launch_mx_quantize(const void* x, Elt xt, int64_t n, Elt fmt, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s);
+// The values that n stored elements stand for, as bf16 / fp32.
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, Elt fmt, int64_t n,
+                                void* x, Elt xt, hipStream_t s);
+
+// C[m, n] = act( a_row[m] * sum_k A[m, k] W[n, k] ). A: MXFP4 or MXFP8 with block scales a_mx, or
+// FP8 (e4m3 codes with one fp32 scale a_row per source row). W: MXFP4 or MXFP8 with block scales
+// w_mx. Grouped launches (mt_start set) walk M-tiles of kGroupBM rows per group, as GemmParams.
+struct MxGemmParams {
+  const uint8_t* A = nullptr;        // [a_rows][K] elements, contiguous rows
+  const uint8_t* a_mx = nullptr;     // [a_rows][K / 32]
+  const float* a_row = nullptr;      // [a_rows]
+  int a_rows = 0;
+  const int32_t* a_gather = nullptr; // source row of row r (nullptr: r)
+  const uint8_t* W = nullptr;        // [G][N][K]
+  const uint8_t* w_mx = nullptr;     // [G][N][K / 32]
+  void* C = nullptr;                 // [M][N]
+  int M = 0, N = 0, K = 0;
+  int out_f32 = 0;                   // C element type: fp32, else bf16
+  int sqrelu = 0;                    // C = relu(acc)^2
+  const int32_t* offs = nullptr;     // grouped: [G + 1] row offsets
+  const int32_t* mt_start = nullptr; // grouped: [G + 1] prefix of ceil(rows_g / kGroupBM)
+  int G = 0;
+};
+hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,498 @@
+// Products of block-scaled (OCP microscaling) matrices on the gfx950 matrix cores:
+//   C[m, n] = act( sum over blocks b of 2^(sa[m, b] + sw[n, b] - 254) sum_{i in b} A[m, i] W[n, i] )
+// through v_mfma_scale_f32_*_f8f6f4, which takes E2M1 or E4M3 elements and one E8M0 scale per 32
+// of them for each operand and accumulates in fp32. A may instead be e4m3 codes with one fp32
+// scale per row (unit block scales; the row scale multiplies the result), which is how the MoE
+// layer's expert rows meet block-scaled expert weights.
+//
+// What the instruction rounds (measured with two nonzero products at chosen distances): of each
+// eight consecutive k, products are cut toward zero to multiples of 2^(e - 13), e the exponent of
+// the largest of them; the groups of eight are then added in fp32. Two E2M1 operands lose nothing
+// (products are multiples of 1/4 up to 36). With an E4M3 operand random data ends 4.5e-6 (E2M1 on
+// the other side) or 1.5e-5 off, which a bf16 result (2^-9) does not see; fp32 results are
+// offered for two E2M1 operands alone.
+//
+// Two kernels:
+//  - mx_rows_kernel, few rows: the weights are the matrix core's first operand, 16 weight rows
+//    against 16, 32 or 64 rows of A, and the workgroup's waves split K and join in LDS, so that
+//    the launch is one pass over W with every CU reading.
+//  - mx_tile_kernel, many rows: BM x BN tiles staged through LDS, dense or grouped by expert.
+//
+// Order of k (32x32x64 / 16x16x128): lane group g holds, of an E4M3 operand, k 16g .. 16g + 15
+// and KS/2 + 16g .. KS/2 + 16g + 15 (KS = 64 or 128: the two 16-byte halves of its 32 bytes), of
+// an E2M1 operand k 32g .. 32g + 31, and the scale byte it passes covers k 32g .. 32g + 31.
+#include <algorithm>
+
+#include "common.hpp"
+#include "mx.hpp"
+
+namespace moe {
+namespace {
+
+// Operand formats of the kernels: E4M3 with block scales, E2M1 with block scales, E4M3 with a
+// row scale (A only).
+enum Fmt : int { kE4 = 0, kE2 = 1, kE4Row = 2 };
+template <int F> constexpr int kBits = F == kE2 ? 4 : 8;
+template <int F> constexpr int kCode = F == kE2 ? 4 : 0;  // the instruction's format field
+
+__device__ __forceinline__ i32x8_t frag(uint4 lo, uint4 hi) {
+  return i32x8_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z,
+                 (int)hi.w};
+}
+constexpr uint4 kZero4 = {0, 0, 0, 0};
+
+__device__ __forceinline__ void store8(const MxGemmParams& p, int64_t row, int col, const float* v) {
+  if (p.out_f32) {
+    float* o = (float*)p.C + row * p.N + col;
+    *(float4*)o = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {  // one rounding, to nearest even, at the end
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+    *(uint4*)((uint16_t*)p.C + row * p.N + col) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ------------------------------------------------------------------------------- few rows
+// Workgroup (x, y): weight rows 16x .. 16x + 15 against rows 16*TB*y .. of A. Wave w takes the
+// K-steps of 128 in its contiguous share; loads of kU steps are in flight together.
+template <int FA, int FW, int TB, int NW>
+__global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxGemmParams p) {
+  constexpr int U = TB >= 4 ? 2 : 4;
+  constexpr int CA = kBits<FA> == 8 ? 2 : 1, CW = kBits<FW> == 8 ? 2 : 1;  // 16-byte chunks
+  __shared__ float part[NW][TB][16][17];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, r = lane & 15;
+  const int n0 = blockIdx.x * 16;
+  const int m0 = blockIdx.y * 16 * TB;
+  const int nb = p.K / kMxBlockElts;        // blocks of a row
+  const int nk = cdiv(p.K, 128);
+  const int per = cdiv(nk, NW);
+  const int k_lo = wave * per, k_hi = min(nk, k_lo + per);
+  const int64_t kbw = (int64_t)p.K * kBits<FW> / 8, kba = (int64_t)p.K * kBits<FA> / 8;
+  const uint8_t* w = p.W + (int64_t)(n0 + r) * kbw;
+  const uint8_t* wx = p.w_mx + (int64_t)(n0 + r) * nb;
+  const uint8_t* a[TB];
+  const uint8_t* ax[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    const int64_t row = min(m0 + 16 * t + r, p.M - 1);
+    a[t] = p.A + row * kba;
+    ax[t] = p.a_mx + row * nb;
+  }
+  f32x4_t acc[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = k_lo; k0 < k_hi; k0 += U) {
+    uint4 wf[U][CW], af[U][TB][CA];
+    int ws[U], as[U][TB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int ks = min(k0 + u, k_hi - 1);   // steps past the share re-read its last (unused)
+      // a chunk past K is read from the row's last one and zeroed; a scale past K from its last
+      auto at = [&](int bits, int c, int chunks) {
+        const int64_t el = (int64_t)ks * 128 + (chunks == 2 ? 64 * c + 16 * g : 32 * g);
+        return el < p.K ? el * bits / 8 : (int64_t)-1;
+      };
+      const int blk = min(ks * 4 + g, nb - 1);
+#pragma unroll
+      for (int c = 0; c < CW; ++c) {
+        const int64_t o = at(kBits<FW>, c, CW);
+        wf[u][c] = *(const uint4*)(w + (o < 0 ? kbw - 16 : o));
+        if (o < 0) wf[u][c] = kZero4;
+      }
+      ws[u] = wx[blk];
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+#pragma unroll
+        for (int c = 0; c < CA; ++c) {
+          const int64_t o = at(kBits<FA>, c, CA);
+          af[u][t][c] = *(const uint4*)(a[t] + (o < 0 ? kba - 16 : o));
+          if (o < 0) af[u][t][c] = kZero4;
+        }
+        as[u][t] = ax[t][blk];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u >= k_hi) break;
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            frag(wf[u][0], CW == 2 ? wf[u][CW - 1] : kZero4),
+            frag(af[u][t][0], CA == 2 ? af[u][t][CA - 1] : kZero4), acc[t], kCode<FW>, kCode<FA>,
+            0, ws[u], 0, as[u][t]);
+    }
+  }
+  // lane: C[row m0 + 16 t + lane % 16][column n0 + 4 g + i]
+#pragma unroll
+  for (int t = 0; t < TB; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[wave][t][r][4 * g + i] = acc[t][i];
+  __syncthreads();
+  // the waves' shares of K added in wave order, 8 columns per thread
+  const int item = threadIdx.x;
+  if (item < TB * 32) {
+    const int t = item >> 5, row = (item >> 1) & 15, c = (item & 1) * 8;
+    const int m = m0 + 16 * t + row;
+    if (m < p.M) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float s = part[0][t][row][c + q];
+#pragma unroll
+        for (int x = 1; x < NW; ++x) s += part[x][t][row][c + q];
+        v[q] = p.sqrelu ? sqrelu(s) : s;
+      }
+      store8(p, m, n0 + c, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------- many rows
+// A workgroup of WGM x WGN waves owns a BM x BN tile of C. Each K-step stages 128 elements of
+// every A and W row in LDS (128 bytes of E4M3, 64 of E2M1) by buffer loads straight to LDS, 1 KB
+// an instruction; the 16-byte chunks of a row are XOR-swizzled by choosing which global chunk a
+// lane fetches, so that 16 consecutive rows at one chunk index fall on distinct banks. Block
+// scales go through LDS too, 16 bytes (512 elements) of every row at a time, loaded one such
+// super-step ahead through registers: read directly by the lanes that need them, 5 scattered
+// dwords per K-step and wave would take as many address cycles as the operands.
+template <int SL> __device__ __forceinline__ int swz(int row) {
+  return SL == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
+template <int SL> __device__ __forceinline__ int slot(int row, int chunk) {
+  return row * SL + ((chunk ^ swz<SL>(row)) << 4);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)(uint32_t)bytes, 0x00020000);
+}
+
+// 16 block scales of a row from block b0 on; blocks past the row's nb read as 1 (code 127).
+// `left`: bytes of the array from the row's block b0 on.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* q, int64_t left, int valid) {
+  uint32_t v[4];
+  if (left >= 16) {
+    typedef uint32_t u32x4a1 __attribute__((ext_vector_type(4), aligned(1)));
+    const u32x4a1 x = *(const u32x4a1*)q;
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else {  // the array ends inside these 16 bytes
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = 0;
+    for (int b = 0; b < 16; ++b)
+      if (b < left) v[b >> 2] |= (uint32_t)q[b] << (8 * (b & 3));
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = min(max(valid - 4 * j, 0), 4);
+    const uint32_t keep = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+    v[j] = (v[j] & keep) | (0x7F7F7F7Fu & ~keep);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Logical tile L -> group, first row, rows, first column: bands of 8 M-tiles, M fastest inside.
+template <int BM, int BN>
+__device__ __forceinline__ bool tile_of(const MxGemmParams& p, int L, int& g, int& row0, int& rows,
+                                        int& n0) {
+  const int nN = cdiv(p.N, BN);
+  int local, mt_g;
+  if (p.mt_start) {
+    if (L >= p.mt_start[p.G] * nN) return false;
+    const int key = L / nN;
+    int lo = 0, hi = p.G - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.mt_start[mid] <= key) lo = mid; else hi = mid - 1;
+    }
+    g = lo;
+    mt_g = p.mt_start[g + 1] - p.mt_start[g];
+    local = L - p.mt_start[g] * nN;
+  } else {
+    g = 0;
+    mt_g = cdiv(p.M, BM);
+    local = L;
+    if (L >= mt_g * nN) return false;
+  }
+  constexpr int GB = 8;
+  const int first = (local / (GB * nN)) * GB;
+  const int gm = min(GB, mt_g - first);
+  const int within = local - first * nN;
+  n0 = (within / gm) * BN;
+  const int mt = first + within % gm;
+  row0 = (p.mt_start ? p.offs[g] : 0) + mt * BM;
+  rows = min(BM, (p.mt_start ? p.offs[g + 1] : p.M) - row0);
+  return rows > 0;
+}
+
+template <int BM, int BN, int WGM, int WGN, int NS, int FA, int FW>
+__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(2)))
+void mx_tile_kernel(MxGemmParams p) {
+  constexpr int NW = WGM * WGN, NT = 64 * NW;
+  constexpr int SA = kBits<FA> * 16, SW = kBits<FW> * 16;   // bytes of a row's K-step
+  constexpr int WM = BM / WGM, WN = BN / WGN, MB = WM / 32, NB = WN / 32;
+  constexpr int RA = 1024 / SA, RW = 1024 / SW;             // rows per 1-KB load
+  constexpr int LA = SA / 16, LW = SW / 16;                 // lanes per row
+  constexpr int GA = BM / (RA * NW), GW = BN / (RW * NW);   // 1-KB loads per wave
+  constexpr int STAGE = BM * SA + BN * SW;
+  constexpr int SROWS = (FA == kE4Row ? 0 : BM) + BN;       // rows whose scales are staged
+  constexpr int SR = (SROWS + NT - 1) / NT;
+  constexpr int EPW = WN + 4;
+  static_assert(GA >= 1 && GW >= 1 && BM % (RA * NW) == 0 && BN % (RW * NW) == 0, "1-KB loads");
+  static_assert(WM % 32 == 0 && WN % 32 == 0 && NW % 2 == 0 && NS >= 2, "tile shape");
+  static_assert(NW * 16 * EPW * 4 <= NS * STAGE, "epilogue strips fit in the stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE];
+  __shared__ __attribute__((aligned(16))) uint4 sc[2][SROWS];
+
+  int g, row0, rows, n0;
+  if (!tile_of<BM, BN>(p, xcd_logical_block(blockIdx.x, gridDim.x), g, row0, rows, n0)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WGN, wn = wave % WGN, lg = lane >> 5, lr = lane & 31;
+  const int kba = p.K * kBits<FA> / 8, kbw = p.K * kBits<FW> / 8;   // bytes of a row
+  const int nb = p.K / kMxBlockElts, nk = cdiv(p.K, 128);
+  const int tail_a = kba % SA, tail_w = kbw % SW;   // bytes of a partial last K-step
+
+  const uint8_t* Wg = p.W + (int64_t)g * p.N * kbw;
+  const __amdgpu_buffer_rsrc_t ra = rsrc(p.A, (int64_t)p.a_rows * kba);
+  const __amdgpu_buffer_rsrc_t rw = rsrc(Wg, (int64_t)p.N * kbw);
+  const int ca = ((lane % LA) ^ swz<SA>(wave * RA + lane / LA)) << 4;
+  const int cw = ((lane % LW) ^ swz<SW>(wave * RW + lane / LW)) << 4;
+  constexpr uint32_t kOut = 0xFFFFFFF0u;   // an offset past every buffer: the load is skipped
+  uint32_t oa[GA], ow[GW];
+#pragma unroll
+  for (int i = 0; i < GA; ++i) {
+    const int r = (wave + NW * i) * RA + lane / LA;
+    const int src = r < rows ? (p.a_gather ? p.a_gather[row0 + r] : row0 + r) : 0;
+    oa[i] = r < rows ? (uint32_t)src * (uint32_t)kba + ca : kOut;
+  }
+#pragma unroll
+  for (int i = 0; i < GW; ++i)
+    ow[i] = (uint32_t)min(n0 + (wave + NW * i) * RW + lane / LW, p.N - 1) * (uint32_t)kbw + cw;
+
+  auto issue = [&](int ks, uint8_t* st) {
+    const bool last = ks == nk - 1;
+    const bool la = !(last && tail_a) || ca < tail_a, lw = !(last && tail_w) || cw < tail_w;
+#pragma unroll
+    for (int i = 0; i < GA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          ra, (__attribute__((address_space(3))) void*)(st + (wave + NW * i) * 1024), 16,
+          (int)(la ? oa[i] : kOut), ks * SA, 0, 0);
+#pragma unroll
+    for (int i = 0; i < GW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rw, (__attribute__((address_space(3))) void*)(st + BM * SA + (wave + NW * i) * 1024), 16,
+          (int)(lw ? ow[i] : kOut), ks * SW, 0, 0);
+  };
+  auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  // the chunks of a partial last K-step that lie past K, zeroed once the stage has landed
+  auto fix_tail = [&](uint8_t* st) {
+    if (tail_a && ca >= tail_a)
+#pragma unroll
+      for (int i = 0; i < GA; ++i) *(uint4*)(st + (wave + NW * i) * 1024 + lane * 16) = kZero4;
+    if (tail_w && cw >= tail_w)
+#pragma unroll
+      for (int i = 0; i < GW; ++i)
+        *(uint4*)(st + BM * SA + (wave + NW * i) * 1024 + lane * 16) = kZero4;
+    barrier();
+  };
+
+  // scales: thread t carries rows t, t + NT, ... of (A rows, W rows)
+  const uint8_t* sp[SR];
+  int64_t sleft[SR];
+#pragma unroll
+  for (int i = 0; i < SR; ++i) {
+    const int r = tid + NT * i;
+    sp[i] = nullptr;
+    sleft[i] = 0;
+    if (FA != kE4Row && r < BM) {
+      const int rr = min(r, rows - 1);
+      const int64_t src = p.a_gather ? p.a_gather[row0 + rr] : row0 + rr;
+      sp[i] = p.a_mx + src * nb;
+      sleft[i] = ((int64_t)p.a_rows - src) * nb;
+    } else if (r < SROWS) {
+      const int64_t n = min(n0 + r - (SROWS - BN), p.N - 1);
+      sp[i] = p.w_mx + ((int64_t)g * p.N + n) * nb;
+      sleft[i] = ((int64_t)(p.mt_start ? p.G - g : 1) * p.N - n) * nb;
+    }
+  }
+  uint4 sv[SR];
+  auto fetch_scales = [&](int ss) {
+#pragma unroll
+    for (int i = 0; i < SR; ++i)
+      if (tid + NT * i < SROWS) sv[i] = load_scales(sp[i] + 16 * ss, sleft[i] - 16 * ss, nb - 16 * ss);
+  };
+  auto put_scales = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < SR; ++i)
+      if (tid + NT * i < SROWS) sc[buf][tid + NT * i] = sv[i];
+  };
+
+  f32x16_t acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  auto read_frag = [&](const uint8_t* base, int row, int s, auto bits) {
+    constexpr int B = decltype(bits)::value, SL = B * 16;
+    if constexpr (B == 8)
+      return frag(*(const uint4*)(base + slot<SL>(row, 4 * s + lg)),
+                  *(const uint4*)(base + slot<SL>(row, 4 * s + 2 + lg)));
+    else
+      return frag(*(const uint4*)(base + slot<SL>(row, 2 * s + lg)), kZero4);
+  };
+  auto compute = [&](const uint8_t* st, int buf, int q) {
+    int xa[MB], xw[NB];   // this lane's scale bytes at bits 0 and 16 (k-sub 0 and 1)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+      xa[i] = FA == kE4Row ? 0x7F7F7F7F
+                           : (int)(((const uint32_t*)&sc[buf][wm * WM + i * 32 + lr])[q] >> (8 * lg));
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      xw[j] = (int)(((const uint32_t*)&sc[buf][SROWS - BN + wn * WN + j * 32 + lr])[q] >> (8 * lg));
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      i32x8_t a[MB], b[NB];
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        a[i] = read_frag(st, wm * WM + i * 32 + lr, s, std::integral_constant<int, kBits<FA>>());
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        b[j] = read_frag(st + BM * SA, wn * WN + j * 32 + lr, s,
+                         std::integral_constant<int, kBits<FW>>());
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          acc[i][j] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                   a[i], b[j], acc[i][j], kCode<FA>, kCode<FW>, 0, xa[i], 0, xw[j])
+                             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                   a[i], b[j], acc[i][j], kCode<FA>, kCode<FW>, 2, xa[i], 2, xw[j]);
+    }
+  };
+
+  // K-step ks + NS - 1 is in flight while K-step ks is multiplied; before ks a wave waits until
+  // at most the loads of the stages after ks are outstanding, then the barrier publishes the
+  // stage (and the scales of the super-step) and frees the stage before.
+  constexpr int PER = GA + GW;
+  static_assert((NS - 2) * PER < 64, "vmcnt range");
+  auto wait_ahead = [&](int ahead) {
+#define MOE_VMCNT(n) __builtin_amdgcn_s_waitcnt((((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8)))
+    if constexpr (NS >= 4) { if (ahead >= 2) { MOE_VMCNT(2 * PER); return; } }
+    if constexpr (NS >= 3) { if (ahead >= 1) { MOE_VMCNT(PER); return; } }
+    MOE_VMCNT(0);
+#undef MOE_VMCNT
+  };
+  fetch_scales(0);
+#pragma unroll
+  for (int q = 0; q < NS - 1; ++q)
+    if (q < nk) issue(q, smem + q * STAGE);
+  put_scales(0);
+  const int nss = cdiv(nk, 4);
+  for (int ss = 0; ss < nss; ++ss) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int ks = 4 * ss + q;
+      if (ks >= nk) break;
+      wait_ahead(min(NS - 2, nk - 1 - ks));
+      barrier();
+      uint8_t* cur = smem + (ks % NS) * STAGE;
+      if (ks == nk - 1 && (tail_a || tail_w)) fix_tail(cur);
+      if (ks + NS - 1 < nk) issue(ks + NS - 1, smem + ((ks + NS - 1) % NS) * STAGE);
+      if (q == 0 && ss + 1 < nss) fetch_scales(ss + 1);
+      compute(cur, ss & 1, q);
+    }
+    // the other buffer was last read a whole super-step ago
+    if (ss + 1 < nss) put_scales((ss + 1) & 1);
+  }
+  barrier();   // every wave is done with the stages: the epilogue reuses them
+
+  // acc[i][j][r] is C[wm*WM + i*32 + (r/4)*8 + lg*4 + r%4][wn*WN + j*32 + lr]; strips of 16 rows
+  // go through this wave's own LDS so that a lane stores 8 consecutive columns
+  float* ep = (float*)smem + wave * 16 * EPW;
+  constexpr int CG = WN / 8, ITEMS = 16 * CG / 64;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int rr = 0; rr < 8; ++rr)
+          ep[((rr >> 2) * 8 + lg * 4 + (rr & 3)) * EPW + j * 32 + lr] = acc[i][j][8 * h + rr];
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        const int item = it * 64 + lane, srow = item / CG, cg = item % CG;
+        const int rl = wm * WM + i * 32 + h * 16 + srow, col = n0 + wn * WN + cg * 8;
+        const float4 lo = *(const float4*)(ep + srow * EPW + cg * 8);
+        const float4 hi = *(const float4*)(ep + srow * EPW + cg * 8 + 4);
+        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (rl < rows && col < p.N) {
+          const int row = row0 + rl;
+          if constexpr (FA == kE4Row) {
+            const float rs = p.a_row[p.a_gather ? p.a_gather[row] : row];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] *= rs;
+          }
+          if (p.sqrelu)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = sqrelu(v[q]);
+          store8(p, row, col, v);
+        }
+      }
+    }
+}
+
+template <int BM, int BN, int WGM, int WGN, int NS, int FA, int FW>
+hipError_t run_tile(const MxGemmParams& p, int mtiles, hipStream_t s) {
+  const int64_t tiles = (int64_t)mtiles * cdiv(p.N, BN);
+  if (tiles <= 0) return hipSuccess;
+  if (tiles > INT32_MAX / 512) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((mx_tile_kernel<BM, BN, WGM, WGN, NS, FA, FW>),
+                     dim3(cdiv((int)tiles, kXcds) * kXcds), dim3(64 * WGM * WGN), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int FA, int FW>
+hipError_t run_dense(const MxGemmParams& p, hipStream_t s) {
+  if (p.M <= 16) {
+    hipLaunchKernelGGL((mx_rows_kernel<FA, FW, 1, 8>), dim3(p.N / 16), dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
+  if (p.M <= 128) {
+    const int tb = p.M <= 32 ? 2 : 4;
+    const dim3 grid(p.N / 16, cdiv(p.M, 16 * tb));
+    if (tb == 2) hipLaunchKernelGGL((mx_rows_kernel<FA, FW, 2, 8>), grid, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL((mx_rows_kernel<FA, FW, 4, 8>), grid, dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
+  return run_tile<128, 192, 2, 2, 2, FA, FW>(p, cdiv(p.M, 128), s);
+}
+
+}  // namespace
+
+hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, hipStream_t s) {
+  if (p.K < 32 || p.K % 32 || p.N < 16 || p.N % 16 || !p.w_mx) return hipErrorInvalidValue;
+  // 32-bit operand offsets
+  constexpr int64_t kLim = ((int64_t)1 << 31) - 1;
+  const int ab = a == Elt::MXFP4 ? 4 : 8, wb = w == Elt::MXFP4 ? 4 : 8;
+  if ((int64_t)p.a_rows * p.K * ab / 8 > kLim || (int64_t)p.N * p.K * wb / 8 > kLim)
+    return hipErrorInvalidValue;
+  if (w != Elt::MXFP4 && w != Elt::MXFP8) return hipErrorInvalidValue;
+  const bool w4 = w == Elt::MXFP4;
+  if (p.mt_start) {  // grouped: e4m3 rows with a row scale against block-scaled experts
+    if (a != Elt::FP8 || !p.a_row || !p.offs) return hipErrorInvalidValue;
+    return w4 ? run_tile<kGroupBM, 192, 2, 2, 2, kE4Row, kE2>(p, max_mtiles, s)
+              : run_tile<kGroupBM, 192, 2, 2, 2, kE4Row, kE4>(p, max_mtiles, s);
+  }
+  if (p.M <= 0) return hipSuccess;
+  if (!p.a_mx || p.a_gather || p.a_rows != p.M) return hipErrorInvalidValue;
+  if (a == Elt::MXFP4) return w4 ? run_dense<kE2, kE2>(p, s) : run_dense<kE2, kE4>(p, s);
+  if (a == Elt::MXFP8) return w4 ? run_dense<kE4, kE2>(p, s) : run_dense<kE4, kE4>(p, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe

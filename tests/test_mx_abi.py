@@ -1,0 +1,92 @@
+"""CPU checks of the block-scaled (MX) entry points: argument errors are reported before anything
+is launched, and the binding refuses tensors that do not describe a block-scaled matrix."""
+import ctypes as C
+
+import pytest
+import torch
+
+import sparse_moe_layer_05_amd as moe
+from sparse_moe_layer_05_amd import binding as B
+
+FAKE = C.c_void_p(0x10000)    # aligned, never dereferenced: validation fails or returns first
+ODD = C.c_void_p(0x10004)
+BAD, UNS, OK = B.MOE_ERR_INVALID_ARG, B.MOE_ERR_UNSUPPORTED, B.MOE_OK
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), OK), (dict(rows=-1), BAD), (dict(cols=0), BAD), (dict(cols=16), BAD),
+    (dict(cols=48), BAD), (dict(cols=-32), BAD), (dict(rows=(1 << 36) // 64 + 1, cols=64), BAD),
+    (dict(rows=1 << 62, cols=64), BAD), (dict(dt=B.MOE_FP8_E4M3), UNS), (dict(dt=9), UNS),
+    (dict(fmt=B.MOE_BF16), UNS), (dict(fmt=B.MOE_FP8_E4M3), UNS), (dict(x=None), BAD),
+    (dict(codes=None), BAD), (dict(scales=None), BAD), (dict(x=ODD), BAD), (dict(codes=ODD), BAD),
+])
+def test_quantise_and_dequantise_argument_errors(kw, code):
+    a = dict(x=FAKE, dt=B.MOE_BF16, rows=4, cols=64, fmt=B.MOE_MXFP4, codes=FAKE, scales=ODD)
+    a.update(kw)
+    L = moe.lib()
+    if a["rows"] == 0 or code != OK:
+        assert L.moe_mx_quantize(a["x"], a["dt"], a["rows"], a["cols"], a["fmt"], a["codes"],
+                                 a["scales"], None) == code
+        assert L.moe_mx_dequantize(a["codes"], a["scales"], a["fmt"], a["rows"], a["cols"], a["x"],
+                                   a["dt"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=0), OK), (dict(M=-1), BAD), (dict(N=0), BAD), (dict(N=24), BAD), (dict(K=16), BAD),
+    (dict(K=0), BAD), (dict(K=80), BAD), (dict(fa=B.MOE_FP8_E4M3), UNS), (dict(fw=B.MOE_BF16), UNS),
+    (dict(dt=B.MOE_FP8_E4M3), UNS), (dict(A=None), BAD), (dict(sa=None), BAD), (dict(W=None), BAD),
+    (dict(sw=None), BAD), (dict(Cm=None), BAD), (dict(A=ODD), BAD), (dict(W=ODD), BAD),
+    (dict(Cm=ODD), BAD),
+    # fp32 results of an 8-bit operand
+    (dict(fa=B.MOE_MXFP8, dt=B.MOE_F32), UNS), (dict(fw=B.MOE_MXFP8, dt=B.MOE_F32), UNS),
+    (dict(dt=B.MOE_F32, M=0), OK),
+    # an operand of 2 GiB or more: 32-bit offsets
+    (dict(M=1 << 20, K=2048, fa=B.MOE_MXFP8), BAD), (dict(N=1 << 20, K=4096), BAD),
+])
+def test_product_argument_errors(kw, code):
+    a = dict(A=FAKE, sa=ODD, fa=B.MOE_MXFP4, W=FAKE, sw=ODD, fw=B.MOE_MXFP4, M=4, N=32, K=64,
+             Cm=FAKE, dt=B.MOE_BF16)
+    a.update(kw)
+    assert moe.lib().moe_mx_gemm(a["A"], a["sa"], a["fa"], a["W"], a["sw"], a["fw"], a["M"], a["N"],
+                                 a["K"], a["Cm"], a["dt"], None) == code
+
+
+def ws(**kw):
+    d = B.MoeDesc()
+    base = dict(T=64, H=256, E=16, k=2, I=128, I_shared=0, latent=0, act_dtype=1,
+                expert_dtype=B.MOE_MXFP4, flags=B.MX_GROUPED)
+    base.update(kw)
+    for n, v in base.items():
+        setattr(d, n, v)
+    n = C.c_size_t(0)
+    return moe.lib().moe_workspace_size(C.byref(d), C.byref(n))
+
+
+def test_grouped_block_scaled_descriptors():
+    assert ws() == OK and ws(expert_dtype=B.MOE_MXFP8) == OK and ws(latent=64) == OK
+    assert ws(flags=B.MX_GROUPED | B.ROUTING_GIVEN) == OK
+    assert ws(expert_dtype=B.MOE_BF16) == UNS and ws(expert_dtype=B.MOE_FP8_E4M3) == UNS
+    assert ws(flags=B.MX_GROUPED | B.PATH_STREAM) == BAD
+    assert ws(flags=B.MX_GROUPED | B.PATH_GROUPED) == BAD
+    assert ws(I=144) == BAD and ws(act_dtype=0) == UNS
+
+
+def test_binding_refuses_what_is_not_block_scaled():
+    u8 = torch.uint8
+    z = lambda *s: torch.zeros(*s, dtype=u8)  # noqa: E731
+    for call in (
+            lambda: moe.mx_quantize(torch.zeros(4, 48)),                       # no whole blocks
+            lambda: moe.mx_quantize(torch.zeros(4, 0)),
+            lambda: moe.mx_quantize(torch.zeros(4, 64), "mxfp6"),
+            lambda: moe.mx_quantize(torch.zeros(4, 64, dtype=torch.float16)),
+            lambda: moe.mx_quantize(torch.zeros(4, 64)),                       # not on a GPU
+            lambda: moe.mx_dequantize(z(4, 33), z(4, 1)),                      # 33 bytes a block
+            lambda: moe.mx_dequantize(z(4, 32), z(3, 1)),
+            lambda: moe.mx_dequantize(z(4, 32), z(4, 1)),                      # not on a GPU
+            lambda: moe.mx_dequantize(torch.zeros(4, 32), z(4, 1)),
+            lambda: moe.mx_dequantize(z(4, 32), z(4, 1), dtype=torch.float16),
+            lambda: moe.mx_gemm(z(4, 32), z(4, 1), z(16, 64), z(16, 2)),       # K differs
+            lambda: moe.mx_gemm(z(2, 4, 32), z(2, 4, 1), z(16, 32), z(16, 1)),
+            lambda: moe.mx_gemm(z(4, 32), z(4, 1), z(16, 32), z(16, 1))):      # not on a GPU
+        with pytest.raises(ValueError):
+            call()
