@@ -330,9 +330,8 @@ def _own_layer(s):
     if "call" not in s:
         c = s["case"]
         given = c["op"] == "experts"
-        s["rt"] = moe.alloc_routing(c["T"], c["E"], c["k"], DEV)
-        if given:
-            s["rt"]["idx"], s["rt"]["gates"] = s["idx"], s["gates"]
+        rt = moe.alloc_routing(c["T"], c["E"], c["k"], DEV)
+        s["rt"] = {n: s[n] if given else rt[n] for n in ("idx", "gates")}
         s["call"] = moe.layer_from(s, c["k"], path="grouped_mx" if given else "few",
                                    routing=s["rt"], routing_given=given, expert_dtype=c["w"])
     y = s["call"]()
