@@ -179,6 +179,27 @@ int32_t latent_moe_forward(const moe_desc_t *desc, const moe_weights_t *w, void 
 int32_t moe_layer_forward_static(const moe_desc_t *desc, const moe_weights_t *w, void *y,
                                  moe_routing_t *routing, void *stream);
 
+/* The whole layer for at most MOE_FEW_TOKENS tokens (moe_layer_forward, or latent_moe_forward when
+ * desc->latent > 0) in three launches (four for LatentMoE), where the decode path takes six to
+ * nine: for single sequences and small decode batches, whose time is launches and not bytes.
+ * Arguments, formats, roundings and errors as moe_layer_forward, with these differences:
+ *   - T <= MOE_FEW_TOKENS and act_dtype MOE_BF16, and T * D <= 65536 for 8- and 4-bit experts
+ *     (D = H, or latent), else MOE_ERR_UNSUPPORTED; flags: MOE_PATH_AUTO with or without
+ *     MOE_ROUTING_GIVEN, else MOE_ERR_INVALID_ARG.
+ *   - Workspace: moe_few_workspace_size bytes; its contents need no preparation and are not kept
+ *     between calls.
+ *   - The router's logits are summed in fp64 and rounded to fp32, and sums run in another order
+ *     than on the other paths: y differs from theirs by roundings, and a near-tie of two keys can
+ *     fall the other way.
+ *   - counts, offsets, perm and pos of the routing record cost one more launch when any of them
+ *     is asked for.
+ * Given routing: pairs with an expert outside [0, E) and repeated experts of a token (after its
+ * first) are dropped, as in moe_dispatch; a token with none left gets the shared expert alone. */
+#define MOE_FEW_TOKENS 16
+int32_t moe_few_workspace_size(const moe_desc_t *desc, size_t *bytes);
+int32_t moe_few_forward(const moe_desc_t *desc, const moe_weights_t *w, void *y, void *ws,
+                        size_t ws_bytes, moe_routing_t *routing, void *stream);
+
 /* Router alone (steps logits -> scores -> top-k -> gates). If `logits` is non-NULL it is used as
  * the fp32 router logits [T, E] and x / W_r are ignored; otherwise logits are computed from
  * x [T, H] and W_r [E, H] (dtype `dt`) into `logits_out` [T, E], which is then required.

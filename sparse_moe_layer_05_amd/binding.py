@@ -20,16 +20,19 @@ _EXPERT_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "e4m3": MOE_FP8_E4M3, "mxfp4
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
 PATH_AUTO, PATH_GROUPED, PATH_STREAM, ROUTING_GIVEN, SAVED_IN_WORKSPACE = 0, 1, 2, 4, 8
 WGRAD_BF16, MX_GROUPED = 16, 32
-# "grouped_mx": matrix-core tiles for MXFP4 / MXFP8 experts (many tokens)
+# "grouped_mx": matrix-core tiles for MXFP4 / MXFP8 experts (many tokens); "few": the few-token
+# layer (an entry point of its own)
 _PATHS = {"auto": PATH_AUTO, "grouped": PATH_GROUPED, "stream": PATH_STREAM,
-          "grouped_mx": MX_GROUPED}
+          "grouped_mx": MX_GROUPED, "few": PATH_AUTO}
+FEW_TOKENS = 16
 _MX_FORMATS = {"mxfp4": MOE_MXFP4, "mxfp8": MOE_MXFP8}
 MX_BLOCK = 32
 
 EXPORTS = ("moe_workspace_size", "moe_layer_forward", "latent_moe_forward", "moe_route",
            "moe_dispatch_workspace_size", "moe_dispatch", "moe_bias_update",
            "moe_backward_workspace_size", "moe_layer_forward_train", "moe_layer_backward",
-           "moe_layer_forward_static", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
+           "moe_layer_forward_static", "moe_few_workspace_size", "moe_few_forward",
+           "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
            "moe_status_str",
            "moe_trace_enable",
            "moe_trace_count", "moe_trace_read", "moe_trace_reset")
@@ -77,7 +80,8 @@ def lib() -> C.CDLL:
             L = C.CDLL(LIB_PATH)
             vp, i32, sz = C.c_void_p, C.c_int32, C.c_size_t
             L.moe_workspace_size.argtypes = [C.POINTER(MoeDesc), C.POINTER(sz)]
-            for fn in (L.moe_layer_forward, L.latent_moe_forward):
+            L.moe_few_workspace_size.argtypes = [C.POINTER(MoeDesc), C.POINTER(sz)]
+            for fn in (L.moe_layer_forward, L.latent_moe_forward, L.moe_few_forward):
                 fn.argtypes = [C.POINTER(MoeDesc), C.POINTER(MoeWeights), vp, vp, sz,
                                C.POINTER(MoeRouting), vp]
             L.moe_layer_forward_static.argtypes = [C.POINTER(MoeDesc), C.POINTER(MoeWeights),
@@ -222,9 +226,10 @@ def make_desc(x, W_r, W_up, k, Ws_up=None, W_in=None, path="auto", routing_given
     return d
 
 
-def workspace_size(desc: MoeDesc) -> int:
+def workspace_size(desc: MoeDesc, few: bool = False) -> int:
     n = C.c_size_t(0)
-    _check(lib().moe_workspace_size(C.byref(desc), C.byref(n)), "moe_workspace_size")
+    name = "moe_few_workspace_size" if few else "moe_workspace_size"
+    _check(getattr(lib(), name)(C.byref(desc), C.byref(n)), name)
     return n.value
 
 
@@ -258,10 +263,13 @@ class Layer:
         self._keep = [x, W_r, b, W_up, W_down, s_up, s_down, Ws_up, Ws_down, W_in, W_out]
         self.y = out if out is not None else torch.empty_like(x)
         self.no_alloc = no_alloc
+        few = path == "few"      # moe_few_forward: at most FEW_TOKENS tokens, few launches
+        if few and no_alloc:
+            raise ValueError("path 'few' takes its own workspace: no_alloc is not offered")
         if no_alloc:          # moe_layer_forward_static: the library's own per-GPU scratch
             self.ws_bytes, self.ws = 0, None
         else:
-            self.ws_bytes = workspace_size(self.desc)
+            self.ws_bytes = workspace_size(self.desc, few)
             self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=x.device)
         self.routing = routing
         self.r = None
@@ -270,7 +278,9 @@ class Layer:
             for name, _ in MoeRouting._fields_:
                 setattr(r, name, _p(routing.get(name)))
             self.r = r
-        self.fn = lib().latent_moe_forward if self.desc.latent else lib().moe_layer_forward
+        self.fn_name = "moe_few_forward" if few else \
+            "latent_moe_forward" if self.desc.latent else "moe_layer_forward"
+        self.fn = getattr(lib(), self.fn_name)
 
     def __call__(self, stream=None):
         r = C.byref(self.r) if self.r is not None else None
@@ -281,7 +291,7 @@ class Layer:
             return self.y
         rc = self.fn(C.byref(self.desc), C.byref(self.w), _p(self.y), _p(self.ws), self.ws_bytes,
                      r, _stream(stream))
-        _check(rc, "latent_moe_forward" if self.desc.latent else "moe_layer_forward")
+        _check(rc, self.fn_name)
         return self.y
 
 

@@ -9,6 +9,7 @@
 
 #include "moe.h"
 #include "backward.hpp"
+#include "few.hpp"
 #include "gemm_kt.hpp"
 #include "kernels.hpp"
 #include "mx.hpp"
@@ -276,14 +277,9 @@ hipError_t stream_dense(const void* A, int64_t lda, const void* W, int N, int K,
   return launch_stream(p, s);
 }
 
-int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, size_t ws_bytes,
-                moe_routing_t* r, void* stream, bool latent_call) {
-  Plan pl;
-  int32_t rc = make_plan(d, latent_call, &pl);
-  if (rc) return rc;
-  if (pl.T == 0) return MOE_OK;  // empty batch: nothing to read or write
+int32_t check_forward_args(const Plan& pl, const moe_weights_t* w, const void* y, bool given,
+                           const moe_routing_t* r) {
   if (!w || !y) return MOE_ERR_INVALID_ARG;
-  const bool given = d->flags & MOE_ROUTING_GIVEN;
   // 8-bit or 4-bit expert weights: e4m3 with per-channel scales, or MXFP4 / MXFP8 blocks
   const bool narrow = pl.ex == Elt::FP8 || pl.ex == Elt::MXFP4 || pl.ex == Elt::MXFP8;
   if (!w->x || !w->b || !w->W_up || !w->W_down || (!given && !w->W_r)) return MOE_ERR_INVALID_ARG;
@@ -295,6 +291,19 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
                         w->W_out, y};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, size_t ws_bytes,
+                moe_routing_t* r, void* stream, bool latent_call) {
+  Plan pl;
+  int32_t rc = make_plan(d, latent_call, &pl);
+  if (rc) return rc;
+  if (pl.T == 0) return MOE_OK;  // empty batch: nothing to read or write
+  const bool given = d->flags & MOE_ROUTING_GIVEN;
+  if ((rc = check_forward_args(pl, w, y, given, r))) return rc;
+  // 8-bit or 4-bit expert weights: e4m3 with per-channel scales, or MXFP4 / MXFP8 blocks
+  const bool narrow = pl.ex == Elt::FP8 || pl.ex == Elt::MXFP4 || pl.ex == Elt::MXFP8;
   if (!ws || ws_bytes < pl.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
 
   hipStream_t s = (hipStream_t)stream;
@@ -618,6 +627,128 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
       MOE_SPAN(act == Elt::F32 ? "gemm_f32_store:latent_out" : "gemm_bf16_store:latent_out");
       MOE_TRY(dense(act, act, Epi::Store, z, L, w->W_out, L, y, H, T, H, L, s));
     }
+  }
+  return hip_status(hipGetLastError());
+}
+
+// ---------------------------------------------------------------- few tokens
+
+struct FewPlan {
+  Plan p;  // dimensions and types as make_plan checks them
+  size_t logits = 0, score = 0, idx = 0, gates = 0, counts = 0, offsets = 0, perm = 0, pos = 0;
+  size_t dscratch = 0, n_slots = 0, slot_e = 0, gate_m = 0, slot_mask = 0, hmax = 0;
+  size_t h = 0, hs = 0, u = 0, z = 0, total = 0;
+};
+
+int32_t make_few_plan(const moe_desc_t* d, FewPlan* out) {
+  if (!d) return MOE_ERR_INVALID_ARG;
+  FewPlan f;
+  int32_t rc = make_plan(d, d->latent > 0, &f.p);
+  if (rc) return rc;
+  const Plan& p = f.p;
+  if (d->flags & ~MOE_ROUTING_GIVEN) return MOE_ERR_INVALID_ARG;
+  if (p.act != Elt::BF16 || p.T > kFewTokens) return MOE_ERR_UNSUPPORTED;
+  const bool narrow = p.ex != Elt::BF16;
+  if (narrow && (int64_t)p.T * p.D > kFewNarrowElts) return MOE_ERR_UNSUPPORTED;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + kAlign - 1) / kAlign * kAlign;
+    return at;
+  };
+  const size_t T = p.T, E = p.E, P = p.P, S = few_slots(p.T, p.E, p.k);
+  f.logits = take(T * E * 4);
+  f.score = take(T * E * 4);
+  f.idx = take(P * 4);
+  f.gates = take(P * 4);
+  f.counts = take(E * 4);
+  f.offsets = take((E + 1) * 4);
+  f.perm = take(P * 4);
+  f.pos = take(P * 4);
+  f.dscratch = take(dispatch_scratch_ints(p.T, p.E, p.k) * 4);
+  f.n_slots = take(4);
+  f.slot_e = take(S * 4);
+  f.gate_m = take(S * kFewTokens * 4);
+  f.slot_mask = take(S * 4);
+  if (narrow) f.hmax = take(S * kFewTokens * 4);
+  f.h = take(S * T * (size_t)p.I * 2);
+  if (p.Is) f.hs = take(T * (size_t)p.Is * 2);
+  if (p.L) {
+    f.u = take(T * (size_t)p.L * 2);
+    f.z = take(T * (size_t)p.L * 2);
+  }
+  f.total = off;
+  *out = f;
+  return MOE_OK;
+}
+
+int32_t few_forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws,
+                    size_t ws_bytes, moe_routing_t* r, hipStream_t s) {
+  FewPlan f;
+  int32_t rc = make_few_plan(d, &f);
+  if (rc) return rc;
+  const Plan& pl = f.p;
+  if (pl.T == 0) return MOE_OK;
+  const bool given = d->flags & MOE_ROUTING_GIVEN;
+  if ((rc = check_forward_args(pl, w, y, given, r))) return rc;
+  if (!ws || ws_bytes < f.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  uint8_t* base = (uint8_t*)ws;
+  auto pick = [&](auto* user, size_t off) {
+    using Ptr = decltype(user);
+    return user ? user : (Ptr)(base + off);
+  };
+  FewParams p;
+  p.T = pl.T; p.H = pl.H; p.E = pl.E; p.k = pl.k; p.I = pl.I; p.Is = pl.Is; p.L = pl.L; p.D = pl.D;
+  p.ex = pl.ex;
+  p.given = given;
+  p.x = (const uint16_t*)w->x; p.W_r = (const uint16_t*)w->W_r; p.b = w->b;
+  p.W_up = (const uint8_t*)w->W_up; p.W_down = (const uint8_t*)w->W_down;
+  p.s_up = w->s_up; p.s_down = w->s_down;
+  p.Ws_up = (const uint16_t*)w->Ws_up; p.Ws_down = (const uint16_t*)w->Ws_down;
+  p.W_in = (const uint16_t*)w->W_in; p.W_out = (const uint16_t*)w->W_out;
+  p.y = (uint16_t*)y;
+  int32_t* idx = pick(r ? r->idx : (int32_t*)nullptr, f.idx);
+  float* gates = pick(r ? r->gates : (float*)nullptr, f.gates);
+  if (given) {
+    p.idx_in = idx;
+    p.gates_in = gates;
+  }
+  p.idx = idx;
+  p.gates = gates;
+  p.logits = pick(r ? r->logits : (float*)nullptr, f.logits);
+  p.score = (float*)(base + f.score);
+  p.n_slots = (int32_t*)(base + f.n_slots);
+  p.slot_e = (int32_t*)(base + f.slot_e);
+  p.gate_m = (float*)(base + f.gate_m);
+  p.slot_mask = (uint32_t*)(base + f.slot_mask);
+  p.hmax = pl.ex != Elt::BF16 ? (uint32_t*)(base + f.hmax) : nullptr;
+  p.h = (uint16_t*)(base + f.h);
+  p.hs = pl.Is ? (uint16_t*)(base + f.hs) : nullptr;
+  p.u = pl.L ? (uint16_t*)(base + f.u) : nullptr;
+  p.z = pl.L ? (uint16_t*)(base + f.z) : nullptr;
+  {
+    MOE_SPAN("few:front");
+    MOE_TRY(launch_few_front(p, s));
+  }
+  {
+    MOE_SPAN("few:up");
+    MOE_TRY(launch_few_up(p, s));
+  }
+  {
+    MOE_SPAN("few:down");
+    MOE_TRY(launch_few_down(p, s));
+  }
+  if (pl.L) {
+    MOE_SPAN("few:out");
+    MOE_TRY(launch_few_out(p, s));
+  }
+  // the dispatch products are not used here: made when the caller's record asks for them
+  if (r && (r->counts || r->offsets || r->perm || r->pos)) {
+    MOE_SPAN("dispatch:all");
+    MOE_TRY(launch_dispatch(idx, pl.T, pl.E, pl.k, pick(r->counts, f.counts),
+                            pick(r->offsets, f.offsets), pick(r->perm, f.perm),
+                            pick(r->pos, f.pos), (int32_t*)(base + f.dscratch), 0, nullptr,
+                            DispatchExtras(), s));
   }
   return hip_status(hipGetLastError());
 }
@@ -1068,6 +1199,20 @@ int32_t moe_layer_forward_static(const moe_desc_t* desc, const moe_weights_t* w,
   if (static_scratch(&ws, &bytes) != hipSuccess || side_of(&side) != hipSuccess)
     return MOE_ERR_HIP;
   return forward(desc, w, y, ws, bytes, routing, stream, latent);
+}
+
+int32_t moe_few_workspace_size(const moe_desc_t* desc, size_t* bytes) {
+  if (!desc || !bytes) return MOE_ERR_INVALID_ARG;
+  FewPlan f;
+  const int32_t rc = make_few_plan(desc, &f);
+  if (rc) return rc;
+  *bytes = f.total;
+  return MOE_OK;
+}
+
+int32_t moe_few_forward(const moe_desc_t* desc, const moe_weights_t* w, void* y, void* ws,
+                        size_t ws_bytes, moe_routing_t* routing, void* stream) {
+  return few_forward(desc, w, y, ws, ws_bytes, routing, (hipStream_t)stream);
 }
 
 int32_t moe_route(const float* logits, const void* x, const void* W_r, const float* b, int32_t T,
