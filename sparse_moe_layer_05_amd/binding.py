@@ -289,9 +289,8 @@ class Layer:
                                                 r, _stream(stream))
             _check(rc, "moe_layer_forward_static")
             return self.y
-        rc = self.fn(C.byref(self.desc), C.byref(self.w), _p(self.y), _p(self.ws), self.ws_bytes,
-                     r, _stream(stream))
-        _check(rc, self.fn_name)
+        _launch(self.fn, self.fn_name, self.y.device, stream, C.byref(self.desc), C.byref(self.w),
+                _p(self.y), _p(self.ws), self.ws_bytes, r)
         return self.y
 
 
@@ -424,29 +423,43 @@ def _float_code(dtype: torch.dtype) -> int:
     return MOE_F32 if dtype == torch.float32 else MOE_BF16
 
 
-def _on_gpu(t, what):
-    """The device that a call runs on: that of its first tensor, whatever device is current."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} is on {t.device}, expected a GPU")
-    return torch.cuda.device(t.device)
+def _launch(fn, name, device, stream, *args):
+    """fn(*args, stream) on `device`, whatever device is current, on `stream` (None: the device's
+    current stream). The stream's raw handle is read directly: a torch.cuda.Stream object per call
+    costs more host time than the launch."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors are on {device}, expected a GPU")
+    i = device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(i)
+    elif stream.device.index != i:
+        raise ValueError(f"{name}: tensors are on {device}, the stream is on {stream.device}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == i:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, raw)
+    if rc != MOE_OK:
+        raise MoeError(rc, name)
 
 
 def _mx_format(codes, scales, what):
     """(moe_dtype_t, element columns) of a block-scaled matrix, read off its shapes: one scale per
     32 columns, two MXFP4 elements or one MXFP8 element per byte."""
-    for t, n in ((codes, what), (scales, f"the scales of {what}")):
-        if t is None or t.dtype != torch.uint8:
-            raise ValueError(f"{n} must be a uint8 tensor")
-    if codes.dim() < 1 or scales.shape[:-1] != codes.shape[:-1] or scales.device != codes.device:
-        raise ValueError(f"{what} {tuple(codes.shape)} on {codes.device} and its scales "
-                         f"{tuple(scales.shape)} on {scales.device} do not belong together")
-    cols = MX_BLOCK * scales.shape[-1]
-    if cols and codes.shape[-1] * 2 == cols:
+    cs, ss = codes.shape, scales.shape
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{what} and its scales must be uint8 tensors")
+    if not cs or cs[:-1] != ss[:-1] or scales.device != codes.device:
+        raise ValueError(f"{what} {tuple(cs)} on {codes.device} and its scales {tuple(ss)} on "
+                         f"{scales.device} do not belong together")
+    cols = MX_BLOCK * ss[-1]
+    if cols and cs[-1] * 2 == cols:
         return MOE_MXFP4, cols
-    if cols and codes.shape[-1] == cols:
+    if cols and cs[-1] == cols:
         return MOE_MXFP8, cols
-    raise ValueError(f"{what}: {codes.shape[-1]} bytes and {scales.shape[-1]} scales a row are "
-                     "neither MXFP4 nor MXFP8")
+    raise ValueError(f"{what}: {cs[-1]} bytes and {ss[-1]} scales a row are neither MXFP4 nor MXFP8")
 
 
 def mx_quantize(x, fmt="mxfp4", *, codes=None, scales=None, stream=None):
@@ -455,22 +468,26 @@ def mx_quantize(x, fmt="mxfp4", *, codes=None, scales=None, stream=None):
     or [.., cols] ("mxfp8"), scales [.., cols / 32], both uint8. See moe_mx_quantize in moe.h."""
     if fmt not in _MX_FORMATS:
         raise ValueError(f"fmt {fmt!r} is not one of {sorted(_MX_FORMATS)}")
-    dt = _float_code(x.dtype)
-    if x.dim() < 1 or x.shape[-1] % MX_BLOCK or not x.shape[-1]:
-        raise ValueError(f"x {tuple(x.shape)}: the last dimension is not a multiple of {MX_BLOCK}")
-    cols, lead = x.shape[-1], tuple(x.shape[:-1])
-    u8 = dict(dtype=torch.uint8, device=x.device)
-    per = 2 if fmt == "mxfp4" else 1
-    with _on_gpu(x, "x"):
-        made = [t is None for t in (codes, scales)]
-        codes = torch.empty(lead + (cols // per,), **u8) if codes is None else codes
-        scales = torch.empty(lead + (cols // MX_BLOCK,), **u8) if scales is None else scales
-        _need(codes, lead + (cols // per,), "codes", torch.uint8, x.device)
-        _need(scales, lead + (cols // MX_BLOCK,), "scales", torch.uint8, x.device)
-        rc = lib().moe_mx_quantize(_p(x), dt, x.numel() // cols, cols, _MX_FORMATS[fmt], _p(codes),
-                                   _p(scales), _stream(stream))
-        _check(rc, "moe_mx_quantize")
-        _used_on(stream, codes if made[0] else None, scales if made[1] else None)
+    dt, shape = _float_code(x.dtype), x.shape
+    if not shape or shape[-1] % MX_BLOCK or not shape[-1]:
+        raise ValueError(f"x {tuple(shape)}: the last dimension is not a multiple of {MX_BLOCK}")
+    cols, lead, dev = shape[-1], shape[:-1], x.device
+    cshape = lead + (cols // 2 if fmt == "mxfp4" else cols,)
+    sshape = lead + (cols // MX_BLOCK,)
+    made = []
+    if codes is None:
+        codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
+        made.append(codes)
+    else:
+        _need(codes, cshape, "codes", torch.uint8, dev)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
+        made.append(scales)
+    else:
+        _need(scales, sshape, "scales", torch.uint8, dev)
+    _launch(lib().moe_mx_quantize, "moe_mx_quantize", dev, stream, _p(x), dt, x.numel() // cols,
+            cols, _MX_FORMATS[fmt], _p(codes), _p(scales))
+    _used_on(stream, *made)
     return codes, scales
 
 
@@ -479,15 +496,16 @@ def mx_dequantize(codes, scales, *, dtype=torch.float32, out=None, stream=None):
     the format is read off the shapes. See moe_mx_dequantize in moe.h."""
     fmt, cols = _mx_format(codes, scales, "codes")
     dt = _float_code(dtype)
-    shape = tuple(codes.shape[:-1]) + (cols,)
-    with _on_gpu(codes, "codes"):
-        made = out is None
-        out = torch.empty(shape, dtype=dtype, device=codes.device) if made else out
-        _need(out, shape, "out", dtype, codes.device)
-        rc = lib().moe_mx_dequantize(_p(codes), _p(scales), fmt, out.numel() // cols, cols, _p(out),
-                                     dt, _stream(stream))
-        _check(rc, "moe_mx_dequantize")
-        _used_on(stream, out if made else None)
+    shape, dev = codes.shape[:-1] + (cols,), codes.device
+    made = out is None
+    if made:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out, shape, "out", dtype, dev)
+    _launch(lib().moe_mx_dequantize, "moe_mx_dequantize", dev, stream, _p(codes), _p(scales), fmt,
+            out.numel() // cols, cols, _p(out), dt)
+    if made:
+        _used_on(stream, out)
     return out
 
 
@@ -497,19 +515,20 @@ def mx_gemm(a, a_scales, w, w_scales, *, out_dtype=torch.bfloat16, out=None, str
     moe_mx_gemm in moe.h."""
     fa, K = _mx_format(a, a_scales, "a")
     fw, kw = _mx_format(w, w_scales, "w")
-    if a.dim() != 2 or w.dim() != 2 or K != kw or a.device != w.device:
-        raise ValueError(f"a {tuple(a.shape)} ({K} columns, {a.device}) and w {tuple(w.shape)} "
+    dev = a.device
+    if a.dim() != 2 or w.dim() != 2 or K != kw or dev != w.device:
+        raise ValueError(f"a {tuple(a.shape)} ({K} columns, {dev}) and w {tuple(w.shape)} "
                          f"({kw} columns, {w.device}) do not multiply")
-    dt = _float_code(out_dtype)
-    shape = (a.shape[0], w.shape[0])
-    with _on_gpu(a, "a"):
-        made = out is None
-        out = torch.empty(shape, dtype=out_dtype, device=a.device) if made else out
-        _need(out, shape, "out", out_dtype, a.device)
-        rc = lib().moe_mx_gemm(_p(a), _p(a_scales), fa, _p(w), _p(w_scales), fw, shape[0], shape[1],
-                               K, _p(out), dt, _stream(stream))
-        _check(rc, "moe_mx_gemm")
-        _used_on(stream, out if made else None)
+    dt, M, N = _float_code(out_dtype), a.shape[0], w.shape[0]
+    made = out is None
+    if made:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _need(out, (M, N), "out", out_dtype, dev)
+    _launch(lib().moe_mx_gemm, "moe_mx_gemm", dev, stream, _p(a), _p(a_scales), fa, _p(w),
+            _p(w_scales), fw, M, N, K, _p(out), dt)
+    if made:
+        _used_on(stream, out)
     return out
 
 

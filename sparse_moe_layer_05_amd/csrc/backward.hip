@@ -354,3 +354,6 @@ hipError_t launch_pairs_to_tokens(const float* du, const int32_t* pos, int T, in
 }
 
 }  // namespace moe
+
+#include "mx_convert.hpp"
+#include "mx_tiles.hpp"

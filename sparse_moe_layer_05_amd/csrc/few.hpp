@@ -10,7 +10,7 @@
 namespace moe {
 
 constexpr int kFewTokens = 16;          // one matrix-core block of tokens
-constexpr int kFewNarrowElts = 65536;   // T * D of 8- and 4-bit experts: their rows stay in LDS
+constexpr int kFewNarrowElts = 65536;   // T * D and T * I of 8- and 4-bit experts: rows stay in LDS
 
 struct FewParams {
   int T = 0, H = 0, E = 0, k = 0, I = 0, Is = 0, L = 0, D = 0;
@@ -40,6 +40,8 @@ struct FewParams {
   float* gate_m = nullptr;              // [slots][kFewTokens] gate of a token, 0 where not selected
   uint32_t* slot_mask = nullptr;        // [slots] bit t: token t selected the expert
   uint32_t* hmax = nullptr;             // [slots][kFewTokens] bits of max h (8- and 4-bit experts)
+  float* slabs = nullptr;               // [D / 16][parts][kFewTokens][16] (parts > 1)
+  int32_t* joined = nullptr;            // [D / 16] parts of a column block that have ended
   uint16_t* h = nullptr;                // [slots][T][I] bf16
   uint16_t* hs = nullptr;               // [T][Is] bf16
   uint16_t* u = nullptr;                // [T][L] bf16
@@ -48,8 +50,14 @@ struct FewParams {
 
 __host__ __device__ inline int few_slots(int T, int E, int k) { return E < T * k ? E : T * k; }
 
-// The launches, in order; launch_few_front does nothing where there is nothing to do before the
-// experts, launch_few_out is LatentMoE's.
+// Parts that the down projection's column blocks of 16 are cut into: about two workgroups of
+// eight waves per CU.
+inline int few_parts(int D) {
+  const int n = 512 / (D / 16);
+  return n < 1 ? 1 : (n > 8 ? 8 : n);
+}
+
+// The launches, in order; launch_few_out is LatentMoE's.
 hipError_t launch_few_front(const FewParams& p, hipStream_t s);
 hipError_t launch_few_up(const FewParams& p, hipStream_t s);
 hipError_t launch_few_down(const FewParams& p, hipStream_t s);

@@ -5,6 +5,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "moe.h"
@@ -637,6 +638,7 @@ struct FewPlan {
   Plan p;  // dimensions and types as make_plan checks them
   size_t logits = 0, score = 0, idx = 0, gates = 0, counts = 0, offsets = 0, perm = 0, pos = 0;
   size_t dscratch = 0, n_slots = 0, slot_e = 0, gate_m = 0, slot_mask = 0, hmax = 0;
+  size_t slabs = 0, joined = 0;
   size_t h = 0, hs = 0, u = 0, z = 0, total = 0;
 };
 
@@ -649,7 +651,7 @@ int32_t make_few_plan(const moe_desc_t* d, FewPlan* out) {
   if (d->flags & ~MOE_ROUTING_GIVEN) return MOE_ERR_INVALID_ARG;
   if (p.act != Elt::BF16 || p.T > kFewTokens) return MOE_ERR_UNSUPPORTED;
   const bool narrow = p.ex != Elt::BF16;
-  if (narrow && (int64_t)p.T * p.D > kFewNarrowElts) return MOE_ERR_UNSUPPORTED;
+  if (narrow && (int64_t)p.T * std::max(p.D, p.I) > kFewNarrowElts) return MOE_ERR_UNSUPPORTED;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -671,6 +673,8 @@ int32_t make_few_plan(const moe_desc_t* d, FewPlan* out) {
   f.gate_m = take(S * kFewTokens * 4);
   f.slot_mask = take(S * 4);
   if (narrow) f.hmax = take(S * kFewTokens * 4);
+  f.slabs = take((size_t)p.D * few_parts(p.D) * kFewTokens * 4);
+  f.joined = take((size_t)p.D / 16 * 4);
   f.h = take(S * T * (size_t)p.I * 2);
   if (p.Is) f.hs = take(T * (size_t)p.Is * 2);
   if (p.L) {
@@ -722,6 +726,8 @@ int32_t few_forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* 
   p.gate_m = (float*)(base + f.gate_m);
   p.slot_mask = (uint32_t*)(base + f.slot_mask);
   p.hmax = pl.ex != Elt::BF16 ? (uint32_t*)(base + f.hmax) : nullptr;
+  p.slabs = (float*)(base + f.slabs);
+  p.joined = (int32_t*)(base + f.joined);
   p.h = (uint16_t*)(base + f.h);
   p.hs = pl.Is ? (uint16_t*)(base + f.hs) : nullptr;
   p.u = pl.L ? (uint16_t*)(base + f.u) : nullptr;
@@ -1297,7 +1303,7 @@ int32_t moe_mx_gemm(const void* A, const uint8_t* a_scales, moe_dtype_t a_fmt, c
   if (M < 0 || N < 16 || N % 16 || K < kMxBlockElts || K % kMxBlockElts) return MOE_ERR_INVALID_ARG;
   if (!mx_format(a_fmt) || !mx_format(w_fmt) || (c_dt != MOE_F32 && c_dt != MOE_BF16))
     return MOE_ERR_UNSUPPORTED;
-  // fp32 results only where the matrix core's sums hold fp32 (see mx_gemm.hip)
+  // fp32 results only where the matrix core's sums hold fp32 (see mx_tiles.hpp)
   if (c_dt == MOE_F32 && (a_fmt != MOE_MXFP4 || w_fmt != MOE_MXFP4)) return MOE_ERR_UNSUPPORTED;
   // 32-bit operand offsets: A and W each span less than 2 GiB
   constexpr int64_t kOp = ((int64_t)1 << 31) - 1;

@@ -11,11 +11,16 @@
 // Four lanes share a block, eight elements each: 16- or 32-byte loads, the maximum over the four
 // by two quad permutations, no LDS. Rows are contiguous, so a matrix is one run of blocks. Each
 // thread takes kIter groups of eight whose loads are all in flight together.
+// Included once, by backward.hip: these kernels are part of that object, so that the library stays the
+// objects that its parts are linked from elsewhere (host code under the sanitizers).
+#pragma once
+
 #include "common.hpp"
 #include "mx.hpp"
 
 namespace moe {
 namespace {
+namespace mx_convert {
 
 constexpr int kIter = 4;      // groups of 8 elements per thread
 constexpr int kThreads = 256;
@@ -155,7 +160,10 @@ dim3 grid_of(int64_t n8) {
   return dim3((unsigned)((n8 + kThreads * kIter - 1) / (kThreads * kIter)));
 }
 
+}  // namespace mx_convert
 }  // namespace
+
+using namespace mx_convert;
 
 hipError_t launch_mx_quantize(const void* x, Elt xt, int64_t n, Elt fmt, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {

@@ -21,6 +21,10 @@
 // Order of k (32x32x64 / 16x16x128): lane group g holds, of an E4M3 operand, k 16g .. 16g + 15
 // and KS/2 + 16g .. KS/2 + 16g + 15 (KS = 64 or 128: the two 16-byte halves of its 32 bytes), of
 // an E2M1 operand k 32g .. 32g + 31, and the scale byte it passes covers k 32g .. 32g + 31.
+// Included once, by backward.hip: these kernels are part of that object, so that the library stays the
+// objects that its parts are linked from elsewhere (host code under the sanitizers).
+#pragma once
+
 #include <algorithm>
 
 #include "common.hpp"
@@ -28,6 +32,7 @@
 
 namespace moe {
 namespace {
+namespace mx_tiles {
 
 // Operand formats of the kernels: E4M3 with block scales, E2M1 with block scales, E4M3 with a
 // row scale (A only).
@@ -472,7 +477,10 @@ hipError_t run_dense(const MxGemmParams& p, hipStream_t s) {
   return run_tile<128, 192, 2, 2, 2, FA, FW>(p, cdiv(p.M, 128), s);
 }
 
+}  // namespace mx_tiles
 }  // namespace
+
+using namespace mx_tiles;
 
 hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, hipStream_t s) {
   if (p.K < 32 || p.K % 32 || p.N < 16 || p.N % 16 || !p.w_mx) return hipErrorInvalidValue;

@@ -705,3 +705,4 @@ hipError_t launch_bias_update(const int32_t* counts, const float* target, int E,
 
 }  // namespace moe
 
+#include "few_kernels.hpp"

@@ -35,6 +35,8 @@ def size(d):
     (dict(expert_dtype=B.MOE_MXFP8, T=16, H=4096), OK),
     (dict(expert_dtype=B.MOE_MXFP8, T=16, H=4128), UNS),     # T * D over 65536
     (dict(expert_dtype=B.MOE_MXFP8, T=16, H=8192, latent=1024), OK),
+    (dict(expert_dtype=B.MOE_FP8_E4M3, T=16, I=4096), OK),
+    (dict(expert_dtype=B.MOE_FP8_E4M3, T=16, I=4112), UNS),  # T * I over 65536
     (dict(T=16, H=8192), OK),                                # bf16: no such bound
     (dict(flags=B.PATH_STREAM), BAD), (dict(flags=B.PATH_GROUPED), BAD), (dict(flags=3), BAD),
     (dict(flags=B.SAVED_IN_WORKSPACE), BAD), (dict(flags=B.ROUTING_GIVEN), OK),
