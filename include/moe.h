@@ -183,8 +183,8 @@ int32_t moe_layer_forward_static(const moe_desc_t *desc, const moe_weights_t *w,
  * desc->latent > 0) in three launches (four for LatentMoE), where the decode path takes six to
  * nine: for single sequences and small decode batches, whose time is launches and not bytes.
  * Arguments, formats, roundings and errors as moe_layer_forward, with these differences:
- *   - T <= MOE_FEW_TOKENS and act_dtype MOE_BF16, and T * D and T * I <= 65536 for 8- and
- *     4-bit experts (D = H, or latent), else MOE_ERR_UNSUPPORTED; flags: MOE_PATH_AUTO with or without
+ *   - T <= MOE_FEW_TOKENS and act_dtype MOE_BF16, and for 8- and 4-bit experts T * D and T * I
+ *     <= 65536, D (H, or latent) and I rounded up to multiples of 128, else MOE_ERR_UNSUPPORTED; flags: MOE_PATH_AUTO with or without
  *     MOE_ROUTING_GIVEN, else MOE_ERR_INVALID_ARG.
  *   - Workspace: moe_few_workspace_size bytes; its contents need no preparation and are not kept
  *     between calls.

@@ -10,7 +10,8 @@
 namespace moe {
 
 constexpr int kFewTokens = 16;          // one matrix-core block of tokens
-constexpr int kFewNarrowElts = 65536;   // T * D and T * I of 8- and 4-bit experts: rows stay in LDS
+// 8- and 4-bit experts: T * D and T * I in whole steps of 128, whose rows stay in LDS as bf16.
+constexpr int kFewNarrowElts = 65536;
 
 struct FewParams {
   int T = 0, H = 0, E = 0, k = 0, I = 0, Is = 0, L = 0, D = 0;
@@ -43,9 +44,12 @@ struct FewParams {
   float* slabs = nullptr;               // [D / 16][parts][kFewTokens][16] (parts > 1)
   int32_t* joined = nullptr;            // [D / 16] parts of a column block that have ended
   uint16_t* h = nullptr;                // [slots][T][I] bf16
-  uint16_t* hs = nullptr;               // [T][Is] bf16
+  uint16_t* h_lo = nullptr;             // what h's rounding left over (bf16 experts)
+  uint16_t* hs = nullptr;               // [T][Is] bf16, and what its rounding left over
+  uint16_t* hs_lo = nullptr;
   uint16_t* u = nullptr;                // [T][L] bf16
-  uint16_t* z = nullptr;                // [T][L] bf16
+  uint16_t* z = nullptr;                // [T][L] bf16, and what its rounding left over
+  uint16_t* z_lo = nullptr;
 };
 
 __host__ __device__ inline int few_slots(int T, int E, int k) { return E < T * k ? E : T * k; }

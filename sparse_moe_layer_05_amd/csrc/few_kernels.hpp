@@ -18,14 +18,21 @@
 // not select it are dropped (not multiplied by zero, so a NaN stays in its own row).
 //
 // Products: the weights are the matrix core's first operand (16 rows), loaded from HBM straight to
-// registers. Waves split K and join in LDS in wave order, so results are deterministic. Formats
-// and roundings are those of the decode path: 8- and 4-bit experts meet rows quantised per row to
-// e4m3 (scale amax / 448), h is rounded to bf16 first.
+// registers and multiplied as bf16: e4m3 and E2M1 elements times their block scales are bf16
+// numbers, and so are e4m3 activation codes, while the 8- and 4-bit instructions cut products (13
+// bits below the largest of eight) and thereby move roundings of h, one in some hundred rows its
+// quantisation scale and with it 4% of the row. The conversions hide under the loads. Waves split
+// K and join in LDS in wave order: results are deterministic.
+//
+// Formats as on the decode path: 8- and 4-bit experts meet rows quantised per row to e4m3 (scale
+// amax / 448), h rounded to bf16 first. Where the definition does not round, intermediates are
+// kept as the sum of two bf16 (16 bits; the shared expert's h, a bf16 expert's h, LatentMoE's z),
+// multiplied in two instructions by the weights that are in registers anyway.
 //
 // Router: logits are summed in fp64 and rounded to fp32, so that the selection does not depend on
 // the order of the sum; scores and keys as in the router kernels.
-// Included once, by routing.hip: these kernels are part of that object, so that the library stays the
-// objects that its parts are linked from elsewhere (host code under the sanitizers).
+// Included once, by routing.hip: these kernels are part of that object, so that the library stays
+// the objects that its parts are linked from elsewhere (host code under the sanitizers).
 #pragma once
 
 #include <algorithm>
@@ -41,93 +48,128 @@ namespace few_layer {
 constexpr int TB = kFewTokens;
 
 // ---------------------------------------------------------------------- weight streams
-// A step is KS elements of K, one matrix-core instruction; lane l holds weight row l % 16 and
-// token l % 16, group g = l / 16 the elements k_of(c, g) .. of its 16-byte chunks c. Result
-// register i of lane l is out[weight row 4 g + i][token l % 16].
+// A step is KS elements of K: MF matrix-core instructions. Lane l holds weight row l % 16 and
+// token l % 16; group g = l / 16 holds, of both operands and for instruction j of a step, the 8
+// elements from k_of(j, g) on (any order of k serves: both sides use the same). bf16: one 16-byte
+// chunk of 8 elements. 8- and 4-bit weights: 32 consecutive elements a lane, one block scale.
+// Result register i of lane l is out[weight row 4 g + i][token l % 16].
 template <Elt F> struct Fmt {
   static constexpr bool narrow = F != Elt::BF16;
   static constexpr bool mx = F == Elt::MXFP4 || F == Elt::MXFP8;
-  static constexpr int KS = narrow ? 128 : 32;
+  static constexpr int KS = narrow ? 128 : 32, MF = narrow ? 4 : 1;
   static constexpr int bits = F == Elt::MXFP4 ? 4 : (narrow ? 8 : 16);
-  static constexpr int CW = F == Elt::MXFP4 ? 1 : (narrow ? 2 : 1);  // 16-byte chunks of weights
-  static constexpr int CA = narrow ? 2 : 1;                          // and of activations
-  // first element of chunk c in a step
-  static __device__ __forceinline__ int kw(int c, int g) {
-    return F == Elt::MXFP4 ? 32 * g : (narrow ? 64 * c + 16 * g : 8 * g);
-  }
-  static __device__ __forceinline__ int ka(int c, int g) { return narrow ? 64 * c + 16 * g : 8 * g; }
+  static constexpr int CW = F == Elt::BF16 || F == Elt::MXFP4 ? 1 : 2;  // 16-byte chunks of weights
+  static constexpr int EC = 128 / bits;                                // elements of a chunk
+  static __device__ __forceinline__ int kw(int c, int g) { return (narrow ? 32 : 8) * g + EC * c; }
+  static __device__ __forceinline__ int k_of(int j, int g) { return (narrow ? 32 : 8) * g + 8 * j; }
 };
 
-__device__ __forceinline__ i32x8_t cat(uint4 p, uint4 q) {
-  return i32x8_t{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
+// One step's weights of a lane.
+template <Elt F> struct WStep {
+  uint4 c[Fmt<F>::CW];
+  int sc;   // E8M0 code (MX)
+};
+// Loads step s of the row at w (wx: its block scales). Chunks at or past kend are read from the
+// row's start; mask_step zeroes them.
+template <Elt F>
+__device__ __forceinline__ void load_step(WStep<F>& x, const uint8_t* w, const uint8_t* wx, int s,
+                                          int kend, int K, int g) {
+  using M = Fmt<F>;
+#pragma unroll
+  for (int c = 0; c < M::CW; ++c) {
+    const int el = s * M::KS + M::kw(c, g);
+    x.c[c] = *(const uint4*)(w + (int64_t)(el < kend ? el : 0) * M::bits / 8);
+  }
+  if constexpr (M::mx) x.sc = wx[min(s * 4 + g, K / 32 - 1)];
+}
+template <Elt F>
+__device__ __forceinline__ void mask_step(WStep<F>& x, int s, int kend, int g) {
+  using M = Fmt<F>;
+#pragma unroll
+  for (int c = 0; c < M::CW; ++c)
+    if (s * M::KS + M::kw(c, g) >= kend) x.c[c] = make_uint4(0, 0, 0, 0);
+}
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bits_of(bf16x2_t v) { return __builtin_bit_cast(uint32_t, v); }
+// Instruction j's weight fragment in bf16.
+template <Elt F>
+__device__ __forceinline__ bf16x8_t wfrag(const WStep<F>& x, int j) {
+  uint4 o = x.c[0];
+  if constexpr (F == Elt::MXFP4) {
+    const float s = __uint_as_float((uint32_t)x.sc << 23);
+    const uint32_t w = j == 0 ? x.c[0].x : j == 1 ? x.c[0].y : j == 2 ? x.c[0].z : x.c[0].w;
+    o = make_uint4(bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)));
+  } else if constexpr (Fmt<F>::narrow) {
+    const float s = Fmt<F>::mx ? __uint_as_float((uint32_t)x.sc << 23) : 1.f;
+    const uint4 c = j < 2 ? x.c[0] : x.c[Fmt<F>::CW - 1];
+    const uint32_t lo = j & 1 ? c.z : c.x, hi = j & 1 ? c.w : c.y;
+    o = make_uint4(bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true)));
+  }
+  return __builtin_bit_cast(bf16x8_t, o);
+}
+__device__ __forceinline__ f32x4_t mul(bf16x8_t w, uint4 a, f32x4_t acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8_t, a), acc, 0, 0, 0);
 }
 
-// acc += W[row, steps s0 .. s1) * A. w: the lane's weight row; wx: its block scales (MX);
-// aload(el) loads the lane's token chunk that starts at element el. U steps of loads are in flight
-// together; chunks past K are read from the row's start and zeroed on both sides.
-template <Elt F, int U, class ALoad>
-__device__ __forceinline__ f32x4_t dot_steps(const uint8_t* w, const uint8_t* wx, int K, int s0,
-                                             int s1, int g, ALoad aload, f32x4_t acc) {
-  using M = Fmt<F>;
-  const int kend = min(K, s1 * M::KS);
+// 8 bf16 -> the bf16 values of their e4m3 codes: e4m3(v * inv).
+__device__ __forceinline__ uint32_t code2(uint32_t p, float inv) {
+  const uint32_t c = cvt_fp8x2(bf16_bits_to_f32(p & 0xFFFF) * inv, bf16_bits_to_f32(p >> 16) * inv);
+  return bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, false));
+}
+__device__ __forceinline__ uint4 codes8(uint4 v, float inv) {
+  return make_uint4(code2(v.x, inv), code2(v.y, inv), code2(v.z, inv), code2(v.w, inv));
+}
+
+// Four fp32 as a pair of bf16 each, v = hi + lo up to 2^-17 of v, at column n of row o.
+__device__ __forceinline__ void store_pair(uint16_t* hi, uint16_t* lo, int64_t at, const float* v) {
+  const uint2 h = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  *(uint2*)(hi + at) = h;
+  *(uint2*)(lo + at) =
+      make_uint2(pack_bf16x2(v[0] - bf16_bits_to_f32(h.x & 0xFFFF), v[1] - bf16_bits_to_f32(h.x >> 16)),
+                 pack_bf16x2(v[2] - bf16_bits_to_f32(h.y & 0xFFFF), v[3] - bf16_bits_to_f32(h.y >> 16)));
+}
+
+// acc += W[row, steps s0 .. s1) * (A + A2) of bf16 rows in memory, U steps of loads in flight.
+// No branch on the steps past the end: loads whose use is conditional are moved to it, one by
+// one, instead of being in flight together.
+template <int U, bool LO>
+__device__ __forceinline__ f32x4_t dot_rows(const uint16_t* w, const uint16_t* a,
+                                            const uint16_t* a2, int K, int s0, int s1, int g,
+                                            f32x4_t acc) {
+  const int kend = min(K, s1 * 32);
   for (int s = s0; s < s1; s += U) {
-    uint4 wf[U][M::CW];
-    uint4 af[U][M::CA];
-    int sc[U];
+    uint4 wf[U], af[U], bf[LO ? U : 1];
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const int k0 = (s + q) * M::KS;
-#pragma unroll
-      for (int c = 0; c < M::CW; ++c) {
-        const int el = k0 + M::kw(c, g);
-        wf[q][c] = *(const uint4*)(w + (int64_t)(el < kend ? el : 0) * M::bits / 8);
-      }
-#pragma unroll
-      for (int c = 0; c < M::CA; ++c) {
-        const int el = k0 + M::ka(c, g);
-        af[q][c] = aload(el < kend ? el : 0);
-      }
-      if constexpr (M::mx) sc[q] = wx[min(k0 / 32 + g, K / 32 - 1)];
-      else sc[q] = 127;
+      const int el = (s + q) * 32 + 8 * g, at = el < kend ? el : 0;
+      wf[q] = *(const uint4*)(w + at);
+      af[q] = *(const uint4*)(a + at);
+      if constexpr (LO) bf[q] = *(const uint4*)(a2 + at);
     }
-    // no branch on the steps past the end: loads whose use is conditional are moved to it, one by
-    // one, instead of being in flight together
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const int k0 = (s + q) * M::KS;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint4 wv[M::CW], av[M::CA];
-#pragma unroll
-      for (int c = 0; c < M::CW; ++c) wv[c] = k0 + M::kw(c, g) < kend ? wf[q][c] : zero;
-#pragma unroll
-      for (int c = 0; c < M::CA; ++c) av[c] = k0 + M::ka(c, g) < kend ? af[q][c] : zero;
-      if constexpr (!M::narrow)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[0]),
-                                                     __builtin_bit_cast(bf16x8_t, av[0]), acc, 0,
-                                                     0, 0);
-      else
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            cat(wv[0], M::CW == 2 ? wv[M::CW - 1] : zero), cat(av[0], av[M::CA - 1]), acc,
-            F == Elt::MXFP4 ? 4 : 0, 0, 0, sc[q], 0, 127);
+      if ((s + q) * 32 + 8 * g >= kend) wf[q] = make_uint4(0, 0, 0, 0);
+      acc = mul(__builtin_bit_cast(bf16x8_t, wf[q]), af[q], acc);
+      if constexpr (LO) acc = mul(__builtin_bit_cast(bf16x8_t, wf[q]), bf[q], acc);
     }
   }
   return acc;
 }
 
-// 4 bf16 -> 4 e4m3 codes of v * inv.
-__device__ __forceinline__ uint32_t codes4(uint32_t p, uint32_t q, float inv) {
-  return cvt_fp8x2(bf16_bits_to_f32(p & 0xFFFF) * inv, bf16_bits_to_f32(p >> 16) * inv) |
-         cvt_fp8x2(bf16_bits_to_f32(q & 0xFFFF) * inv, bf16_bits_to_f32(q >> 16) * inv) << 16;
-}
-
-// out[t][n0 .. n0 + 15] = act(A1[t] . W1[n] + A2[t] . W2[n]) in bf16, by the NW waves of a
-// workgroup, each over a contiguous share of the steps. part: [NW][16][17] floats of LDS.
+// out[t][n0 .. n0 + 15] = act(A1[t] . W1[n] + A2[t] . W2[n]) by the NW waves of a workgroup, each
+// over a contiguous share of the steps. LO: the activations are pairs. out_lo: so is the result.
 struct Dense {
-  const uint16_t *A1, *W1, *A2, *W2;
+  const uint16_t *A1, *A1lo, *W1, *A2, *A2lo, *W2;
   int K1, K2, N, T, sq;
-  uint16_t* out;
+  uint16_t *out, *out_lo;
 };
-template <int NW, int U>
+template <int NW, int U, bool LO>
 __device__ __forceinline__ void dense_unit(const Dense& d, int n0, float (*part)[16][17]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, r = lane & 15;
@@ -135,13 +177,12 @@ __device__ __forceinline__ void dense_unit(const Dense& d, int n0, float (*part)
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   const int st1 = cdiv(d.K1, 32), st = st1 + cdiv(d.K2, 32), per = cdiv(st, NW);
   const int lo = min(st, wave * per), hi = min(st, lo + per);
-  auto seg = [&](const uint16_t* A, const uint16_t* W, int K, int a, int b) {
-    const uint16_t* row = A + (int64_t)t * K;
-    acc = dot_steps<Elt::BF16, U>((const uint8_t*)(W + (int64_t)(n0 + r) * K), nullptr, K, a, b, g,
-                                  [&](int el) { return *(const uint4*)(row + el); }, acc);
-  };
-  if (lo < st1) seg(d.A1, d.W1, d.K1, lo, min(hi, st1));
-  if (hi > st1) seg(d.A2, d.W2, d.K2, max(lo, st1) - st1, hi - st1);
+  if (lo < st1)
+    acc = dot_rows<U, LO>(d.W1 + (int64_t)(n0 + r) * d.K1, d.A1 + (int64_t)t * d.K1,
+                          d.A1lo + (int64_t)t * d.K1, d.K1, lo, min(hi, st1), g, acc);
+  if (hi > st1)
+    acc = dot_rows<U, LO>(d.W2 + (int64_t)(n0 + r) * d.K2, d.A2 + (int64_t)t * d.K2,
+                          d.A2lo + (int64_t)t * d.K2, d.K2, max(lo, st1) - st1, hi - st1, g, acc);
 #pragma unroll
   for (int i = 0; i < 4; ++i) part[wave][r][4 * g + i] = acc[i];
   __syncthreads();
@@ -154,8 +195,11 @@ __device__ __forceinline__ void dense_unit(const Dense& d, int n0, float (*part)
       for (int q = 1; q < NW; ++q) v[i] += part[q][r][4 * g + i];
       if (d.sq) v[i] = sqrelu(v[i]);
     }
-    *(uint2*)(d.out + (int64_t)r * d.N + n0 + 4 * g) =
-        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    const int64_t at = (int64_t)r * d.N + n0 + 4 * g;
+    if (d.out_lo)
+      store_pair(d.out, d.out_lo, at, v);
+    else
+      *(uint2*)(d.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
 }
 
@@ -216,12 +260,14 @@ __global__ __launch_bounds__(256) void few_front(FewParams p) {
   if (!p.L) return;
   int n = bid - nr;
   if (n < p.Is / 16) {
-    dense_unit<4, 7>(Dense{p.x, p.Ws_up, nullptr, nullptr, p.H, 0, p.Is, p.T, 1, p.hs}, 16 * n, part);
+    dense_unit<4, 8, false>(Dense{p.x, p.x, p.Ws_up, nullptr, nullptr, nullptr, p.H, 0, p.Is, p.T,
+                                  1, p.hs, p.hs_lo}, 16 * n, part);
     return;
   }
   n -= p.Is / 16;
   if (n < p.L / 16)
-    dense_unit<4, 7>(Dense{p.x, p.W_in, nullptr, nullptr, p.H, 0, p.L, p.T, 0, p.u}, 16 * n, part);
+    dense_unit<4, 8, false>(Dense{p.x, p.x, p.W_in, nullptr, nullptr, nullptr, p.H, 0, p.L, p.T, 0,
+                                  p.u, nullptr}, 16 * n, part);
 }
 
 // --------------------------------------------------------------------------------- 2 up
@@ -229,19 +275,17 @@ __global__ __launch_bounds__(256) void few_front(FewParams p) {
 // its waves split K, and the loads are issued before the selection, which needs two round trips to
 // the scores and a chain of wave-wide maxima. Then units of (touched expert, 16 rows of W_up), one
 // wave each over all of K, double buffered: while a batch of U steps is multiplied the next one
-// (of this unit or of the wave's next) is in flight. Activations are read from LDS: bf16 rows, or
-// e4m3 codes for 8- and 4-bit experts. NPER * 64 >= E; XLDS: the rows fit (else from L2).
+// (of this unit or of the wave's next) is in flight. Activations are read from LDS, as bf16 rows
+// or the bf16 values of their e4m3 codes, zeros up to a whole step. NPER * 64 >= E; XLDS: the rows
+// fit (else bf16 ones are read from L2).
 constexpr int kUpWaves = 8;
 constexpr int kUpThreads = 64 * kUpWaves;
-constexpr size_t kUpRowsLds = 96 * 1024;   // of the staged activations
+constexpr size_t kUpRowsLds = 130 * 1024;   // of the staged activations
 constexpr int kSharedSteps = 12;   // steps of the shared unit in flight per wave
 
-// LDS row stride of the staged activations, an odd number of 16-byte chunks (16 rows at one chunk
-// index then fall on distinct banks).
-__host__ __device__ inline int up_stride(int row_bytes) {
-  const int c = (row_bytes + 15) / 16;
-  return 16 * (c | 1);
-}
+// LDS row stride in bytes of K staged elements, whole steps of 128 and an odd number of 16-byte
+// chunks (16 rows at one chunk index then fall on distinct banks).
+__host__ __device__ inline int lds_stride(int K) { return (K + 127) / 128 * 256 + 16; }
 
 template <Elt F, int NPER, bool XLDS>
 __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
@@ -253,7 +297,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   __shared__ int cnt[NPER];
   __shared__ float part[kUpWaves][16][17];
   __shared__ float row_scale[TB];
-  extern __shared__ __attribute__((aligned(16))) uint8_t xl[];  // [T] rows of lds bytes
+  extern __shared__ __attribute__((aligned(16))) uint8_t xl[];  // [T] rows of ldx bytes
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r = lane & 15;
@@ -271,15 +315,15 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
     const uint16_t* w = p.Ws_up + (int64_t)(16 * blockIdx.x + r) * p.H;
 #pragma unroll
     for (int q = 0; q < kSharedSteps; ++q) {
-      const int el = (slo + q) * 32 + 8 * g;
-      sw[q] = *(const uint4*)(w + (el < send ? el : 0));
-      sa[q] = *(const uint4*)(srow + (el < send ? el : 0));
+      const int el = (slo + q) * 32 + 8 * g, at = el < send ? el : 0;
+      sw[q] = *(const uint4*)(w + at);
+      sa[q] = *(const uint4*)(srow + at);
     }
   }
 
   for (int i = tid; i < NPER * 64; i += kUpThreads) emask[i] = 0;
   __syncthreads();
-  const int ldx = up_stride(M::narrow ? p.D : 2 * p.D);
+  const int ldx = lds_stride(p.D);
   for (int tk = wave; tk < p.T; tk += kUpWaves) {
     // selection of token tk
     bool ok = lane < p.k;
@@ -307,6 +351,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
     if (ok) atomicOr(&emask[idx_l[tk * p.k + lane]], 1u << tk);
     // its row: bf16 as it is, or e4m3 codes with scale amax / 448 (1 for a zero row)
     const uint16_t* row = in + (int64_t)tk * p.D;
+    float inv = 1.f;
     if constexpr (M::narrow) {
       float m = 0.f;
       for (int c = lane * 8; c < p.D; c += 512) {
@@ -318,15 +363,15 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
       }
 #pragma unroll
       for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-      const float inv = m > 0.f ? 448.f / m : 1.f;
+      inv = m > 0.f ? 448.f / m : 1.f;
       if (lane == 0) row_scale[tk] = m > 0.f ? m / 448.f : 1.f;
-      for (int c = lane * 8; c < p.D; c += 512) {
-        const uint4 v = *(const uint4*)(row + c);
-        *(uint2*)(xl + tk * ldx + c) = make_uint2(codes4(v.x, v.y, inv), codes4(v.z, v.w, inv));
-      }
-    } else if constexpr (XLDS) {
-      for (int c = lane * 8; c < p.D; c += 512) *(uint4*)(xl + tk * ldx + 2 * c) = *(const uint4*)(row + c);
     }
+    if constexpr (XLDS)
+      for (int c = lane * 8; c < ldx / 2 - 8; c += 512) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (c < p.D) v = *(const uint4*)(row + c);
+        *(uint4*)(xl + tk * ldx + 2 * c) = M::narrow ? codes8(v, inv) : v;
+      }
   }
   __syncthreads();
   // touched experts, ascending
@@ -338,8 +383,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   int n_slots = 0;
 #pragma unroll
   for (int c = 0; c < NPER; ++c) {
-    const bool mine = c % kUpWaves == wave;
-    if (mine) {
+    if (c % kUpWaves == wave) {
       const bool on = emask[c * 64 + lane] != 0;
       const uint64_t any = __ballot(on);
       if (on) slot_l[n_slots + __popcll(any & ((1ull << lane) - 1))] = c * 64 + lane;
@@ -372,20 +416,15 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   for (int n = blockIdx.x; n < nsh; n += gridDim.x) {
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
     int from = slo;
-    if (n == (int)blockIdx.x) {
+    if (n == (int)blockIdx.x && slo < shi) {
 #pragma unroll
       for (int q = 0; q < kSharedSteps; ++q) {
-        const bool inside = (slo + q) * 32 + 8 * g < send;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8_t, inside ? sw[q] : zero),
-            __builtin_bit_cast(bf16x8_t, inside ? sa[q] : zero), acc, 0, 0, 0);
+        if ((slo + q) * 32 + 8 * g >= send) sw[q] = make_uint4(0, 0, 0, 0);
+        acc = mul(__builtin_bit_cast(bf16x8_t, sw[q]), sa[q], acc);
       }
       from = min(shi, slo + kSharedSteps);
     }
-    acc = dot_steps<Elt::BF16, 8>((const uint8_t*)(p.Ws_up + (int64_t)(16 * n + r) * p.H), nullptr,
-                                  p.H, from, shi, g,
-                                  [&](int el) { return *(const uint4*)(srow + el); }, acc);
+    acc = dot_rows<8, false>(p.Ws_up + (int64_t)(16 * n + r) * p.H, srow, srow, p.H, from, shi, g, acc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[wave][r][4 * g + i] = acc[i];
     __syncthreads();
@@ -398,17 +437,16 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
         for (int q = 1; q < kUpWaves; ++q) v[i] += part[q][r][4 * g + i];
         v[i] = sqrelu(v[i]);
       }
-      *(uint2*)(p.hs + (int64_t)r * p.Is + 16 * n + 4 * g) =
-          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      store_pair(p.hs, p.hs_lo, (int64_t)r * p.Is + 16 * n + 4 * g, v);
     }
     if (n + (int)gridDim.x < nsh) __syncthreads();
   }
 
-  // routed units: u = wave-slot, + waves of the grid
+  // routed units: wave-slot, + waves of the grid
   const int nb = p.I / 16, total = n_slots * nb, stride = gridDim.x * kUpWaves;
   int u = wave * gridDim.x + blockIdx.x;
   if (u >= total) return;
-  constexpr int U = F == Elt::BF16 ? 12 : 7;
+  constexpr int U = F == Elt::BF16 ? 12 : (F == Elt::MXFP4 ? 8 : 6);
   const int steps = cdiv(p.D, M::KS), nbat = cdiv(steps, U);
   struct Unit { const uint8_t *w, *wx; int slot, n0, e; };
   auto resolve = [&](int v) {
@@ -421,60 +459,37 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
     x.wx = M::mx ? (const uint8_t*)p.s_up + row * (p.D / 32) : nullptr;
     return x;
   };
-  auto issue = [&](const Unit& x, int b, uint4* wf, int* sc) {
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int k0 = (b * U + q) * M::KS;   // chunks past D: the row's start, zeroed when used
-#pragma unroll
-      for (int c = 0; c < M::CW; ++c) {
-        const int el = k0 + M::kw(c, g);
-        wf[q * M::CW + c] = *(const uint4*)(x.w + (int64_t)(el < p.D ? el : 0) * M::bits / 8);
-      }
-      if constexpr (M::mx) sc[q] = x.wx[min(k0 / 32 + g, p.D / 32 - 1)];
-      else sc[q] = 127;
-    }
-  };
   Unit cur = resolve(u), nxt = cur;
   bool more = u + stride < total;
   if (more) nxt = resolve(u + stride);
   int b = 0;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  auto step = [&](uint4* wc, int* sc, uint4* wn, int* sn) {
+  auto issue = [&](const Unit& x, int bb, WStep<F>* w) {
+#pragma unroll
+    for (int q = 0; q < U; ++q) load_step<F>(w[q], x.w, x.wx, bb * U + q, p.D, p.D, g);
+  };
+  auto step = [&](WStep<F>* wc, WStep<F>* wn) {
     const bool last = b + 1 == nbat;
-    const bool other = last && more;
     Unit src = cur;
-    if (other) src = nxt;
-    issue(src, last ? 0 : b + 1, wn, sn);
+    if (last && more) src = nxt;
+    issue(src, last ? 0 : b + 1, wn);   // always the same number of loads
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const int k0 = (b * U + q) * M::KS;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint4 wv[M::CW], av[M::CA];
+      mask_step<F>(wc[q], b * U + q, p.D, g);
 #pragma unroll
-      for (int c = 0; c < M::CW; ++c) wv[c] = k0 + M::kw(c, g) < p.D ? wc[q * M::CW + c] : zero;
-#pragma unroll
-      for (int c = 0; c < M::CA; ++c) {
-        const int el = k0 + M::ka(c, g);
-        const int at = el < p.D ? el : 0;
-        const uint4 v = M::narrow ? *(const uint4*)(xl + t * ldx + at)
-                        : XLDS    ? *(const uint4*)(xl + t * ldx + 2 * at)
-                                  : *(const uint4*)(in + (int64_t)t * p.D + at);
-        av[c] = el < p.D ? v : zero;
+      for (int j = 0; j < M::MF; ++j) {
+        const int el = min((b * U + q), steps - 1) * M::KS + M::k_of(j, g);
+        const uint4 a = XLDS ? *(const uint4*)(xl + t * ldx + 2 * el)
+                             : *(const uint4*)(in + (int64_t)t * p.D + (el < p.D ? el : 0));
+        acc = mul(wfrag<F>(wc[q], j), a, acc);
       }
-      if constexpr (!M::narrow)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[0]),
-                                                     __builtin_bit_cast(bf16x8_t, av[0]), acc, 0,
-                                                     0, 0);
-      else
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            cat(wv[0], M::CW == 2 ? wv[M::CW - 1] : zero), cat(av[0], av[M::CA - 1]), acc,
-            F == Elt::MXFP4 ? 4 : 0, 0, 0, sc[q], 0, 127);
     }
     if (!last) {
       ++b;
       return true;
     }
     const bool sel = (emask[cur.e] >> r) & 1;   // bits of tokens below T only
+    const int64_t at = ((int64_t)cur.slot * p.T + r) * p.I + cur.n0 + 4 * g;
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -486,10 +501,12 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
       v[i] = sqrelu(v[i]);
       acc[i] = 0.f;
     }
-    const uint32_t lo2 = pack_bf16x2(v[0], v[1]), hi2 = pack_bf16x2(v[2], v[3]);
-    if (sel)
-      *(uint2*)(p.h + ((int64_t)cur.slot * p.T + r) * p.I + cur.n0 + 4 * g) = make_uint2(lo2, hi2);
-    if constexpr (M::narrow) {  // the row's maximum (h >= 0: bf16 bits order as integers)
+    if constexpr (!M::narrow) {
+      if (sel) store_pair(p.h, p.h_lo, at, v);
+    } else {
+      const uint32_t lo2 = pack_bf16x2(v[0], v[1]), hi2 = pack_bf16x2(v[2], v[3]);
+      if (sel) *(uint2*)(p.h + at) = make_uint2(lo2, hi2);
+      // the row's maximum (h >= 0: bf16 bits order as integers)
       uint32_t m = max(max(lo2 << 16, lo2 & 0xFFFF0000u), max(hi2 << 16, hi2 & 0xFFFF0000u));
       m = max(m, (uint32_t)__shfl_xor((int)m, 16));
       m = max(m, (uint32_t)__shfl_xor((int)m, 32));
@@ -503,130 +520,219 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
     if (more) nxt = resolve(u + stride);
     return true;
   };
-  uint4 w0[U * M::CW], w1[U * M::CW];
-  int s0[U], s1[U];
-  issue(cur, 0, w0, s0);
+  WStep<F> w0[U], w1[U];
+  issue(cur, 0, w0);
   for (;;) {
-    if (!step(w0, s0, w1, s1)) break;
-    if (!step(w1, s1, w0, s0)) break;
+    if (!step(w0, w1)) break;
+    if (!step(w1, w0)) break;
   }
 }
 
 // ------------------------------------------------------------------------------- 3 down
 // Workgroup (n, part): 16 columns of y (or z) over a contiguous share of the list (slot, step) of
-// all touched experts, which its waves share evenly; the shared expert's steps likewise. Parts of
-// a column block are written to fp32 slabs, and the workgroup that ends last adds them in part
-// order (a counter that launch 1 cleared; nobody waits). 8- and 4-bit experts: the h rows of the
-// share are first turned into e4m3 codes in LDS, as many slots at a time as fit.
+// all touched experts, which its waves share evenly, double buffered across slots; the shared
+// expert's steps likewise, their loads issued first of all. Parts of a column block go to fp32
+// slabs, and the workgroup that ends last adds them in part order (a counter that launch 1
+// cleared; nobody waits). 8- and 4-bit experts: the h rows of the share are first turned into e4m3
+// codes (as bf16) in LDS, as many slots at a time as fit.
 constexpr int kDownWaves = 8;
 constexpr int kDownThreads = 64 * kDownWaves;
-constexpr int kDownRowsLds = 72 * 1024;
+constexpr int kDownRowsLds = 64 * 1024;
+constexpr int kDownShared = 5;   // steps of the shared expert in flight per wave
 
 template <Elt F>
-__global__ __launch_bounds__(kDownThreads) void few_down(FewParams p) {
+__global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap) {
   using M = Fmt<F>;
   __shared__ float part[kDownWaves][16][17];
-  __shared__ int first_row[1024 + 1];          // narrow: first code row of a slot of this pass
-  extern __shared__ __attribute__((aligned(16))) uint8_t hq[];  // narrow: code rows
+  __shared__ int first_row[1024];              // narrow: first code row of a slot of this pass
+  extern __shared__ __attribute__((aligned(16))) uint8_t hq[];  // narrow: cap code rows
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int t = min(r, p.T - 1);
   const int n0 = blockIdx.x * 16;
   const int parts = gridDim.y, mine = blockIdx.y;
-  const int n_slots = *p.n_slots;
-  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-  if (p.Is && !p.L) {
-    const int steps = cdiv(p.Is, 32), per = cdiv(steps, kDownWaves * parts);
-    const int lo = min(steps, (mine * kDownWaves + wave) * per), hi = min(steps, lo + per);
-    const uint16_t* row = p.hs + (int64_t)t * p.Is;
-    sum = dot_steps<Elt::BF16, 8>((const uint8_t*)(p.Ws_down + (int64_t)(n0 + r) * p.Is), nullptr,
-                                  p.Is, lo, hi, g,
-                                  [&](int el) { return *(const uint4*)(row + el); }, sum);
+
+  // the shared expert's first loads
+  const int nss = p.Is && !p.L ? cdiv(p.Is, 32) : 0, sper = cdiv(nss, kDownWaves * parts);
+  const int slo = min(nss, (mine * kDownWaves + wave) * sper), shi = min(nss, slo + sper);
+  const int send = min(p.Is, shi * 32);
+  uint4 sw[kDownShared];
+  const uint16_t* shrow = p.hs + (int64_t)t * p.Is;
+  const uint16_t* slrow = p.hs_lo + (int64_t)t * p.Is;
+  const uint16_t* swrow = p.Ws_down + (int64_t)(n0 + r) * p.Is;
+  if (slo < shi) {
+#pragma unroll
+    for (int q = 0; q < kDownShared; ++q) {
+      const int el = (slo + q) * 32 + 8 * g, at = el < send ? el : 0;
+      sw[q] = *(const uint4*)(swrow + at);
+    }
   }
+  const int n_slots = *p.n_slots;
   const int spe = cdiv(p.I, M::KS);      // steps per expert
   const int total = n_slots * spe, share = cdiv(total, parts);
   const int begin = min(total, mine * share), end = min(total, begin + share);
-  const int ldh = up_stride(p.I);
-
-  // steps [at, stop) of one wave
-  auto run = [&](int at, int stop, int pass_slot) {
-    while (at < stop) {
-      const int slot = at / spe, s0 = at - slot * spe, s1 = min(spe, s0 + stop - at);
-      at += s1 - s0;
-      const int e = p.slot_e[slot];
-      const uint32_t mask = p.slot_mask[slot];
-      const int64_t row = (int64_t)e * p.D + n0 + r;
-      const bool sel = (mask >> r) & 1;
-      float scale = p.gate_m[slot * TB + r];
-      // tokens that did not select the expert read another's row (their products are dropped)
-      const int src = sel ? r : __ffs(mask) - 1;
-      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-      const uint8_t* w = p.W_down + row * p.I * M::bits / 8;
-      const uint8_t* wx = M::mx ? (const uint8_t*)p.s_down + row * (p.I / 32) : nullptr;
-      if constexpr (M::narrow) {
-        const float m = __uint_as_float(p.hmax[slot * TB + src]);
-        scale *= m > 0.f ? m / 448.f : 1.f;
-        const uint8_t* q = hq + (first_row[slot - pass_slot] + __popc(mask & ((1u << src) - 1))) * ldh;
-        acc = dot_steps<F, 4>(w, wx, p.I, s0, s1, g,
-                              [&](int el) { return *(const uint4*)(q + el); }, acc);
-      } else {
-        const uint16_t* h = p.h + ((int64_t)slot * p.T + src) * p.I;
-        acc = dot_steps<F, 8>(w, wx, p.I, s0, s1, g,
-                              [&](int el) { return *(const uint4*)(h + el); }, acc);
-      }
+  const int ldh = lds_stride(p.I);
+  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+  auto shared_part = [&]() {
+    if (slo >= shi) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v = acc[i] * scale;
-        if constexpr (F == Elt::FP8)
-          v *= ((const float*)p.s_down)[(int64_t)e * p.D + n0 + 4 * g + i];
-        if (sel) sum[i] += v;
+    for (int q = 0; q < kDownShared; ++q) {
+      const int el = (slo + q) * 32 + 8 * g, at = el < send ? el : 0;
+      if (el >= send) sw[q] = make_uint4(0, 0, 0, 0);
+      sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), *(const uint4*)(shrow + at), sum);
+      sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), *(const uint4*)(slrow + at), sum);
+    }
+    sum = dot_rows<2, true>(swrow, shrow, slrow, p.Is, min(shi, slo + kDownShared), shi, g, sum);
+  };
+
+  // one wave's steps [at, stop), in batches of up to U steps of one slot
+  constexpr int U = F == Elt::BF16 ? 4 : (F == Elt::MXFP4 ? 4 : 3);
+  struct Pos {
+    int slot, s, s1;           // batch: steps s .. of the slot, which ends (here) at s1
+    const uint8_t *w, *wx;
+    const uint16_t *a, *a2;    // bf16: the token's h; narrow: a is its code row in LDS
+    float scale;
+    bool sel;
+    int row;                   // this lane's weight row
+  };
+  auto enter = [&](int at, int stop, int pass_slot) {   // the batch that starts at step `at`
+    Pos x;
+    x.slot = at / spe;
+    x.s = at - x.slot * spe;
+    x.s1 = min(spe, x.s + stop - at);
+    const int e = p.slot_e[x.slot];
+    const uint32_t mask = p.slot_mask[x.slot];
+    x.sel = (mask >> r) & 1;
+    // tokens that did not select the expert read another's row (their products are dropped)
+    const int src = x.sel ? r : __ffs(mask) - 1;
+    x.row = e * p.D + n0 + r;
+    x.w = p.W_down + (int64_t)x.row * p.I * M::bits / 8;
+    x.wx = M::mx ? (const uint8_t*)p.s_down + (int64_t)x.row * (p.I / 32) : nullptr;
+    x.scale = p.gate_m[x.slot * TB + r];
+    if constexpr (M::narrow) {
+      const float m = __uint_as_float(p.hmax[x.slot * TB + src]);
+      x.scale *= m > 0.f ? m / 448.f : 1.f;
+      x.a = (const uint16_t*)(hq + (first_row[x.slot - pass_slot] +
+                                    __popc(mask & ((1u << src) - 1))) * ldh);
+      x.a2 = nullptr;
+    } else {
+      x.a = p.h + ((int64_t)x.slot * p.T + src) * p.I;
+      x.a2 = p.h_lo + ((int64_t)x.slot * p.T + src) * p.I;
+    }
+    return x;
+  };
+  struct Batch {
+    WStep<F> w[U];
+    uint4 a[M::narrow ? 1 : U], b[M::narrow ? 1 : U];
+  };
+  auto issue = [&](const Pos& x, Batch& o) {
+    const int kend = min(p.I, x.s1 * M::KS);
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      load_step<F>(o.w[q], x.w, x.wx, x.s + q, kend, p.I, g);
+      if constexpr (!M::narrow) {
+        const int el = (x.s + q) * M::KS + M::k_of(0, g), at = el < kend ? el : 0;
+        o.a[q] = *(const uint4*)(x.a + at);
+        o.b[q] = *(const uint4*)(x.a2 + at);
       }
+    }
+  };
+  auto run = [&](int at, int stop, int pass_slot, bool first) {
+    if (at >= stop) {
+      if (first) shared_part();
+      return;
+    }
+    Pos cur = enter(at, stop, pass_slot);
+    Batch b0, b1;
+    issue(cur, b0);
+    if (first) shared_part();
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    auto step = [&](Batch& bc, Batch& bn) {
+      const int took = min(U, cur.s1 - cur.s);
+      at += took;
+      const bool slot_done = cur.s + took == cur.s1, done = at >= stop;
+      Pos nxt = cur;
+      if (!done && slot_done) nxt = enter(at, stop, pass_slot);
+      else if (!done) nxt.s = cur.s + took;
+      issue(nxt, bn);      // the last time: again, unused
+      const int kend = min(p.I, cur.s1 * M::KS);
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        mask_step<F>(bc.w[q], cur.s + q, kend, g);
+#pragma unroll
+        for (int j = 0; j < M::MF; ++j) {
+          const bf16x8_t w = wfrag<F>(bc.w[q], j);
+          if constexpr (M::narrow) {
+            const int el = min(cur.s + q, spe - 1) * M::KS + M::k_of(j, g);
+            acc = mul(w, *(const uint4*)(cur.a + el), acc);
+          } else {
+            acc = mul(w, bc.a[q], acc);
+            acc = mul(w, bc.b[q], acc);
+          }
+        }
+        // reads of later steps' codes stay behind (they would only add registers: at most 128, so
+        // that two workgroups fit a CU)
+        if constexpr (M::narrow) __builtin_amdgcn_sched_barrier(0);
+      }
+      if (slot_done) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = acc[i] * cur.scale;
+          if constexpr (F == Elt::FP8)
+            v *= ((const float*)p.s_down)[cur.row - r + 4 * g + i];
+          if (cur.sel) sum[i] += v;
+          acc[i] = 0.f;
+        }
+      }
+      cur = nxt;
+      return !done;
+    };
+    for (;;) {
+      if (!step(b0, b1)) break;
+      if (!step(b1, b0)) break;
     }
   };
   if constexpr (!M::narrow) {
     const int per = cdiv(end - begin, kDownWaves);
     const int lo = min(end, begin + wave * per);
-    run(lo, min(end, lo + per), 0);
+    run(lo, min(end, lo + per), 0, true);
   } else {
-    const int cap = kDownRowsLds / ldh;   // >= kFewTokens (checked by the launcher)
-    for (int at = begin; at < end;) {
-      // slots of this pass: as many as have room, at least one
-      const int slot0 = at / spe, slot_end = cdiv(end, spe);
-      __syncthreads();                    // the pass before is done with the code rows
-      if (wave == 0) {
-        int rows = 0, n = 0;
-        for (int s = slot0; s < slot_end; s += 64) {   // wave-wide prefix of the slots' row counts
-          const int c = s + lane < slot_end ? __popc(p.slot_mask[s + lane]) : 0;
-          int inc = c;
+    bool first = true;
+    for (int at = begin; at < end || first;) {
+      // slots of this pass: as many as have room (cap >= kFewTokens rows: at least one)
+      const int slot0 = at / spe, slot_end = at < end ? cdiv(end, spe) : slot0;
+      if (!first) __syncthreads();        // the pass before is done with the code rows
+      int rows = 0, n = 0;                // every wave: prefix of the slots' row counts
+      for (int s = slot0; s < slot_end; s += 64) {
+        const int c = s + lane < slot_end ? __popc(p.slot_mask[s + lane]) : 0;
+        int inc = c;
 #pragma unroll
-          for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(inc, o);
-            if (lane >= o) inc += v;
-          }
-          const bool fits = s + lane < slot_end && rows + inc <= cap;
-          if (fits) first_row[s - slot0 + lane] = rows + inc - c;
-          const int k = __popcll(__ballot(fits));
-          n += k;
-          rows += k ? __shfl(inc, k - 1) : 0;
-          if (k < 64) break;
+        for (int o = 1; o < 64; o <<= 1) {
+          const int v = __shfl_up(inc, o);
+          if (lane >= o) inc += v;
         }
-        if (lane == 0) part[0][0][16] = __int_as_float(n);
+        const bool fits = s + lane < slot_end && rows + inc <= cap;
+        if (fits && wave == 0) first_row[s - slot0 + lane] = rows + inc - c;
+        const int k = __popcll(__ballot(fits));
+        n += k;
+        rows += k ? __shfl(inc, k - 1) : 0;
+        if (k < 64) break;
       }
-      __syncthreads();
-      const int n = __float_as_int(part[0][0][16]);
+      n = __builtin_amdgcn_readfirstlane(n);
+      int j = 0;
       for (int s = slot0; s < slot0 + n; ++s) {
         const uint32_t mask = p.slot_mask[s];
-        int j = first_row[s - slot0];
         for (uint32_t m = mask; m; m &= m - 1, ++j) {   // rows dealt to the waves
           if (j % kDownWaves != wave) continue;
           const int tk = __ffs(m) - 1;
           const float top = __uint_as_float(p.hmax[s * TB + tk]);
           const float inv = top > 0.f ? 448.f / top : 1.f;
           const uint16_t* h = p.h + ((int64_t)s * p.T + tk) * p.I;
-          for (int c = lane * 8; c < p.I; c += 512) {
-            const uint4 v = *(const uint4*)(h + c);
-            *(uint2*)(hq + j * ldh + c) = make_uint2(codes4(v.x, v.y, inv), codes4(v.z, v.w, inv));
+          for (int c = lane * 8; c < ldh / 2 - 8; c += 512) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (c < p.I) v = *(const uint4*)(h + c);
+            *(uint4*)(hq + j * ldh + 2 * c) = codes8(v, inv);
           }
         }
       }
@@ -634,10 +740,10 @@ __global__ __launch_bounds__(kDownThreads) void few_down(FewParams p) {
       const int stop = min(end, (slot0 + n) * spe);
       const int per = cdiv(stop - at, kDownWaves);
       const int lo = min(stop, at + wave * per);
-      run(lo, min(stop, lo + per), slot0);
+      run(lo, min(stop, lo + per), slot0, first);
+      first = false;
       at = stop;
     }
-    __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) part[wave][r][4 * g + i] = sum[i];
@@ -655,30 +761,34 @@ __global__ __launch_bounds__(kDownThreads) void few_down(FewParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       __hip_atomic_store(slab + mine * 256 + i, v[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // the slab is written through to memory (agent scope); wait for that, then count
+    // the slab is written through to memory (agent scope); wait for that, then count (a release
+    // fence would write back the whole L2 instead: 18 us more on a Nano-shaped token)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     int before = 0;
     if (lane == 0)
       before = __hip_atomic_fetch_add(p.joined + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (__builtin_amdgcn_readfirstlane(before) != parts - 1) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = 0.f;
-      for (int q = 0; q < parts; ++q)
+    for (int i = 0; i < 4; ++i) v[i] = 0.f;
+    for (int q = 0; q < parts; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
         v[i] += __hip_atomic_load(slab + q * 256 + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
   }
-  uint16_t* out = p.L ? p.z : p.y;
-  if (r < p.T)
-    *(uint2*)(out + (int64_t)r * p.D + n0 + 4 * g) =
-        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  if (r < p.T) {
+    const int64_t at = (int64_t)r * p.D + n0 + 4 * g;
+    if (p.L)
+      store_pair(p.z, p.z_lo, at, v);
+    else
+      *(uint2*)(p.y + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
 }
 
 // -------------------------------------------------------------------------------- 4 out
 __global__ __launch_bounds__(512) void few_out(FewParams p) {
   __shared__ float part[8][16][17];
-  dense_unit<8, 8>(Dense{p.z, p.W_out, p.hs, p.Ws_down, p.L, p.Is, p.H, p.T, 0, p.y},
-                   16 * blockIdx.x, part);
+  dense_unit<8, 4, true>(Dense{p.z, p.z_lo, p.W_out, p.hs, p.hs_lo, p.Ws_down, p.L, p.Is, p.H, p.T,
+                               0, p.y, nullptr}, 16 * blockIdx.x, part);
 }
 
 template <Elt F, bool XLDS>
@@ -692,14 +802,11 @@ hipError_t run_up(const FewParams& p, int grid, size_t lds, hipStream_t s) {
 
 template <Elt F>
 hipError_t run_down(const FewParams& p, hipStream_t s) {
-  size_t lds = 0;
-  if (Fmt<F>::narrow) {
-    // room for every pair's code row, or as many as kDownRowsLds holds
-    const int64_t ldh = up_stride(p.I), rows = std::min<int64_t>((int64_t)p.T * p.k, kDownRowsLds / ldh);
-    if (rows < std::min(p.T * p.k, p.T)) return hipErrorInvalidValue;
-    lds = (size_t)(rows * ldh);
-  }
-  hipLaunchKernelGGL((few_down<F>), dim3(p.D / 16, few_parts(p.D)), dim3(kDownThreads), lds, s, p);
+  int rows = 0;
+  if (Fmt<F>::narrow)  // every pair's code row, or what kDownRowsLds holds, but a slot's at least
+    rows = std::min(p.T * p.k, std::max(kDownRowsLds / lds_stride(p.I), p.T));
+  hipLaunchKernelGGL((few_down<F>), dim3(p.D / 16, few_parts(p.D)), dim3(kDownThreads),
+                     (size_t)rows * lds_stride(p.I), s, p, rows);
   return hipGetLastError();
 }
 
@@ -723,14 +830,15 @@ hipError_t launch_few_up(const FewParams& p, hipStream_t s) {
   const int64_t units = (int64_t)few_slots(p.T, p.E, p.k) * (p.I / 16);
   const int64_t want = std::max<int64_t>(units, p.L ? 1 : p.Is / 16);
   const int grid = (int)std::min<int64_t>(256, want);
-  const size_t narrow = (size_t)p.T * up_stride(p.D), wide = (size_t)p.T * up_stride(2 * p.D);
+  const size_t lds = (size_t)p.T * lds_stride(p.D);
+  if (p.ex != Elt::BF16 && lds > kUpRowsLds) return hipErrorInvalidValue;
   switch (p.ex) {
     case Elt::BF16:
-      return wide <= kUpRowsLds ? run_up<Elt::BF16, true>(p, grid, wide, s)
-                                : run_up<Elt::BF16, false>(p, grid, 0, s);
-    case Elt::FP8: return run_up<Elt::FP8, true>(p, grid, narrow, s);
-    case Elt::MXFP4: return run_up<Elt::MXFP4, true>(p, grid, narrow, s);
-    case Elt::MXFP8: return run_up<Elt::MXFP8, true>(p, grid, narrow, s);
+      return lds <= kUpRowsLds ? run_up<Elt::BF16, true>(p, grid, lds, s)
+                               : run_up<Elt::BF16, false>(p, grid, 0, s);
+    case Elt::FP8: return run_up<Elt::FP8, true>(p, grid, lds, s);
+    case Elt::MXFP4: return run_up<Elt::MXFP4, true>(p, grid, lds, s);
+    case Elt::MXFP8: return run_up<Elt::MXFP8, true>(p, grid, lds, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -639,7 +639,7 @@ struct FewPlan {
   size_t logits = 0, score = 0, idx = 0, gates = 0, counts = 0, offsets = 0, perm = 0, pos = 0;
   size_t dscratch = 0, n_slots = 0, slot_e = 0, gate_m = 0, slot_mask = 0, hmax = 0;
   size_t slabs = 0, joined = 0;
-  size_t h = 0, hs = 0, u = 0, z = 0, total = 0;
+  size_t h = 0, h_lo = 0, hs = 0, hs_lo = 0, u = 0, z = 0, z_lo = 0, total = 0;
 };
 
 int32_t make_few_plan(const moe_desc_t* d, FewPlan* out) {
@@ -651,7 +651,8 @@ int32_t make_few_plan(const moe_desc_t* d, FewPlan* out) {
   if (d->flags & ~MOE_ROUTING_GIVEN) return MOE_ERR_INVALID_ARG;
   if (p.act != Elt::BF16 || p.T > kFewTokens) return MOE_ERR_UNSUPPORTED;
   const bool narrow = p.ex != Elt::BF16;
-  if (narrow && (int64_t)p.T * std::max(p.D, p.I) > kFewNarrowElts) return MOE_ERR_UNSUPPORTED;
+  if (narrow && (int64_t)p.T * ((std::max(p.D, p.I) + 127LL) / 128 * 128) > kFewNarrowElts)
+    return MOE_ERR_UNSUPPORTED;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -676,10 +677,15 @@ int32_t make_few_plan(const moe_desc_t* d, FewPlan* out) {
   f.slabs = take((size_t)p.D * few_parts(p.D) * kFewTokens * 4);
   f.joined = take((size_t)p.D / 16 * 4);
   f.h = take(S * T * (size_t)p.I * 2);
-  if (p.Is) f.hs = take(T * (size_t)p.Is * 2);
+  if (!narrow) f.h_lo = take(S * T * (size_t)p.I * 2);
+  if (p.Is) {
+    f.hs = take(T * (size_t)p.Is * 2);
+    f.hs_lo = take(T * (size_t)p.Is * 2);
+  }
   if (p.L) {
     f.u = take(T * (size_t)p.L * 2);
     f.z = take(T * (size_t)p.L * 2);
+    f.z_lo = take(T * (size_t)p.L * 2);
   }
   f.total = off;
   *out = f;
@@ -729,7 +735,10 @@ int32_t few_forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* 
   p.slabs = (float*)(base + f.slabs);
   p.joined = (int32_t*)(base + f.joined);
   p.h = (uint16_t*)(base + f.h);
+  p.h_lo = (uint16_t*)(base + f.h_lo);
   p.hs = pl.Is ? (uint16_t*)(base + f.hs) : nullptr;
+  p.hs_lo = pl.Is ? (uint16_t*)(base + f.hs_lo) : nullptr;
+  p.z_lo = pl.L ? (uint16_t*)(base + f.z_lo) : nullptr;
   p.u = pl.L ? (uint16_t*)(base + f.u) : nullptr;
   p.z = pl.L ? (uint16_t*)(base + f.z) : nullptr;
   {
