@@ -95,6 +95,9 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
   }
   // fp32 grouped launches: 16-row tiles when experts average at most 16 rows, else 64
   p.bm = p.act == Elt::F32 ? ((int64_t)p.T * p.k <= 16LL * p.E ? 16 : 64) : kGroupBM;
+#ifdef MX_SHAPE
+  if (mx_grouped) p.bm = MX_SHAPE;
+#endif
 
   const size_t ea = p.act == Elt::F32 ? 4 : 2;  // activation / intermediate element bytes
   size_t off = 0;
@@ -525,7 +528,7 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
         MOE_TRY(launch_quant_rows((const uint16_t*)xin, D, T, D, xq, sx, s));
       }
       MxGemmParams m;
-      m.offs = offsets; m.mt_start = mt_start; m.G = E;
+      m.offs = offsets; m.mt_start = mt_start; m.G = E; m.bm = pl.bm;
       m.A = xq; m.a_row = sx; m.a_rows = T; m.a_gather = perm;
       m.W = (const uint8_t*)w->W_up; m.w_mx = (const uint8_t*)w->s_up;
       m.C = h; m.M = P; m.N = I; m.K = D; m.sqrelu = 1;

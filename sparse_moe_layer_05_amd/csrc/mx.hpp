@@ -22,7 +22,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, Elt
 
 // C[m, n] = act( a_row[m] * sum_k A[m, k] W[n, k] ). A: MXFP4 or MXFP8 with block scales a_mx, or
 // FP8 (e4m3 codes with one fp32 scale a_row per source row). W: MXFP4 or MXFP8 with block scales
-// w_mx. Grouped launches (mt_start set) walk M-tiles of kGroupBM rows per group, as GemmParams.
+// w_mx. Grouped launches (mt_start set) walk M-tiles of bm rows per group, as GemmParams.
 struct MxGemmParams {
   const uint8_t* A = nullptr;        // [a_rows][K] elements, contiguous rows
   const uint8_t* a_mx = nullptr;     // [a_rows][K / 32]
@@ -36,8 +36,9 @@ struct MxGemmParams {
   int out_f32 = 0;                   // C element type: fp32, else bf16
   int sqrelu = 0;                    // C = relu(acc)^2
   const int32_t* offs = nullptr;     // grouped: [G + 1] row offsets
-  const int32_t* mt_start = nullptr; // grouped: [G + 1] prefix of ceil(rows_g / kGroupBM)
+  const int32_t* mt_start = nullptr; // grouped: [G + 1] prefix of ceil(rows_g / bm)
   int G = 0;
+  int bm = 0;                        // grouped: 64, 128 or 256
 };
 hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, hipStream_t s);
 

@@ -161,39 +161,57 @@ __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxGemmParams p) {
 // an instruction; the 16-byte chunks of a row are XOR-swizzled by choosing which global chunk a
 // lane fetches, so that 16 consecutive rows at one chunk index fall on distinct banks. Block
 // scales go through LDS too, 16 bytes (512 elements) of every row at a time, loaded one such
-// super-step ahead through registers: read directly by the lanes that need them, 5 scattered
-// dwords per K-step and wave would take as many address cycles as the operands.
+// super-step ahead through registers: read directly by the lanes that need them, scattered dwords
+// per K-step and wave would take as many address cycles as the operands. The first half of the
+// waves load the operands, the other half the scales: a wave's wait for its scales would wait for
+// its operand loads in flight too. All waves multiply.
 template <int SL> __device__ __forceinline__ int swz(int row) {
   return SL == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
 }
 template <int SL> __device__ __forceinline__ int slot(int row, int chunk) {
   return row * SL + ((chunk ^ swz<SL>(row)) << 4);
 }
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)(uint32_t)bytes, 0x00020000);
+// A raw buffer resource over [base, base + bytes) in scalar registers: accesses at offsets beyond
+// it are skipped.
+__device__ __forceinline__ i32x4_t rsrc(const void* base, int64_t bytes) {
+  const uint64_t b = (uint64_t)base;
+  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+                 __builtin_amdgcn_readfirstlane((int)((b >> 32) & 0xFFFF)),
+                 __builtin_amdgcn_readfirstlane((int)(uint32_t)bytes), 0x00020000};
+}
+// 16 bytes per lane from buffer offset voff + soff to LDS byte lds + 16 * lane. Written as an
+// instruction, not through the builtin: for every LDS read after the builtin the compiler waits
+// until all such loads have landed (it cannot tell the stages apart), which leaves one K-step in
+// flight however many stages there are. The load has no register result; its landing is awaited by
+// the explicit vmcnt waits of the main loop. The nop is the wait state between a write of m0 and a
+// load that uses it.
+__device__ __forceinline__ void dma16(i32x4_t r, uint32_t lds, uint32_t voff, int soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_of(const void* q) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)q;
 }
 
-// 16 block scales of a row from block b0 on; blocks past the row's nb read as 1 (code 127).
-// `left`: bytes of the array from the row's block b0 on.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* q, int64_t left, int valid) {
-  uint32_t v[4];
-  if (left >= 16) {
-    typedef uint32_t u32x4a1 __attribute__((ext_vector_type(4), aligned(1)));
-    const u32x4a1 x = *(const u32x4a1*)q;
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  } else {  // the array ends inside these 16 bytes
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = 0;
-    for (int b = 0; b < 16; ++b)
-      if (b < left) v[b >> 2] |= (uint32_t)q[b] << (8 * (b & 3));
-  }
+// The 16 bytes v shifted down by `by` bytes, and those from byte `valid` on set to 0x7F (scale 1).
+__device__ __forceinline__ uint4 trim_scales(uint4 v, int by, int valid) {
+  uint32_t w[8] = {v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+  const int d = by >> 2, b = 8 * (by & 3);
+  uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    uint32_t lo = w[j], hi = w[j + 1];
+#pragma unroll
+    for (int q = 1; q < 4; ++q) {
+      lo = d == q ? w[j + q] : lo;
+      hi = d == q ? w[j + q + 1] : hi;
+    }
+    o[j] = (uint32_t)((((uint64_t)hi << 32) | lo) >> b);
     const int n = min(max(valid - 4 * j, 0), 4);
     const uint32_t keep = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
-    v[j] = (v[j] & keep) | (0x7F7F7F7Fu & ~keep);
+    o[j] = (o[j] & keep) | (0x7F7F7F7Fu & ~keep);
   }
-  return make_uint4(v[0], v[1], v[2], v[3]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Logical tile L -> group, first row, rows, first column: bands of 8 M-tiles, M fastest inside.
@@ -231,20 +249,19 @@ __device__ __forceinline__ bool tile_of(const MxGemmParams& p, int L, int& g, in
 }
 
 template <int BM, int BN, int WGM, int WGN, int NS, int FA, int FW>
-__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(2)))
-void mx_tile_kernel(MxGemmParams p) {
-  constexpr int NW = WGM * WGN, NT = 64 * NW;
+__global__ __launch_bounds__(64 * WGM * WGN, 2) void mx_tile_kernel(MxGemmParams p) {
+  constexpr int NW = WGM * WGN, DW = NW / 2;                // waves, waves that load operands
   constexpr int SA = kBits<FA> * 16, SW = kBits<FW> * 16;   // bytes of a row's K-step
   constexpr int WM = BM / WGM, WN = BN / WGN, MB = WM / 32, NB = WN / 32;
   constexpr int RA = 1024 / SA, RW = 1024 / SW;             // rows per 1-KB load
   constexpr int LA = SA / 16, LW = SW / 16;                 // lanes per row
-  constexpr int GA = BM / (RA * NW), GW = BN / (RW * NW);   // 1-KB loads per wave
+  constexpr int GA = BM / (RA * DW), GW = BN / (RW * DW);   // 1-KB loads per loading wave
   constexpr int STAGE = BM * SA + BN * SW;
   constexpr int SROWS = (FA == kE4Row ? 0 : BM) + BN;       // rows whose scales are staged
-  constexpr int SR = (SROWS + NT - 1) / NT;
+  constexpr int ST = 64 * (NW - DW), SR = (SROWS + ST - 1) / ST;
   constexpr int EPW = WN + 4;
-  static_assert(GA >= 1 && GW >= 1 && BM % (RA * NW) == 0 && BN % (RW * NW) == 0, "1-KB loads");
-  static_assert(WM % 32 == 0 && WN % 32 == 0 && NW % 2 == 0 && NS >= 2, "tile shape");
+  static_assert(GA >= 1 && GW >= 1 && BM % (RA * DW) == 0 && BN % (RW * DW) == 0, "1-KB loads");
+  static_assert(WM % 32 == 0 && WN % 32 == 0 && DW % 2 == 0 && NS >= 2, "tile shape");
   static_assert(NW * 16 * EPW * 4 <= NS * STAGE, "epilogue strips fit in the stages");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE];
   __shared__ __attribute__((aligned(16))) uint4 sc[2][SROWS];
@@ -254,83 +271,95 @@ void mx_tile_kernel(MxGemmParams p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WGN, wn = wave % WGN, lg = lane >> 5, lr = lane & 31;
+  const bool loads = wave < DW;
   const int kba = p.K * kBits<FA> / 8, kbw = p.K * kBits<FW> / 8;   // bytes of a row
   const int nb = p.K / kMxBlockElts, nk = cdiv(p.K, 128);
   const int tail_a = kba % SA, tail_w = kbw % SW;   // bytes of a partial last K-step
 
-  const uint8_t* Wg = p.W + (int64_t)g * p.N * kbw;
-  const __amdgpu_buffer_rsrc_t ra = rsrc(p.A, (int64_t)p.a_rows * kba);
-  const __amdgpu_buffer_rsrc_t rw = rsrc(Wg, (int64_t)p.N * kbw);
+  const i32x4_t ra = rsrc(p.A, (int64_t)p.a_rows * kba);
+  const i32x4_t rw = rsrc(p.W + (int64_t)g * p.N * kbw, (int64_t)p.N * kbw);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_of(smem)) + wave * 1024;
   const int ca = ((lane % LA) ^ swz<SA>(wave * RA + lane / LA)) << 4;
   const int cw = ((lane % LW) ^ swz<SW>(wave * RW + lane / LW)) << 4;
   constexpr uint32_t kOut = 0xFFFFFFF0u;   // an offset past every buffer: the load is skipped
   uint32_t oa[GA], ow[GW];
+  if (loads) {
 #pragma unroll
-  for (int i = 0; i < GA; ++i) {
-    const int r = (wave + NW * i) * RA + lane / LA;
-    const int src = r < rows ? (p.a_gather ? p.a_gather[row0 + r] : row0 + r) : 0;
-    oa[i] = r < rows ? (uint32_t)src * (uint32_t)kba + ca : kOut;
-  }
-#pragma unroll
-  for (int i = 0; i < GW; ++i)
-    ow[i] = (uint32_t)min(n0 + (wave + NW * i) * RW + lane / LW, p.N - 1) * (uint32_t)kbw + cw;
-
-  auto issue = [&](int ks, uint8_t* st) {
-    const bool last = ks == nk - 1;
-    const bool la = !(last && tail_a) || ca < tail_a, lw = !(last && tail_w) || cw < tail_w;
-#pragma unroll
-    for (int i = 0; i < GA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          ra, (__attribute__((address_space(3))) void*)(st + (wave + NW * i) * 1024), 16,
-          (int)(la ? oa[i] : kOut), ks * SA, 0, 0);
+    for (int i = 0; i < GA; ++i) {
+      const int r = (wave + DW * i) * RA + lane / LA;
+      const int src = r < rows ? (p.a_gather ? p.a_gather[row0 + r] : row0 + r) : 0;
+      oa[i] = r < rows ? (uint32_t)src * (uint32_t)kba + ca : kOut;
+    }
 #pragma unroll
     for (int i = 0; i < GW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rw, (__attribute__((address_space(3))) void*)(st + BM * SA + (wave + NW * i) * 1024), 16,
-          (int)(lw ? ow[i] : kOut), ks * SW, 0, 0);
+      ow[i] = (uint32_t)min(n0 + (wave + DW * i) * RW + lane / LW, p.N - 1) * (uint32_t)kbw + cw;
+  }
+
+  auto issue = [&](int ks, int stage) {
+    if (!loads) return;
+    const bool last = ks == nk - 1;
+    const bool la = !(last && tail_a) || ca < tail_a, lw = !(last && tail_w) || cw < tail_w;
+    const uint32_t st = lds0 + stage * STAGE;
+#pragma unroll
+    for (int i = 0; i < GA; ++i) dma16(ra, st + DW * i * 1024, la ? oa[i] : kOut, ks * SA);
+#pragma unroll
+    for (int i = 0; i < GW; ++i)
+      dma16(rw, st + BM * SA + DW * i * 1024, lw ? ow[i] : kOut, ks * SW);
   };
   auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
   // the chunks of a partial last K-step that lie past K, zeroed once the stage has landed
   auto fix_tail = [&](uint8_t* st) {
-    if (tail_a && ca >= tail_a)
+    if (loads) {
+      if (tail_a && ca >= tail_a)
 #pragma unroll
-      for (int i = 0; i < GA; ++i) *(uint4*)(st + (wave + NW * i) * 1024 + lane * 16) = kZero4;
-    if (tail_w && cw >= tail_w)
+        for (int i = 0; i < GA; ++i) *(uint4*)(st + (wave + DW * i) * 1024 + lane * 16) = kZero4;
+      if (tail_w && cw >= tail_w)
 #pragma unroll
-      for (int i = 0; i < GW; ++i)
-        *(uint4*)(st + BM * SA + (wave + NW * i) * 1024 + lane * 16) = kZero4;
+        for (int i = 0; i < GW; ++i)
+          *(uint4*)(st + BM * SA + (wave + DW * i) * 1024 + lane * 16) = kZero4;
+    }
     barrier();
   };
 
-  // scales: thread t carries rows t, t + NT, ... of (A rows, W rows)
+  // scales: thread t of the other waves carries rows t, t + ST, ... of (A rows, W rows). A row's
+  // 16 bytes are loaded from where they start, or from the array's last 16 (the array is longer
+  // than that) and moved down.
+  const int st0 = tid - 64 * DW;
   const uint8_t* sp[SR];
-  int64_t sleft[SR];
+  int64_t sleft[SR];   // bytes of the array from the row's first scale on
+  uint4 sv[SR];
+  if (!loads) {
 #pragma unroll
-  for (int i = 0; i < SR; ++i) {
-    const int r = tid + NT * i;
-    sp[i] = nullptr;
-    sleft[i] = 0;
-    if (FA != kE4Row && r < BM) {
-      const int rr = min(r, rows - 1);
-      const int64_t src = p.a_gather ? p.a_gather[row0 + rr] : row0 + rr;
-      sp[i] = p.a_mx + src * nb;
-      sleft[i] = ((int64_t)p.a_rows - src) * nb;
-    } else if (r < SROWS) {
-      const int64_t n = min(n0 + r - (SROWS - BN), p.N - 1);
-      sp[i] = p.w_mx + ((int64_t)g * p.N + n) * nb;
-      sleft[i] = ((int64_t)(p.mt_start ? p.G - g : 1) * p.N - n) * nb;
+    for (int i = 0; i < SR; ++i) {
+      const int r = min(st0 + ST * i, SROWS - 1);
+      if (FA != kE4Row && r < BM) {
+        const int rr = min(r, rows - 1);
+        const int64_t src = p.a_gather ? p.a_gather[row0 + rr] : row0 + rr;
+        sp[i] = p.a_mx + src * nb;
+        sleft[i] = ((int64_t)p.a_rows - src) * nb;
+      } else {
+        const int64_t n = min(n0 + r - (SROWS - BN), p.N - 1);
+        sp[i] = p.w_mx + ((int64_t)g * p.N + n) * nb;
+        sleft[i] = ((int64_t)(p.mt_start ? p.G - g : 1) * p.N - n) * nb;
+      }
     }
   }
-  uint4 sv[SR];
   auto fetch_scales = [&](int ss) {
+    if (loads) return;
 #pragma unroll
-    for (int i = 0; i < SR; ++i)
-      if (tid + NT * i < SROWS) sv[i] = load_scales(sp[i] + 16 * ss, sleft[i] - 16 * ss, nb - 16 * ss);
+    for (int i = 0; i < SR; ++i) {
+      typedef uint32_t u32x4a1 __attribute__((ext_vector_type(4), aligned(1)));
+      const u32x4a1 x = *(const u32x4a1*)(sp[i] + min((int64_t)16 * ss, sleft[i] - 16));
+      sv[i] = make_uint4(x.x, x.y, x.z, x.w);
+    }
   };
-  auto put_scales = [&](int buf) {
+  auto put_scales = [&](int ss) {
+    if (loads) return;
 #pragma unroll
     for (int i = 0; i < SR; ++i)
-      if (tid + NT * i < SROWS) sc[buf][tid + NT * i] = sv[i];
+      if (st0 + ST * i < SROWS)
+        sc[ss & 1][st0 + ST * i] =
+            trim_scales(sv[i], (int)max((int64_t)0, 16 * ss + 16 - sleft[i]), nb - 16 * ss);
   };
 
   f32x16_t acc[MB][NB];
@@ -383,7 +412,7 @@ void mx_tile_kernel(MxGemmParams p) {
   // at most the loads of the stages after ks are outstanding, then the barrier publishes the
   // stage (and the scales of the super-step) and frees the stage before.
   constexpr int PER = GA + GW;
-  static_assert((NS - 2) * PER < 64, "vmcnt range");
+  static_assert((NS - 1) * PER < 64, "vmcnt range");
   auto wait_ahead = [&](int ahead) {
 #define MOE_VMCNT(n) __builtin_amdgcn_s_waitcnt((((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8)))
     if constexpr (NS >= 4) { if (ahead >= 2) { MOE_VMCNT(2 * PER); return; } }
@@ -394,24 +423,27 @@ void mx_tile_kernel(MxGemmParams p) {
   fetch_scales(0);
 #pragma unroll
   for (int q = 0; q < NS - 1; ++q)
-    if (q < nk) issue(q, smem + q * STAGE);
+    if (q < nk) issue(q, q);
   put_scales(0);
   const int nss = cdiv(nk, 4);
+  int cur = 0, ahead = NS - 1;   // stages of K-step ks and of the one issued next
   for (int ss = 0; ss < nss; ++ss) {
+    if (ss + 1 < nss) fetch_scales(ss + 1);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int ks = 4 * ss + q;
       if (ks >= nk) break;
       wait_ahead(min(NS - 2, nk - 1 - ks));
       barrier();
-      uint8_t* cur = smem + (ks % NS) * STAGE;
-      if (ks == nk - 1 && (tail_a || tail_w)) fix_tail(cur);
-      if (ks + NS - 1 < nk) issue(ks + NS - 1, smem + ((ks + NS - 1) % NS) * STAGE);
-      if (q == 0 && ss + 1 < nss) fetch_scales(ss + 1);
-      compute(cur, ss & 1, q);
+      uint8_t* st = smem + cur * STAGE;
+      if (ks == nk - 1 && (tail_a || tail_w)) fix_tail(st);
+      if (ks + NS - 1 < nk) issue(ks + NS - 1, ahead);
+      compute(st, ss & 1, q);
+      cur = cur + 1 == NS ? 0 : cur + 1;
+      ahead = ahead + 1 == NS ? 0 : ahead + 1;
     }
     // the other buffer was last read a whole super-step ago
-    if (ss + 1 < nss) put_scales((ss + 1) & 1);
+    if (ss + 1 < nss) put_scales(ss + 1);
   }
   barrier();   // every wave is done with the stages: the epilogue reuses them
 
@@ -461,6 +493,24 @@ hipError_t run_tile(const MxGemmParams& p, int mtiles, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tile shapes, largest first: 8 waves and one workgroup per CU, or 4 waves and two. A K-step's loads
+// take over a microsecond to land, so as many stages as LDS holds are in flight.
+template <int FA, int FW>
+constexpr int stages(int BM, int BN, int lds) {
+  const int stage = (BM * kBits<FA> + BN * kBits<FW>) * 16;
+  const int n = (lds - 32 * ((FA == kE4Row ? 0 : BM) + BN)) / stage;
+  return n > 4 ? 4 : n;
+}
+template <int FA, int FW>
+hipError_t run_shape(const MxGemmParams& p, int shape, int mtiles, hipStream_t s) {
+  constexpr int kLds = 160 * 1024;
+  switch (shape) {
+    case 256: return run_tile<256, 256, 2, 4, stages<FA, FW>(256, 256, kLds), FA, FW>(p, mtiles, s);
+    case 128: return run_tile<128, 256, 2, 4, stages<FA, FW>(128, 256, kLds), FA, FW>(p, mtiles, s);
+    default: return run_tile<64, 128, 2, 2, stages<FA, FW>(64, 128, kLds / 2), FA, FW>(p, mtiles, s);
+  }
+}
+
 template <int FA, int FW>
 hipError_t run_dense(const MxGemmParams& p, hipStream_t s) {
   if (p.M <= 16) {
@@ -474,7 +524,12 @@ hipError_t run_dense(const MxGemmParams& p, hipStream_t s) {
     else hipLaunchKernelGGL((mx_rows_kernel<FA, FW, 4, 8>), grid, dim3(512), 0, s, p);
     return hipGetLastError();
   }
-  return run_tile<128, 192, 2, 2, 2, FA, FW>(p, cdiv(p.M, 128), s);
+#ifdef MX_SHAPE
+  const int shape = MX_SHAPE;
+#else
+  const int shape = 128;
+#endif
+  return run_shape<FA, FW>(p, shape, cdiv(p.M, shape), s);
 }
 
 }  // namespace mx_tiles
@@ -493,8 +548,9 @@ hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, h
   const bool w4 = w == Elt::MXFP4;
   if (p.mt_start) {  // grouped: e4m3 rows with a row scale against block-scaled experts
     if (a != Elt::FP8 || !p.a_row || !p.offs) return hipErrorInvalidValue;
-    return w4 ? run_tile<kGroupBM, 192, 2, 2, 2, kE4Row, kE2>(p, max_mtiles, s)
-              : run_tile<kGroupBM, 192, 2, 2, 2, kE4Row, kE4>(p, max_mtiles, s);
+    if (p.bm != 64 && p.bm != 128 && p.bm != 256) return hipErrorInvalidValue;
+    return w4 ? run_shape<kE4Row, kE2>(p, p.bm, max_mtiles, s)
+              : run_shape<kE4Row, kE4>(p, p.bm, max_mtiles, s);
   }
   if (p.M <= 0) return hipSuccess;
   if (!p.a_mx || p.a_gather || p.a_rows != p.M) return hipErrorInvalidValue;

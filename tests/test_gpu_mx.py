@@ -239,10 +239,12 @@ def test_layer_with_block_scaled_experts_on_tiles(name):
     cfg = LAYERS[name]
     inp = mi.make_layer(cfg, seed=2)
     y, rt = layer_out(inp, "grouped_mx")
-    g = O.gates_for(O.logits(inp), rt["idx"])
-    ref = O.forward_tokens(inp, rt["idx"], g, np.arange(cfg.T), True)
-    print(f"[gpu] grouped_mx {name}: {rel(y, ref):.2e}", flush=True)
-    assert rel(y, ref) <= 5e-3
+    t = np.arange(0, cfg.T, 1 + cfg.T // 100)
+    t = np.union1d(t, np.arange(cfg.T - 3, cfg.T).clip(0))      # the oracle is one thread
+    g = O.gates_for(O.logits(inp, t), rt["idx"][t])
+    ref = O.forward_tokens(inp, rt["idx"][t], g, t, True)
+    print(f"[gpu] grouped_mx {name}: {rel(y[t], ref):.2e}", flush=True)
+    assert rel(y[t], ref) <= 5e-3
     # the decode path on the same selection: the same quantised rows, other summation orders and
     # one more rounding of the experts' rows here
     z, _ = layer_out(inp, "stream", given=(rt["idx"], rt["gates"]))
