@@ -95,9 +95,7 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
   }
   // fp32 grouped launches: 16-row tiles when experts average at most 16 rows, else 64
   p.bm = p.act == Elt::F32 ? ((int64_t)p.T * p.k <= 16LL * p.E ? 16 : 64) : kGroupBM;
-#ifdef MX_SHAPE
-  if (mx_grouped) p.bm = MX_SHAPE;
-#endif
+  if (mx_grouped) p.bm = mx_group_bm(p.P, p.E);
 
   const size_t ea = p.act == Elt::F32 ? 4 : 2;  // activation / intermediate element bytes
   size_t off = 0;

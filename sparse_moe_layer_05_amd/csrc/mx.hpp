@@ -38,8 +38,12 @@ struct MxGemmParams {
   const int32_t* offs = nullptr;     // grouped: [G + 1] row offsets
   const int32_t* mt_start = nullptr; // grouped: [G + 1] prefix of ceil(rows_g / bm)
   int G = 0;
-  int bm = 0;                        // grouped: 64, 128 or 256
+  int bm = 0;                        // grouped: 64 or 128 (mx_group_bm)
 };
+// Rows of the grouped launches' M-tiles. Tiles of 64 rows where experts hold at most 96 on average
+// (every expert's last tile is partly empty): LatentMoE, 47 rows an expert, 308 us per layer
+// against 317 on 128; Nano, 384 rows, 1480 against 1261.
+inline int mx_group_bm(int P, int E) { return P <= 96 * (int64_t)E ? 64 : 128; }
 hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, hipStream_t s);
 
 }  // namespace moe

@@ -89,39 +89,40 @@ __global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxGemmParams p) {
   f32x4_t acc[TB];
 #pragma unroll
   for (int t = 0; t < TB; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // Chunks past this wave's share are read from the row's start and zeroed on the weights' side;
+  // no branch on them: loads whose use is conditional are moved to it, one by one, instead of
+  // being in flight together.
+  const int kend = min(p.K, k_hi * 128);
+  auto el_of = [&](int ks, int c, int chunks) {
+    return ks * 128 + (chunks == 2 ? 64 * c + 16 * g : 32 * g);
+  };
   for (int k0 = k_lo; k0 < k_hi; k0 += U) {
     uint4 wf[U][CW], af[U][TB][CA];
     int ws[U], as[U][TB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int ks = min(k0 + u, k_hi - 1);   // steps past the share re-read its last (unused)
-      // a chunk past K is read from the row's last one and zeroed; a scale past K from its last
-      auto at = [&](int bits, int c, int chunks) {
-        const int64_t el = (int64_t)ks * 128 + (chunks == 2 ? 64 * c + 16 * g : 32 * g);
-        return el < p.K ? el * bits / 8 : (int64_t)-1;
-      };
-      const int blk = min(ks * 4 + g, nb - 1);
+      const int blk = min((k0 + u) * 4 + g, nb - 1);
 #pragma unroll
       for (int c = 0; c < CW; ++c) {
-        const int64_t o = at(kBits<FW>, c, CW);
-        wf[u][c] = *(const uint4*)(w + (o < 0 ? kbw - 16 : o));
-        if (o < 0) wf[u][c] = kZero4;
+        const int el = el_of(k0 + u, c, CW);
+        wf[u][c] = *(const uint4*)(w + (int64_t)(el < kend ? el : 0) * kBits<FW> / 8);
       }
       ws[u] = wx[blk];
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
 #pragma unroll
         for (int c = 0; c < CA; ++c) {
-          const int64_t o = at(kBits<FA>, c, CA);
-          af[u][t][c] = *(const uint4*)(a[t] + (o < 0 ? kba - 16 : o));
-          if (o < 0) af[u][t][c] = kZero4;
+          const int el = el_of(k0 + u, c, CA);
+          af[u][t][c] = *(const uint4*)(a[t] + (int64_t)(el < kend ? el : 0) * kBits<FA> / 8);
         }
         as[u][t] = ax[t][blk];
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (k0 + u >= k_hi) break;
+#pragma unroll
+      for (int c = 0; c < CW; ++c)
+        if (el_of(k0 + u, c, CW) >= kend) wf[u][c] = kZero4;
 #pragma unroll
       for (int t = 0; t < TB; ++t)
         acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -249,7 +250,8 @@ __device__ __forceinline__ bool tile_of(const MxGemmParams& p, int L, int& g, in
 }
 
 template <int BM, int BN, int WGM, int WGN, int NS, int FA, int FW>
-__global__ __launch_bounds__(64 * WGM * WGN, 2) void mx_tile_kernel(MxGemmParams p) {
+__global__ __launch_bounds__(64 * WGM * WGN, 2)
+void mx_tile_kernel(MxGemmParams p) {
   constexpr int NW = WGM * WGN, DW = NW / 2;                // waves, waves that load operands
   constexpr int SA = kBits<FA> * 16, SW = kBits<FW> * 16;   // bytes of a row's K-step
   constexpr int WM = BM / WGM, WN = BN / WGN, MB = WM / 32, NB = WN / 32;
@@ -493,43 +495,68 @@ hipError_t run_tile(const MxGemmParams& p, int mtiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tile shapes, largest first: 8 waves and one workgroup per CU, or 4 waves and two. A K-step's loads
-// take over a microsecond to land, so as many stages as LDS holds are in flight.
+// Tile shapes by their BM: 256 x 256 on 8 waves, one workgroup per CU; 128 x 256 (128 x 128 where
+// W has 8 bits) and 64 x 128 on 4 waves, two per CU. A K-step's loads take over a microsecond to
+// land, so as many stages as LDS holds are in flight.
 template <int FA, int FW>
 constexpr int stages(int BM, int BN, int lds) {
   const int stage = (BM * kBits<FA> + BN * kBits<FW>) * 16;
   const int n = (lds - 32 * ((FA == kE4Row ? 0 : BM) + BN)) / stage;
   return n > 4 ? 4 : n;
 }
-template <int FA, int FW>
-hipError_t run_shape(const MxGemmParams& p, int shape, int mtiles, hipStream_t s) {
-  constexpr int kLds = 160 * 1024;
-  switch (shape) {
-    case 256: return run_tile<256, 256, 2, 4, stages<FA, FW>(256, 256, kLds), FA, FW>(p, mtiles, s);
-    case 128: return run_tile<128, 256, 2, 4, stages<FA, FW>(128, 256, kLds), FA, FW>(p, mtiles, s);
-    default: return run_tile<64, 128, 2, 2, stages<FA, FW>(64, 128, kLds / 2), FA, FW>(p, mtiles, s);
-  }
+constexpr int kLds = 160 * 1024;
+constexpr int tile_bn(int bm, int w_bits) { return bm == 256 ? 256 : (bm == 128 && w_bits == 4 ? 256 : 128); }
+template <int FA, int FW, int BM>
+hipError_t run_shape(const MxGemmParams& p, int mtiles, hipStream_t s) {
+  constexpr int BN = tile_bn(BM, kBits<FW>);
+  constexpr int NS = stages<FA, FW>(BM, BN, BM == 256 ? kLds : kLds / 2);
+  return run_tile<BM, BN, 2, BM == 256 ? 4 : 2, NS, FA, FW>(p, mtiles, s);
+}
+
+template <int FA, int FW, int TB>
+hipError_t run_rows(const MxGemmParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((mx_rows_kernel<FA, FW, TB, 8>), dim3(p.N / 16, cdiv(p.M, 16 * TB)), dim3(512),
+                     0, s, p);
+  return hipGetLastError();
+}
+
+// Estimated microseconds of a dense product on tiles of BM rows: rounds over the CUs of K-steps
+// and a fixed part (first loads and epilogue). Measured on 4096 x 4096 outputs, K of 512 to 4096:
+// 1.1 / 1.37 / 0.57 us per K-step and 8 / 7 / 3 us fixed; a CU that holds one workgroup of the
+// smaller shapes instead of two takes about 0.55 of their step. 8192 x 3712 x 2688 (4 bits): 67 us
+// on 256 rows, 69 on 128, 116 on 64; 512 x 3712 x 2688: 27, 21.5 and 14.
+double tile_time(int bm, int w_bits, int M, int N, int K) {
+  const int tiles = cdiv(M, bm) * cdiv(N, tile_bn(bm, w_bits)), cap = bm == 256 ? 256 : 512;
+  const double c = bm == 256 ? 1.1 : (bm == 128 ? 1.37 : 0.57) * (tiles <= 256 ? 0.55 : 1.0);
+  return cdiv(tiles, cap) * (cdiv(K, 128) * c + (bm == 256 ? 8 : bm == 128 ? 7 : 3));
 }
 
 template <int FA, int FW>
 hipError_t run_dense(const MxGemmParams& p, hipStream_t s) {
-  if (p.M <= 16) {
-    hipLaunchKernelGGL((mx_rows_kernel<FA, FW, 1, 8>), dim3(p.N / 16), dim3(512), 0, s, p);
-    return hipGetLastError();
+  if (p.M <= 16) return run_rows<FA, FW, 1>(p, s);
+  if (p.M <= 32) return run_rows<FA, FW, 2>(p, s);
+  // Few rows: every 16 weight rows meet 64 rows of A, which re-read each other's operands from L2
+  // (about 10 TB/s over the chip) but fill it where tiles would leave CUs idle.
+  const double re_read = (double)cdiv(p.M, 64) * (p.N / 16) * p.K * (64 * kBits<FA> + 16 * kBits<FW>) / 8;
+  double best_t = p.M <= 512 ? 4 + re_read / 10e6 : 1e30;
+  int best = 0;
+  for (int bm = 64; bm <= 256; bm *= 2) {
+    const double t = tile_time(bm, kBits<FW>, p.M, p.N, p.K);
+    if (p.M > 64 && t < best_t) { best_t = t; best = bm; }
   }
-  if (p.M <= 128) {
-    const int tb = p.M <= 32 ? 2 : 4;
-    const dim3 grid(p.N / 16, cdiv(p.M, 16 * tb));
-    if (tb == 2) hipLaunchKernelGGL((mx_rows_kernel<FA, FW, 2, 8>), grid, dim3(512), 0, s, p);
-    else hipLaunchKernelGGL((mx_rows_kernel<FA, FW, 4, 8>), grid, dim3(512), 0, s, p);
-    return hipGetLastError();
+  switch (best) {
+    case 256: return run_shape<FA, FW, 256>(p, cdiv(p.M, 256), s);
+    case 128: return run_shape<FA, FW, 128>(p, cdiv(p.M, 128), s);
+    case 64: return run_shape<FA, FW, 64>(p, cdiv(p.M, 64), s);
+    default: return run_rows<FA, FW, 4>(p, s);
   }
-#ifdef MX_SHAPE
-  const int shape = MX_SHAPE;
-#else
-  const int shape = 128;
-#endif
-  return run_shape<FA, FW>(p, shape, cdiv(p.M, shape), s);
+}
+
+template <int FW>
+hipError_t run_grouped(const MxGemmParams& p, int mtiles, hipStream_t s) {
+  if (p.bm == 64) return run_shape<kE4Row, FW, 64>(p, mtiles, s);
+  if (p.bm == 128) return run_shape<kE4Row, FW, 128>(p, mtiles, s);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace mx_tiles
@@ -548,9 +575,7 @@ hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, h
   const bool w4 = w == Elt::MXFP4;
   if (p.mt_start) {  // grouped: e4m3 rows with a row scale against block-scaled experts
     if (a != Elt::FP8 || !p.a_row || !p.offs) return hipErrorInvalidValue;
-    if (p.bm != 64 && p.bm != 128 && p.bm != 256) return hipErrorInvalidValue;
-    return w4 ? run_shape<kE4Row, kE2>(p, p.bm, max_mtiles, s)
-              : run_shape<kE4Row, kE4>(p, p.bm, max_mtiles, s);
+    return w4 ? run_grouped<kE2>(p, max_mtiles, s) : run_grouped<kE4>(p, max_mtiles, s);
   }
   if (p.M <= 0) return hipSuccess;
   if (!p.a_mx || p.a_gather || p.a_rows != p.M) return hipErrorInvalidValue;
