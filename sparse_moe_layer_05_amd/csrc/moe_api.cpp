@@ -31,8 +31,11 @@ struct Plan {
   int nsplit = 1, kchunk = 0;
   size_t dscratch = 0, mt_start = 0, xq = 0, sx = 0, hq = 0, sh = 0, xl = 0, z = 0, h = 0, hs = 0;
   size_t Y = 0, total = 0;
-  int lsplit = 1;    // K ranges of the streamed projection into the latent width (decode)
+  int lsplit = 1;    // K ranges of the projection into the latent width (decode, and tiles of
+                     // block-scaled experts)
+  int lchunk = 0;    // columns of a range (tiles)
   size_t xpart = 0;  // its fp32 slabs [lsplit][T][L]
+  bool y32 = false;  // tiles of block-scaled experts: the experts' rows Y are kept in fp32
   int ssplit = 1;    // K ranges of the shared expert's down projection on the decode path (plain
                      // layer): fp32 slabs [ssplit][T][H] after the pair rows of Y
 };
@@ -135,6 +138,13 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
              H / (p.lsplit * 2) >= 256)
         p.lsplit *= 2;
       if (p.lsplit > 1) p.xpart = take((size_t)p.lsplit * Tz * (size_t)p.L * 4);
+    } else if (mx_grouped) {
+      // x W_in^T: few tiles (L columns) over a long K (H), cut as the router's product is
+      // (1001 tokens, H 4096, L 1024: 64 tiles, 62 us uncut)
+      router_split(p.T, p.L, p.H, &p.lsplit, &p.lchunk);
+      if (p.lsplit > 1) p.xpart = take((size_t)p.lsplit * Tz * (size_t)p.L * 4);
+      // the gated sum z is rounded to bf16 on its way to W_out: its terms are not rounded as well
+      p.y32 = true;
     }
   }
   p.h = take(P * (size_t)p.I * ea);
@@ -156,7 +166,7 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
     const size_t rows = P + ((p.Is && !p.L) ? (size_t)p.ssplit * Tz : 0);
     p.Y = take(rows * (size_t)p.D * 4);
   } else {
-    p.Y = take(P * (size_t)p.D * ea);
+    p.Y = take(P * (size_t)p.D * (p.y32 ? 4 : ea));
   }
   p.total = off;
   *pl = p;
@@ -409,6 +419,17 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
     } else if (stream_path) {
       MOE_SPAN("stream:latent_in");
       MOE_TRY(stream_dense(w->x, H, w->W_in, L, H, T, xl, L, kStoreBF16, s));
+    } else if (pl.lsplit > 1) {
+      float* part = (float*)(base + pl.xpart);
+      {
+        MOE_SPAN("gemm_bf16_f32out:latent_in");
+        GemmParams q;
+        q.A = w->x; q.lda = H; q.a_rows = T; q.B = w->W_in; q.ldb = H; q.C = part; q.ldc = L;
+        q.M = T; q.N = L; q.K = H; q.ksplit = pl.lsplit; q.kchunk = pl.lchunk;
+        MOE_TRY(launch_gemm(GemmKind{Elt::BF16, Elt::F32, Epi::Store}, q, 0, s));
+      }
+      MOE_SPAN("reduce:latent_in");
+      MOE_TRY(launch_reduce_slabs(part, pl.lsplit, T, L, L, xl, L, kStoreBF16, s));
     } else {
       MOE_SPAN(act == Elt::F32 ? "gemm_f32_store:latent_in" : "gemm_bf16_store:latent_in");
       MOE_TRY(dense(act, act, Epi::Store, w->x, H, w->W_in, H, xl, L, T, L, H, s));
@@ -540,7 +561,8 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
       }
       m.A = hq; m.a_row = sh; m.a_rows = P; m.a_gather = nullptr;
       m.W = (const uint8_t*)w->W_down; m.w_mx = (const uint8_t*)w->s_down;
-      m.C = Y; m.N = D; m.K = I; m.sqrelu = 0;
+      m.C = Y; m.N = D; m.K = I; m.sqrelu = 0; m.out_f32 = pl.y32;
+      if (pl.y32) y_elt = Elt::F32;
       {
         MOE_SPAN(f4 ? "gemm_mxfp4_store:routed_down" : "gemm_mxfp8_store:routed_down");
         MOE_TRY(launch_mx_gemm(Elt::FP8, pl.ex, m, max_mt, s));
