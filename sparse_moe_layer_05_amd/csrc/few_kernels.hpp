@@ -271,31 +271,37 @@ __global__ __launch_bounds__(256) void few_front(FewParams p) {
 }
 
 // --------------------------------------------------------------------------------- 2 up
-// One workgroup of 8 waves per CU. First the shared expert: workgroup n takes 16 rows of Ws_up,
-// its waves split K, and the loads are issued before the selection, which needs two round trips to
-// the scores and a chain of wave-wide maxima. Then units of (touched expert, 16 rows of W_up), one
-// wave each over all of K, double buffered: while a batch of U steps is multiplied the next one
-// (of this unit or of the wave's next) is in flight. Activations are read from LDS, as bf16 rows
-// or the bf16 values of their e4m3 codes, zeros up to a whole step. NPER * 64 >= E; XLDS: the rows
-// fit (else bf16 ones are read from L2).
-constexpr int kUpWaves = 8;
-constexpr int kUpThreads = 64 * kUpWaves;
+// One workgroup per CU. First the shared expert: workgroup n takes 16 rows of Ws_up, its waves
+// split K, and the loads are issued before the selection, which needs two round trips to the scores
+// and a chain of wave-wide maxima. Then units of (touched expert, 16 rows of W_up), one wave each
+// over all of K, double buffered: while a batch of U steps is multiplied the next one (of this unit
+// or of the wave's next) is in flight. Activations are read from LDS, as bf16 rows or the bf16
+// values of their e4m3 codes, zeros up to a whole step. NPER * 64 >= E; XLDS: the rows fit (else
+// bf16 ones are read from L2).
+// bf16: 8 waves with 12 steps a batch (one token 48.6 us per layer; 16 waves with 6 steps 50.9;
+// two or four waves sharing a unit's K 53 and more). 8- and 4-bit weights, whose units are shorter
+// and leave an uneven second round: 16 waves (MXFP4, 4 tokens: 58.8 us against 61.3; e4m3, 16
+// tokens: 164 against 165). A plain read of the same 80 MB takes 14.5 us, in this pattern (16 rows
+// of 64 bytes an instruction) 16 to 18.
+template <Elt F> constexpr int kUpWaves = F == Elt::BF16 ? 8 : 16;
 constexpr size_t kUpRowsLds = 130 * 1024;   // of the staged activations
-constexpr int kSharedSteps = 12;   // steps of the shared unit in flight per wave
+// steps of the shared unit in flight per wave
+template <Elt F> constexpr int kSharedSteps = F == Elt::BF16 ? 12 : 6;
 
 // LDS row stride in bytes of K staged elements, whole steps of 128 and an odd number of 16-byte
 // chunks (16 rows at one chunk index then fall on distinct banks).
 __host__ __device__ inline int lds_stride(int K) { return (K + 127) / 128 * 256 + 16; }
 
 template <Elt F, int NPER, bool XLDS>
-__global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
+__global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
   using M = Fmt<F>;
+  constexpr int NWV = kUpWaves<F>, NTH = 64 * NWV, SS = kSharedSteps<F>;
   __shared__ int idx_l[TB * 64];
   __shared__ float gates_l[TB * 64];
   __shared__ uint32_t emask[NPER * 64];     // tokens that selected expert e
   __shared__ int slot_l[NPER * 64];         // touched experts, ascending
   __shared__ int cnt[NPER];
-  __shared__ float part[kUpWaves][16][17];
+  __shared__ float part[NWV / 2][16][17];
   __shared__ float row_scale[TB];
   extern __shared__ __attribute__((aligned(16))) uint8_t xl[];  // [T] rows of ldx bytes
   const int tid = threadIdx.x, lane = tid & 63;
@@ -306,25 +312,25 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
 
   // the shared expert's first loads
   const int nsh = p.L ? 0 : p.Is / 16;
-  const int st = cdiv(p.H, 32), sper = cdiv(st, kUpWaves);
+  const int st = cdiv(p.H, 32), sper = cdiv(st, NWV);
   const int slo = min(st, wave * sper), shi = min(st, slo + sper);
   const int send = min(p.H, shi * 32);
-  uint4 sw[kSharedSteps], sa[kSharedSteps];
+  uint4 sw[SS], sa[SS];
   const uint16_t* srow = p.x + (int64_t)t * p.H;
   if ((int)blockIdx.x < nsh && slo < shi) {
     const uint16_t* w = p.Ws_up + (int64_t)(16 * blockIdx.x + r) * p.H;
 #pragma unroll
-    for (int q = 0; q < kSharedSteps; ++q) {
+    for (int q = 0; q < SS; ++q) {
       const int el = (slo + q) * 32 + 8 * g, at = el < send ? el : 0;
       sw[q] = *(const uint4*)(w + at);
       sa[q] = *(const uint4*)(srow + at);
     }
   }
 
-  for (int i = tid; i < NPER * 64; i += kUpThreads) emask[i] = 0;
+  for (int i = tid; i < NPER * 64; i += NTH) emask[i] = 0;
   __syncthreads();
   const int ldx = lds_stride(p.D);
-  for (int tk = wave; tk < p.T; tk += kUpWaves) {
+  for (int tk = wave; tk < p.T; tk += NWV) {
     // selection of token tk
     bool ok = lane < p.k;
     if (p.given) {
@@ -375,7 +381,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   }
   __syncthreads();
   // touched experts, ascending
-  for (int c = wave; c < NPER; c += kUpWaves) {
+  for (int c = wave; c < NPER; c += NWV) {
     const uint64_t any = __ballot(emask[c * 64 + lane] != 0);
     if (lane == 0) cnt[c] = __popcll(any);
   }
@@ -383,7 +389,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   int n_slots = 0;
 #pragma unroll
   for (int c = 0; c < NPER; ++c) {
-    if (c % kUpWaves == wave) {
+    if (c % NWV == wave) {
       const bool on = emask[c * 64 + lane] != 0;
       const uint64_t any = __ballot(on);
       if (on) slot_l[n_slots + __popcll(any & ((1ull << lane) - 1))] = c * 64 + lane;
@@ -393,11 +399,11 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   __syncthreads();
   if (blockIdx.x == gridDim.x - 1) {  // what launch 3 and the caller read
     if (tid == 0) *p.n_slots = n_slots;
-    for (int i = tid; i < n_slots; i += kUpThreads) {
+    for (int i = tid; i < n_slots; i += NTH) {
       p.slot_e[i] = slot_l[i];
       p.slot_mask[i] = emask[slot_l[i]];
     }
-    for (int i = tid; i < n_slots * TB; i += kUpThreads) {
+    for (int i = tid; i < n_slots * TB; i += NTH) {
       const int e = slot_l[i / TB], tk = i % TB;
       float v = 0.f;
       if (tk < p.T)
@@ -406,7 +412,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
       p.gate_m[i] = v;
     }
     if (!p.given)
-      for (int i = tid; i < p.T * p.k; i += kUpThreads) {
+      for (int i = tid; i < p.T * p.k; i += NTH) {
         p.idx[i] = idx_l[i];
         p.gates[i] = gates_l[i];
       }
@@ -418,15 +424,21 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
     int from = slo;
     if (n == (int)blockIdx.x && slo < shi) {
 #pragma unroll
-      for (int q = 0; q < kSharedSteps; ++q) {
+      for (int q = 0; q < SS; ++q) {
         if ((slo + q) * 32 + 8 * g >= send) sw[q] = make_uint4(0, 0, 0, 0);
         acc = mul(__builtin_bit_cast(bf16x8_t, sw[q]), sa[q], acc);
       }
-      from = min(shi, slo + kSharedSteps);
+      from = min(shi, slo + SS);
     }
-    acc = dot_rows<8, false>(p.Ws_up + (int64_t)(16 * n + r) * p.H, srow, srow, p.H, from, shi, g, acc);
+    acc = dot_rows<4, false>(p.Ws_up + (int64_t)(16 * n + r) * p.H, srow, srow, p.H, from, shi, g, acc);
+    constexpr int half = NWV / 2;   // the upper half's sums, then the lower's added to them
+    if (wave >= half)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[wave][r][4 * g + i] = acc[i];
+      for (int i = 0; i < 4; ++i) part[wave - half][r][4 * g + i] = acc[i];
+    __syncthreads();
+    if (wave < half)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[wave][r][4 * g + i] += acc[i];
     __syncthreads();
     if (wave == 0 && r < p.T) {
       float v[4];
@@ -434,7 +446,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
       for (int i = 0; i < 4; ++i) {
         v[i] = part[0][r][4 * g + i];
 #pragma unroll
-        for (int q = 1; q < kUpWaves; ++q) v[i] += part[q][r][4 * g + i];
+        for (int q = 1; q < half; ++q) v[i] += part[q][r][4 * g + i];
         v[i] = sqrelu(v[i]);
       }
       store_pair(p.hs, p.hs_lo, (int64_t)r * p.Is + 16 * n + 4 * g, v);
@@ -443,10 +455,10 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   }
 
   // routed units: wave-slot, + waves of the grid
-  const int nb = p.I / 16, total = n_slots * nb, stride = gridDim.x * kUpWaves;
+  const int nb = p.I / 16, total = n_slots * nb, stride = gridDim.x * NWV;
   int u = wave * gridDim.x + blockIdx.x;
   if (u >= total) return;
-  constexpr int U = F == Elt::BF16 ? 12 : (F == Elt::MXFP4 ? 8 : 6);
+  constexpr int U = F == Elt::BF16 ? 12 : 2;
   const int steps = cdiv(p.D, M::KS), nbat = cdiv(steps, U);
   struct Unit { const uint8_t *w, *wx; int slot, n0, e; };
   auto resolve = [&](int v) {
@@ -464,15 +476,18 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
   if (more) nxt = resolve(u + stride);
   int b = 0;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  auto issue = [&](const Unit& x, int bb, WStep<F>* w) {
+  // none: the same number of loads, all of the row's start
+  auto issue = [&](const Unit& x, int bb, WStep<F>* w, bool none) {
+    const int s = none ? 0 : bb * U, to = none ? 0 : p.D;
 #pragma unroll
-    for (int q = 0; q < U; ++q) load_step<F>(w[q], x.w, x.wx, bb * U + q, p.D, p.D, g);
+    for (int q = 0; q < U; ++q) load_step<F>(w[q], x.w, x.wx, s + q, to, p.D, g);
   };
   auto step = [&](WStep<F>* wc, WStep<F>* wn) {
     const bool last = b + 1 == nbat;
     Unit src = cur;
     if (last && more) src = nxt;
-    issue(src, last ? 0 : b + 1, wn);   // always the same number of loads
+    // always the same number of loads, so that the wait for a batch leaves the next in flight
+    issue(src, last ? 0 : b + 1, wn, last && !more);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       mask_step<F>(wc[q], b * U + q, p.D, g);
@@ -521,7 +536,7 @@ __global__ __launch_bounds__(kUpThreads) void few_up(FewParams p) {
     return true;
   };
   WStep<F> w0[U], w1[U];
-  issue(cur, 0, w0);
+  issue(cur, 0, w0, false);
   for (;;) {
     if (!step(w0, w1)) break;
     if (!step(w1, w0)) break;
@@ -587,7 +602,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
   };
 
   // one wave's steps [at, stop), in batches of up to U steps of one slot
-  constexpr int U = F == Elt::BF16 ? 4 : (F == Elt::MXFP4 ? 4 : 3);
+  constexpr int U = F == Elt::BF16 ? 4 : (F == Elt::MXFP8 ? 1 : 2);
   struct Pos {
     int slot, s, s1;           // batch: steps s .. of the slot, which ends (here) at s1
     const uint8_t *w, *wx;
@@ -626,13 +641,14 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
     WStep<F> w[U];
     uint4 a[M::narrow ? 1 : U], b[M::narrow ? 1 : U];
   };
-  auto issue = [&](const Pos& x, Batch& o) {
-    const int kend = min(p.I, x.s1 * M::KS);
+  // none: the same number of loads, all of the row's start
+  auto issue = [&](const Pos& x, Batch& o, bool none) {
+    const int kend = none ? 0 : min(p.I, x.s1 * M::KS), s = none ? 0 : x.s;
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      load_step<F>(o.w[q], x.w, x.wx, x.s + q, kend, p.I, g);
+      load_step<F>(o.w[q], x.w, x.wx, s + q, kend, p.I, g);
       if constexpr (!M::narrow) {
-        const int el = (x.s + q) * M::KS + M::k_of(0, g), at = el < kend ? el : 0;
+        const int el = (s + q) * M::KS + M::k_of(0, g), at = el < kend ? el : 0;
         o.a[q] = *(const uint4*)(x.a + at);
         o.b[q] = *(const uint4*)(x.a2 + at);
       }
@@ -645,7 +661,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
     }
     Pos cur = enter(at, stop, pass_slot);
     Batch b0, b1;
-    issue(cur, b0);
+    issue(cur, b0, false);
     if (first) shared_part();
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
     auto step = [&](Batch& bc, Batch& bn) {
@@ -655,7 +671,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
       Pos nxt = cur;
       if (!done && slot_done) nxt = enter(at, stop, pass_slot);
       else if (!done) nxt.s = cur.s + took;
-      issue(nxt, bn);      // the last time: again, unused
+      issue(nxt, bn, done);
       const int kend = min(p.I, cur.s1 * M::KS);
 #pragma unroll
       for (int q = 0; q < U; ++q) {
@@ -793,7 +809,7 @@ __global__ __launch_bounds__(512) void few_out(FewParams p) {
 
 template <Elt F, bool XLDS>
 hipError_t run_up(const FewParams& p, int grid, size_t lds, hipStream_t s) {
-  const dim3 block(kUpThreads);
+  const dim3 block(64 * kUpWaves<F>);
   if (p.E <= 128) hipLaunchKernelGGL((few_up<F, 2, XLDS>), dim3(grid), block, lds, s, p);
   else if (p.E <= 512) hipLaunchKernelGGL((few_up<F, 8, XLDS>), dim3(grid), block, lds, s, p);
   else hipLaunchKernelGGL((few_up<F, 16, XLDS>), dim3(grid), block, lds, s, p);
