@@ -290,7 +290,7 @@ int32_t moe_layer_backward(const moe_desc_t *desc, const moe_weights_t *weights,
  * minus the element format's largest (2 or 8), clamped to [-127, 127] (a zero block: code 0);
  * elements rounded to nearest even and saturated, the sign kept on zeros. A block that holds a
  * NaN or an infinity gets scale code 255 and zero elements: it stands for NaN.
- * rows * cols <= 2^36. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
+ * rows * cols <= 2^35. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
  * MOE_ERR_UNSUPPORTED (dt or fmt). */
 int32_t moe_mx_quantize(const void *x, moe_dtype_t dt, int64_t rows, int32_t cols,
                         moe_dtype_t fmt, void *codes, uint8_t *scales, void *stream);

@@ -10,8 +10,9 @@
 namespace moe {
 
 constexpr int kMxBlockElts = 32;  // elements that share one E8M0 scale
-// Elements one conversion launch takes: a grid's threads (32 elements each) stay below 2^32.
-constexpr int64_t kMxMaxElts = (int64_t)1 << 36;
+// Elements one conversion launch takes: a grid's threads (16 elements or more each) stay at or
+// below 2^32.
+constexpr int64_t kMxMaxElts = (int64_t)1 << 35;
 
 // n elements (whole blocks, contiguous) of bf16 / fp32 -> codes and one E8M0 scale per block.
 hipError_t launch_mx_quantize(const void* x, Elt xt, int64_t n, Elt fmt, uint8_t* codes,

@@ -8,9 +8,9 @@
 // the quotient is far below the smallest element and rounds to zero all the same.
 // A block that holds a NaN or an infinity gets scale code 255 (NaN) and zero elements.
 //
-// Four lanes share a block, eight elements each: 16- or 32-byte loads, the maximum over the four
-// by two quad permutations, no LDS. Rows are contiguous, so a matrix is one run of blocks. Each
-// thread takes kIter groups of eight whose loads are all in flight together.
+// A lane takes 16 bytes at a time, so a block is shared by four lanes (bf16) or eight (fp32); its
+// maximum comes from two or three lane permutations, no LDS. Rows are contiguous, so a matrix is
+// one run of blocks. Each thread takes kIter such loads, all in flight together.
 // Included once, by backward.hip: these kernels are part of that object, so that the library stays the
 // objects that its parts are linked from elsewhere (host code under the sanitizers).
 #pragma once
@@ -22,7 +22,7 @@ namespace moe {
 namespace {
 namespace mx_convert {
 
-constexpr int kIter = 4;      // groups of 8 elements per thread
+constexpr int kIter = 4;      // groups of elements per thread
 constexpr int kThreads = 256;
 
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -39,67 +39,75 @@ __device__ __forceinline__ float e8m0(uint32_t code) {
   return __uint_as_float(code ? code << 23 : 0x00400000u);
 }
 
+// Elements a lane takes at once: one 16-byte load.
+template <Elt XT> constexpr int kEpt = XT == Elt::BF16 ? 8 : 4;
 template <Elt XT>
-__device__ __forceinline__ void load8(const void* x, int64_t i, float* v) {
-  if constexpr (XT == Elt::BF16) {
-    const uint4 q = *(const uint4*)((const uint16_t*)x + i);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void unpack(uint4 q, float* v) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (XT == Elt::BF16) {
       v[2 * j] = __uint_as_float(w[j] << 16);
       v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    } else {
+      v[j] = __uint_as_float(w[j]);
     }
-  } else {
-    const float4 a = *(const float4*)((const float*)x + i);
-    const float4 b = *(const float4*)((const float*)x + i + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 }
 
 template <Elt XT, Elt FMT>
-__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void* __restrict__ x,
-                                                               int64_t n8,
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint4* __restrict__ x,
+                                                               int64_t ng,
                                                                uint8_t* __restrict__ codes,
                                                                uint8_t* __restrict__ scales) {
+  constexpr int E = kEpt<XT>, L = kMxBlockElts / E;   // lanes of a block: 4 or 8
   const int64_t first = (int64_t)blockIdx.x * (kThreads * kIter) + threadIdx.x;
-  float v[kIter][8];
+  uint4 in[kIter];
 #pragma unroll
   for (int q = 0; q < kIter; ++q) {
     const int64_t g = first + q * kThreads;
-    if (g < n8) load8<XT>(x, g * 8, v[q]);   // n8 % 4 == 0: quads are whole
+    in[q] = g < ng ? x[g] : make_uint4(0, 0, 0, 0);   // blocks are whole: so are their lanes
   }
 #pragma unroll
   for (int q = 0; q < kIter; ++q) {
     const int64_t g = first + q * kThreads;
-    if (g >= n8) break;
+    float v[E];
+    unpack<XT>(in[q], v);
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[q][j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < E; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     m = quad_max(m);
+    if constexpr (L == 8)   // row_half_mirror: lane i of eight meets lane 7 - i
+      m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));
     const bool bad = m >= 0x7F800000u;
     constexpr int emax = FMT == Elt::MXFP4 ? 2 : 8;
     const int code = max(0, (int)(m >> 23) - emax);
     const float inv = bad ? 0.f : e8m0(254 - code);
-    float e[8];
+    float e[E];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = bad ? 0.f : v[q][j] * inv;
-    if constexpr (FMT == Elt::MXFP4) {
-      // rounds to nearest even and saturates at 6
-      uint32_t c = 0;
-      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, e[0], e[1], 1.f, 0);
-      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, e[2], e[3], 1.f, 1);
-      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, e[4], e[5], 1.f, 2);
-      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, e[6], e[7], 1.f, 3);
-      *(uint32_t*)(codes + g * 4) = c;
+    for (int j = 0; j < E; ++j) e[j] = bad ? 0.f : v[j] * inv;
+    uint32_t c[2] = {0, 0};
+    if constexpr (FMT == Elt::MXFP4) {   // rounds to nearest even and saturates at 6
+      c[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[0], e[0], e[1], 1.f, 0);
+      c[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[0], e[2], e[3], 1.f, 1);
+      if constexpr (E == 8) {
+        c[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[0], e[4], e[5], 1.f, 2);
+        c[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[0], e[6], e[7], 1.f, 3);
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = fminf(fmaxf(e[j], -448.f), 448.f);
-      const uint32_t lo = cvt_fp8x2(e[0], e[1]) | cvt_fp8x2(e[2], e[3]) << 16;
-      const uint32_t hi = cvt_fp8x2(e[4], e[5]) | cvt_fp8x2(e[6], e[7]) << 16;
-      *(uint2*)(codes + g * 8) = make_uint2(lo, hi);
+      for (int j = 0; j < E; ++j) e[j] = fminf(fmaxf(e[j], -448.f), 448.f);
+#pragma unroll
+      for (int j = 0; j < E / 4; ++j)
+        c[j] = cvt_fp8x2(e[4 * j], e[4 * j + 1]) | cvt_fp8x2(e[4 * j + 2], e[4 * j + 3]) << 16;
     }
-    if ((threadIdx.x & 3) == 0) scales[g >> 2] = bad ? 255 : (uint8_t)code;
+    if (g < ng) {
+      constexpr int B = FMT == Elt::MXFP4 ? E / 2 : E;   // bytes of this lane's codes
+      if constexpr (B == 2) *(uint16_t*)(codes + g * 2) = (uint16_t)c[0];
+      else if constexpr (B == 4) *(uint32_t*)(codes + g * 4) = c[0];
+      else *(uint2*)(codes + g * 8) = make_uint2(c[0], c[1]);
+      if ((threadIdx.x & (L - 1)) == 0) scales[g / L] = bad ? 255 : (uint8_t)code;
+    }
   }
 }
 
@@ -156,8 +164,8 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* 
   }
 }
 
-dim3 grid_of(int64_t n8) {
-  return dim3((unsigned)((n8 + kThreads * kIter - 1) / (kThreads * kIter)));
+dim3 grid_of(int64_t groups) {
+  return dim3((unsigned)((groups + kThreads * kIter - 1) / (kThreads * kIter)));
 }
 
 }  // namespace mx_convert
@@ -169,10 +177,9 @@ hipError_t launch_mx_quantize(const void* x, Elt xt, int64_t n, Elt fmt, uint8_t
                               uint8_t* scales, hipStream_t s) {
   if (n <= 0) return hipSuccess;
   if (n % kMxBlockElts || n > kMxMaxElts) return hipErrorInvalidValue;
-  const int64_t n8 = n / 8;
-#define MOE_MXQ(X, F)                                                                           \
-  hipLaunchKernelGGL((mx_quantize_kernel<X, F>), grid_of(n8), dim3(kThreads), 0, s, x, n8, codes, \
-                     scales)
+#define MOE_MXQ(X, F)                                                                     \
+  hipLaunchKernelGGL((mx_quantize_kernel<X, F>), grid_of(n / kEpt<X>), dim3(kThreads), 0, s, \
+                     (const uint4*)x, n / kEpt<X>, codes, scales)
   const bool f4 = fmt == Elt::MXFP4;
   if (xt == Elt::BF16) {
     if (f4) MOE_MXQ(Elt::BF16, Elt::MXFP4); else MOE_MXQ(Elt::BF16, Elt::MXFP8);
