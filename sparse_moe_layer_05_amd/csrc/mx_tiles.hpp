@@ -223,13 +223,13 @@ __device__ __forceinline__ bool tile_of(const MxGemmParams& p, int L, int& g, in
   int local, mt_g;
   if (p.mt_start) {
     if (L >= p.mt_start[p.G] * nN) return false;
-    const int key = L / nN;
-    int lo = 0, hi = p.G - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.mt_start[mid] <= key) lo = mid; else hi = mid - 1;
-    }
-    g = lo;
+    // the last group whose first M-tile is at or before this one: counted by the wave's lanes, one
+    // round trip to the list where a search would take a chain of them
+    const int key = L / nN, lane = threadIdx.x & 63;
+    int below = 0;
+    for (int i = 0; i < p.G; i += 64)
+      below += __popcll(__ballot(i + lane < p.G && p.mt_start[min(i + lane, p.G - 1)] <= key));
+    g = __builtin_amdgcn_readfirstlane(below) - 1;
     mt_g = p.mt_start[g + 1] - p.mt_start[g];
     local = L - p.mt_start[g] * nN;
   } else {
