@@ -194,6 +194,15 @@ __device__ __forceinline__ uint32_t lds_of(const void* q) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)q;
 }
 
+// A barrier of the workgroup for LDS alone: it does not wait for loads in flight. The fences are what
+// tells the compiler that other waves' LDS writes become visible here; to a clobber on an asm
+// statement it need not react for arrays whose address never leaves the kernel.
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // The 16 bytes v shifted down by `by` bytes, and those from byte `valid` on set to 0x7F (scale 1).
 __device__ __forceinline__ uint4 trim_scales(uint4 v, int by, int valid) {
   uint32_t w[8] = {v.x, v.y, v.z, v.w, 0, 0, 0, 0};
@@ -215,7 +224,17 @@ __device__ __forceinline__ uint4 trim_scales(uint4 v, int by, int valid) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Logical tile L -> group, first row, rows, first column: bands of 8 M-tiles, M fastest inside.
+// The local-th tile of a group of mt_g M-tiles: bands of 8 M-tiles, M fastest inside.
+template <int BN>
+__device__ __forceinline__ void place_tile(int local, int mt_g, int nN, int& mt, int& n0) {
+  constexpr int GB = 8;
+  const int first = (local / (GB * nN)) * GB;
+  const int gm = min(GB, mt_g - first);
+  const int within = local - first * nN;
+  n0 = (within / gm) * BN;
+  mt = first + within % gm;
+}
+// Logical tile L -> group, first row, rows, first column.
 template <int BM, int BN>
 __device__ __forceinline__ bool tile_of(const MxGemmParams& p, int L, int& g, int& row0, int& rows,
                                         int& n0) {
@@ -238,15 +257,56 @@ __device__ __forceinline__ bool tile_of(const MxGemmParams& p, int L, int& g, in
     local = L;
     if (L >= mt_g * nN) return false;
   }
-  constexpr int GB = 8;
-  const int first = (local / (GB * nN)) * GB;
-  const int gm = min(GB, mt_g - first);
-  const int within = local - first * nN;
-  n0 = (within / gm) * BN;
-  const int mt = first + within % gm;
+  int mt;
+  place_tile<BN>(local, mt_g, nN, mt, n0);
   row0 = (p.mt_start ? p.offs[g] : 0) + mt * BM;
   rows = min(BM, (p.mt_start ? p.offs[g + 1] : p.M) - row0);
   return rows > 0;
+}
+
+// One K-step (128 elements) of a BM x BN tile from the stage at st (A rows, then W rows) and the
+// scales of its super-step, of which it is the q-th K-step.
+template <int B>
+__device__ __forceinline__ i32x8_t read_frag(const uint8_t* base, int row, int s, int lg) {
+  constexpr int SL = B * 16;
+  if constexpr (B == 8)
+    return frag(*(const uint4*)(base + slot<SL>(row, 4 * s + lg)),
+                *(const uint4*)(base + slot<SL>(row, 4 * s + 2 + lg)));
+  else
+    return frag(*(const uint4*)(base + slot<SL>(row, 2 * s + lg)), kZero4);
+}
+template <int BM, int BN, int WGM, int WGN, int FA, int FW>
+__device__ __forceinline__ void mma_step(f32x16_t (&acc)[BM / WGM / 32][BN / WGN / 32],
+                                         const uint8_t* st, const uint4* sc, int q, int lane,
+                                         int wm, int wn) {
+  constexpr int SA = kBits<FA> * 16, WM = BM / WGM, WN = BN / WGN, MB = WM / 32, NB = WN / 32;
+  constexpr int W0 = FA == kE4Row ? 0 : BM;   // first W row among the staged scales
+  const int lg = lane >> 5, lr = lane & 31;
+  int xa[MB], xw[NB];   // this lane's scale bytes at bits 0 and 16 (k-sub 0 and 1)
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+    xa[i] = FA == kE4Row ? 0x7F7F7F7F
+                         : (int)(((const uint32_t*)&sc[wm * WM + i * 32 + lr])[q] >> (8 * lg));
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+    xw[j] = (int)(((const uint32_t*)&sc[W0 + wn * WN + j * 32 + lr])[q] >> (8 * lg));
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    i32x8_t a[MB], b[NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) a[i] = read_frag<kBits<FA>>(st, wm * WM + i * 32 + lr, s, lg);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      b[j] = read_frag<kBits<FW>>(st + BM * SA, wn * WN + j * 32 + lr, s, lg);
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[i][j] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                 a[i], b[j], acc[i][j], kCode<FA>, kCode<FW>, 0, xa[i], 0, xw[j])
+                           : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                 a[i], b[j], acc[i][j], kCode<FA>, kCode<FW>, 2, xa[i], 2, xw[j]);
+  }
 }
 
 template <int BM, int BN, int WGM, int WGN, int NS, int FA, int FW>
@@ -308,7 +368,6 @@ void mx_tile_kernel(MxGemmParams p) {
     for (int i = 0; i < GW; ++i)
       dma16(rw, st + BM * SA + DW * i * 1024, lw ? ow[i] : kOut, ks * SW);
   };
-  auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
   // the chunks of a partial last K-step that lie past K, zeroed once the stage has landed
   auto fix_tail = [&](uint8_t* st) {
     if (loads) {
@@ -372,42 +431,8 @@ void mx_tile_kernel(MxGemmParams p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  auto read_frag = [&](const uint8_t* base, int row, int s, auto bits) {
-    constexpr int B = decltype(bits)::value, SL = B * 16;
-    if constexpr (B == 8)
-      return frag(*(const uint4*)(base + slot<SL>(row, 4 * s + lg)),
-                  *(const uint4*)(base + slot<SL>(row, 4 * s + 2 + lg)));
-    else
-      return frag(*(const uint4*)(base + slot<SL>(row, 2 * s + lg)), kZero4);
-  };
   auto compute = [&](const uint8_t* st, int buf, int q) {
-    int xa[MB], xw[NB];   // this lane's scale bytes at bits 0 and 16 (k-sub 0 and 1)
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-      xa[i] = FA == kE4Row ? 0x7F7F7F7F
-                           : (int)(((const uint32_t*)&sc[buf][wm * WM + i * 32 + lr])[q] >> (8 * lg));
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-      xw[j] = (int)(((const uint32_t*)&sc[buf][SROWS - BN + wn * WN + j * 32 + lr])[q] >> (8 * lg));
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      i32x8_t a[MB], b[NB];
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-        a[i] = read_frag(st, wm * WM + i * 32 + lr, s, std::integral_constant<int, kBits<FA>>());
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        b[j] = read_frag(st + BM * SA, wn * WN + j * 32 + lr, s,
-                         std::integral_constant<int, kBits<FW>>());
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-          acc[i][j] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                   a[i], b[j], acc[i][j], kCode<FA>, kCode<FW>, 0, xa[i], 0, xw[j])
-                             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                   a[i], b[j], acc[i][j], kCode<FA>, kCode<FW>, 2, xa[i], 2, xw[j]);
-    }
+    mma_step<BM, BN, WGM, WGN, FA, FW>(acc, st, sc[buf], q, lane, wm, wn);
   };
 
   // K-step ks + NS - 1 is in flight while K-step ks is multiplied; before ks a wave waits until
@@ -485,6 +510,270 @@ void mx_tile_kernel(MxGemmParams p) {
     }
 }
 
+// ---------------------------------------------------------------------- experts, persistent
+// Expert products (A: e4m3 rows with a scale each) by one workgroup of 8 waves per CU that walks
+// BM x 256 tiles: workgroup b runs on die b % 8 and takes every (grid / 8)-th tile of that die's
+// contiguous range. The K-steps of all its tiles form one pipeline: while a tile's last K-steps are
+// multiplied and its result is stored, the next tile's first ones are landing, so that neither the
+// first loads nor the epilogue are waited for. What the loading waves need of the next tile (group,
+// rows and their sources) is looked up by the other waves, one load's round trip per K-step, and
+// passed through LDS, so that a loading wave waits for no load but the operands; so are the row
+// scales that the epilogue reads. Without the products a launch over 49152 rows of 128 MXFP4
+// experts (K 2688, N 1856) takes 269 of its 365 us, without the loads 285: operands come through
+// the L1 at 15 to 17 B per clock and CU, in 64-byte requests of which 82% hit the L2 and the rest
+// is each expert read once; lines fetched into L2 ahead of use change nothing.
+constexpr int kStripRows = 8;   // rows of a wave's epilogue strip
+constexpr int kLookups = 5;     // phases of a tile's lookup
+constexpr int kPersistSteps = 8;   // least K-steps of a tile
+
+template <int BM, int NS, int FW>
+__global__ __launch_bounds__(512, 2) void mx_persist_kernel(MxGemmParams p) {
+  constexpr int BN = 256, WGM = 2, WGN = 4, DW = 4;         // waves; the first DW load operands
+  constexpr int SA = 128, SW = kBits<FW> * 16;              // bytes of a row's K-step
+  constexpr int WM = BM / WGM, WN = BN / WGN, MB = WM / 32, NB = WN / 32;
+  constexpr int RA = 1024 / SA, RW = 1024 / SW;             // rows per 1-KB load
+  constexpr int LA = SA / 16, LW = SW / 16;                 // lanes per row
+  constexpr int GA = BM / (RA * DW), GW = BN / (RW * DW);   // 1-KB loads per loading wave
+  constexpr int STAGE = BM * SA + BN * SW;
+  constexpr int EPW = WN + 4, CG = WN / 8, ITEMS = kStripRows * CG / 64;
+  static_assert(GA >= 1 && GW >= 1 && BM % (RA * DW) == 0 && BN % (RW * DW) == 0, "1-KB loads");
+  static_assert(WM % 32 == 0 && NS >= 2 && BM <= 64 * DW && BN == 64 * DW, "tile shape");
+  static_assert(kStripRows * CG % 64 == 0, "whole strips");
+  // a tile's description is written by its predecessor's K-step 3 and read from K-step nk - NS + 1
+  static_assert(kPersistSteps - NS + 1 >= kLookups - 1, "lookups end before the loads need them");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE];
+  __shared__ __attribute__((aligned(16))) uint4 sc[2][BN];
+  __shared__ __attribute__((aligned(16))) float strips[8][kStripRows][EPW];
+  __shared__ int tinfo[2][4];      // group, first row, rows, first column of a tile
+  __shared__ int tsrc[2][BM];      // source row of each of its rows, -1 past the last
+  __shared__ float trow[2][BM];    // and its scale
+
+  const int nN = cdiv(p.N, BN), total = p.mt_start[p.G] * nN;
+  const int die = blockIdx.x % kXcds, step = gridDim.x / kXcds, share = cdiv(total, kXcds);
+  const int hi = min(total, (die + 1) * share);
+  int L = die * share + (int)blockIdx.x / kXcds;
+  if (L >= hi) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WGN, wn = wave % WGN, lg = lane >> 5, lr = lane & 31;
+  const bool loads = wave < DW;
+  const int kba = p.K, kbw = p.K * kBits<FW> / 8;   // bytes of a row
+  const int nb = p.K / kMxBlockElts, nk = cdiv(p.K, 128), nss = cdiv(nk, 4);
+  const int tail_a = kba % SA, tail_w = kbw % SW;   // bytes of a partial last K-step
+
+  // The other waves: tile Lt's description to LDS buffer b, by phases whose loads are used in the
+  // next one; then its scales, a thread a row.
+  const int st0 = tid - 64 * DW;
+  int near0 = 0, near1 = 0, ng = 0, first_mt = 0, end_mt = 0, off0 = 0, off1 = 0, nrows = 0, nn0 = 0;
+  int src = 0;
+  float row_scale = 0.f;
+  auto lookup = [&](int phase, int Lt, int b) {
+    if (loads) return;
+    const int key = Lt / nN;
+    if (phase == 0) {
+      near0 = p.mt_start[min(lane, p.G - 1)];
+      near1 = p.mt_start[min(64 + lane, p.G - 1)];
+    } else if (phase == 1) {   // the last group that starts at or before this M-tile
+      int below = __popcll(__ballot(lane < p.G && near0 <= key)) +
+                  __popcll(__ballot(64 + lane < p.G && near1 <= key));
+      for (int i = 128; i < p.G; i += 64)
+        below += __popcll(__ballot(i + lane < p.G && p.mt_start[min(i + lane, p.G - 1)] <= key));
+      ng = __builtin_amdgcn_readfirstlane(below) - 1;
+      first_mt = p.mt_start[ng];
+      end_mt = p.mt_start[ng + 1];
+      off0 = p.offs[ng];
+      off1 = p.offs[ng + 1];
+    } else if (phase == 2) {
+      int mt;
+      place_tile<BN>(Lt - first_mt * nN, end_mt - first_mt, nN, mt, nn0);
+      const int row0 = off0 + mt * BM;
+      nrows = min(BM, off1 - row0);
+      if (st0 < 4) tinfo[b][st0] = st0 == 0 ? ng : st0 == 1 ? row0 : st0 == 2 ? nrows : nn0;
+      src = row0 + min(min(st0, BM - 1), nrows - 1);
+      if (p.a_gather) src = p.a_gather[src];
+    } else if (phase == 3) {
+      if (st0 < BM) tsrc[b][st0] = st0 < nrows ? src : -1;
+      row_scale = p.a_row[src];
+    } else if (st0 < BM) {
+      trow[b][st0] = row_scale;
+    }
+  };
+  const uint8_t* sp = p.w_mx;   // this thread's row of scales, and the array's bytes from it on
+  int64_t sleft = 16;
+  uint4 sv = kZero4;
+  auto scales_of = [&]() {      // the looked-up tile's
+    const int64_t n = min(nn0 + st0, p.N - 1);
+    sp = p.w_mx + ((int64_t)ng * p.N + n) * nb;
+    sleft = ((int64_t)(p.G - ng) * p.N - n) * nb;
+  };
+  auto fetch_scales = [&](int ss) {
+    if (loads) return;
+    typedef uint32_t u32x4a1 __attribute__((ext_vector_type(4), aligned(1)));
+    const u32x4a1 x = *(const u32x4a1*)(sp + min((int64_t)16 * ss, sleft - 16));
+    sv = make_uint4(x.x, x.y, x.z, x.w);
+  };
+  auto put_scales = [&](int ss, int b) {
+    if (loads) return;
+    sc[b][st0] = trim_scales(sv, (int)max((int64_t)0, 16 * ss + 16 - sleft), nb - 16 * ss);
+  };
+
+  // the loading waves: sources of the tile whose K-steps are being issued
+  const i32x4_t ra = rsrc(p.A, (int64_t)p.a_rows * kba);
+  i32x4_t rw = ra;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_of(smem)) + wave * 1024;
+  const int ca = ((lane % LA) ^ swz<SA>(wave * RA + lane / LA)) << 4;
+  const int cw = ((lane % LW) ^ swz<SW>(wave * RW + lane / LW)) << 4;
+  constexpr uint32_t kOut = 0xFFFFFFF0u;   // an offset past every buffer: the load is skipped
+  uint32_t oa[GA], ow[GW];
+  auto sources = [&](int b) {
+    if (!loads) return;
+    const int g = __builtin_amdgcn_readfirstlane(tinfo[b][0]);
+    const int n0 = __builtin_amdgcn_readfirstlane(tinfo[b][3]);
+    rw = rsrc(p.W + (int64_t)g * p.N * kbw, (int64_t)p.N * kbw);
+#pragma unroll
+    for (int i = 0; i < GA; ++i) {
+      const int s = tsrc[b][(wave + DW * i) * RA + lane / LA];
+      oa[i] = s >= 0 ? (uint32_t)s * (uint32_t)kba + ca : kOut;
+    }
+#pragma unroll
+    for (int i = 0; i < GW; ++i)
+      ow[i] = (uint32_t)min(n0 + (wave + DW * i) * RW + lane / LW, p.N - 1) * (uint32_t)kbw + cw;
+  };
+  int islot = 0, cslot = 0;    // stages issued into next, multiplied next
+  int flying = 0, iks = 0;     // stages issued and not yet multiplied; the next K-step to issue ...
+  bool inext = false;          // ... of the next tile instead of the current one
+  auto issue = [&]() {
+    if (loads) {
+      const bool last = iks == nk - 1;
+      const bool la = !(last && tail_a) || ca < tail_a, lw = !(last && tail_w) || cw < tail_w;
+      const uint32_t st = lds0 + islot * STAGE;
+#pragma unroll
+      for (int i = 0; i < GA; ++i) dma16(ra, st + DW * i * 1024, la ? oa[i] : kOut, iks * SA);
+#pragma unroll
+      for (int i = 0; i < GW; ++i)
+        dma16(rw, st + BM * SA + DW * i * 1024, lw ? ow[i] : kOut, iks * SW);
+    }
+    ++iks;
+    ++flying;
+    islot = islot + 1 == NS ? 0 : islot + 1;
+  };
+  constexpr int PER = GA + GW;
+  static_assert((NS - 2) * PER < 64 && NS <= 4, "vmcnt range");
+  // until at most `ahead` later stages are outstanding (result stores in between wait longer)
+  auto wait_ahead = [&](int ahead) {
+    if (!loads) return;
+#define MOE_VMCNT(n) __builtin_amdgcn_s_waitcnt((((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8)))
+    if constexpr (NS >= 4) { if (ahead >= 2) { MOE_VMCNT(2 * PER); return; } }
+    if constexpr (NS >= 3) { if (ahead >= 1) { MOE_VMCNT(PER); return; } }
+    MOE_VMCNT(0);
+#undef MOE_VMCNT
+  };
+  // the missing part of a partial last K-step reads as zero elements
+  auto fix_tail = [&](uint8_t* st) {
+    if (loads) {
+      if (tail_a && ca >= tail_a)
+#pragma unroll
+        for (int i = 0; i < GA; ++i) *(uint4*)(st + (wave + DW * i) * 1024 + lane * 16) = kZero4;
+      if (tail_w && cw >= tail_w)
+#pragma unroll
+        for (int i = 0; i < GW; ++i)
+          *(uint4*)(st + BM * SA + (wave + DW * i) * 1024 + lane * 16) = kZero4;
+    }
+    barrier();
+  };
+
+  for (int ph = 0; ph < kLookups; ++ph) lookup(ph, L, 0);
+  scales_of();
+  fetch_scales(0);
+  put_scales(0, 0);
+  barrier();
+  sources(0);
+  while (flying < NS - 1) issue();
+  const int last_ss = (nk - 1) / 4 * 4;   // K-step that starts the last super-step
+  for (int tb = 0, sb = 0;; tb ^= 1) {    // LDS buffers of the tile, the super-step
+    const bool more = L + step < hi;
+    const int row0 = __builtin_amdgcn_readfirstlane(tinfo[tb][1]);
+    const int rows = __builtin_amdgcn_readfirstlane(tinfo[tb][2]);
+    const int n0 = __builtin_amdgcn_readfirstlane(tinfo[tb][3]);
+    f32x16_t acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    for (int ks = 0; ks < nk; ++ks) {
+      const int q = ks & 3, ss = ks >> 2;
+      wait_ahead(flying - 1);
+      barrier();               // publishes the stage (and its scales), frees the one before
+      uint8_t* st = smem + cslot * STAGE;
+      if (ks == nk - 1 && (tail_a || tail_w)) fix_tail(st);
+      // the stage NS - 1 ahead, the next tile's first ones after this one's last
+      if (iks == nk && !inext && more) {
+        sources(tb ^ 1);
+        inext = true;
+        iks = 0;
+      }
+      if (iks < nk) issue();
+      if (q == 0 && ss + 1 < nss) fetch_scales(ss + 1);
+      if (more && ks < kLookups) lookup(ks, L + step, tb ^ 1);
+      if (more && ks == last_ss) {
+        scales_of();
+        fetch_scales(0);
+      }
+      mma_step<BM, BN, WGM, WGN, kE4Row, FW>(acc, st, sc[sb], q, lane, wm, wn);
+      --flying;
+      cslot = cslot + 1 == NS ? 0 : cslot + 1;
+      if (q == 3 && ss + 1 < nss) {   // the other buffer was last read before this step's barrier
+        put_scales(ss + 1, sb ^ 1);
+        sb ^= 1;
+      }
+    }
+    if (more) {
+      put_scales(0, sb ^ 1);
+      sb ^= 1;
+    }
+    // acc[i][j][r] is C[wm*WM + i*32 + (r/4)*8 + lg*4 + r%4][wn*WN + j*32 + lr]; strips of 8 rows
+    // go through this wave's own LDS so that a lane stores 8 consecutive columns
+    float (*ep)[EPW] = strips[wave];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr) ep[lg * 4 + rr][j * 32 + lr] = acc[i][j][4 * h + rr];
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+          const int srow = (it * 64 + lane) / CG, cg = lane % CG;
+          const int rl = wm * WM + i * 32 + h * 8 + srow, col = n0 + wn * WN + cg * 8;
+          const float4 x = *(const float4*)&ep[srow][cg * 8];
+          const float4 y = *(const float4*)&ep[srow][cg * 8 + 4];
+          const float rs = trow[tb][rl];
+          float v[8] = {x.x * rs, x.y * rs, x.z * rs, x.w * rs, y.x * rs, y.y * rs, y.z * rs, y.w * rs};
+          if (p.sqrelu)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = sqrelu(v[e]);
+          if (rl < rows && col < p.N) store8(p, row0 + rl, col, v);
+        }
+      }
+    if (!more) break;
+    L += step;
+    inext = false;
+  }
+}
+
+template <int BM, int NS, int FW>
+hipError_t run_persist(const MxGemmParams& p, int mtiles, hipStream_t s) {
+  const int64_t tiles = (int64_t)mtiles * cdiv(p.N, 256);
+  if (tiles <= 0) return hipSuccess;
+  if (tiles > INT32_MAX / 512) return hipErrorInvalidValue;
+  const int grid = std::min(cdiv((int)tiles, kXcds) * kXcds, std::max(kXcds, persist_grid() / 2 / kXcds * kXcds));
+  hipLaunchKernelGGL((mx_persist_kernel<BM, NS, FW>), dim3(grid), dim3(512), 0, s, p);
+  return hipGetLastError();
+}
+
 template <int BM, int BN, int WGM, int WGN, int NS, int FA, int FW>
 hipError_t run_tile(const MxGemmParams& p, int mtiles, hipStream_t s) {
   const int64_t tiles = (int64_t)mtiles * cdiv(p.N, BN);
@@ -552,10 +841,27 @@ hipError_t run_dense(const MxGemmParams& p, hipStream_t s) {
   }
 }
 
+// Stages of the persistent tiles, beside the scales, strips and descriptions.
+template <int FW>
+constexpr int persist_stages(int BM) {
+  const int n = (kLds - 2 * 256 * 16 - 8 * kStripRows * 68 * 4 - 16 * BM - 64) /
+                ((8 * BM + kBits<FW> * 256) * 16);
+  return n > 4 ? 4 : n;
+}
+// Expert products: the persistent tiles where K fills their pipeline (8 steps, which the lookup of
+// the next tile needs too). Microseconds, persistent / a workgroup per tile: 49152 rows of 128
+// MXFP4 experts, K 2688, N 1856 365 / 393 and K 1856, N 2688 404 / 433; 24024 rows of 512 MXFP8
+// experts, K 1024, N 512 81 / 90, but K 512, N 1024 (4 steps, with the lookups after the last) 115
+// / 113.
 template <int FW>
 hipError_t run_grouped(const MxGemmParams& p, int mtiles, hipStream_t s) {
-  if (p.bm == 64) return run_shape<kE4Row, FW, 64>(p, mtiles, s);
-  if (p.bm == 128) return run_shape<kE4Row, FW, 128>(p, mtiles, s);
+  const bool walk = cdiv(p.K, 128) >= kPersistSteps;
+  if (p.bm == 64)
+    return walk ? run_persist<64, persist_stages<FW>(64), FW>(p, mtiles, s)
+                : run_shape<kE4Row, FW, 64>(p, mtiles, s);
+  if (p.bm == 128)
+    return walk ? run_persist<128, persist_stages<FW>(128), FW>(p, mtiles, s)
+                : run_shape<kE4Row, FW, 128>(p, mtiles, s);
   return hipErrorInvalidValue;
 }
 

@@ -212,6 +212,18 @@ LAYERS = {
                                 expert_dtype="mxfp4"),
     "mxfp8_long": mi.LayerConfig("mxfp8_long", T=700, H=2080, E=8, k=3, I=1184, I_shared=96,
                                  expert_dtype="mxfp8"),
+    # K of 9 steps, the last a quarter: workgroups that walk several tiles, of 64 and of 128 rows
+    "mxfp4_walk64": mi.LayerConfig("mxfp4_walk64", T=1500, H=1056, E=64, k=3, I=1056,
+                                   expert_dtype="mxfp4"),
+    "mxfp8_walk64": mi.LayerConfig("mxfp8_walk64", T=1500, H=1056, E=64, k=3, I=1056,
+                                   expert_dtype="mxfp8"),
+    "mxfp4_walk128": mi.LayerConfig("mxfp4_walk128", T=4500, H=1056, E=8, k=3, I=1056,
+                                    expert_dtype="mxfp4"),
+    "mxfp8_walk128": mi.LayerConfig("mxfp8_walk128", T=4500, H=1056, E=8, k=3, I=1056,
+                                    expert_dtype="mxfp8"),
+    # the fewest steps of such a K and more experts than two waves' lanes
+    "mxfp4_walk_wide": mi.LayerConfig("mxfp4_walk_wide", T=800, H=1024, E=200, k=8, I=1024,
+                                      expert_dtype="mxfp4"),
     "latent_mxfp4": mi.LayerConfig("latent_mxfp4", T=90, H=256, E=64, k=8, I=64, latent=96,
                                    I_shared=80, expert_dtype="mxfp4"),
 }
