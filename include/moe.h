@@ -184,8 +184,8 @@ int32_t moe_layer_forward_static(const moe_desc_t *desc, const moe_weights_t *w,
  * nine: for single sequences and small decode batches, whose time is launches and not bytes.
  * Arguments, formats, roundings and errors as moe_layer_forward, with these differences:
  *   - T <= MOE_FEW_TOKENS and act_dtype MOE_BF16, and for 8- and 4-bit experts T * D and T * I
- *     <= 65536, D (H, or latent) and I rounded up to multiples of 128, else MOE_ERR_UNSUPPORTED; flags: MOE_PATH_AUTO with or without
- *     MOE_ROUTING_GIVEN, else MOE_ERR_INVALID_ARG.
+ *     <= 65536, D (H, or latent) and I rounded up to multiples of 128, else MOE_ERR_UNSUPPORTED.
+ *   - flags: MOE_PATH_AUTO with or without MOE_ROUTING_GIVEN, else MOE_ERR_INVALID_ARG.
  *   - Workspace: moe_few_workspace_size bytes; its contents need no preparation and are not kept
  *     between calls.
  *   - The router's logits are summed in fp64 and rounded to fp32, and sums run in another order

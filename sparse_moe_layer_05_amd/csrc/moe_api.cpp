@@ -36,6 +36,7 @@ struct Plan {
   int lchunk = 0;    // columns of a range (tiles)
   size_t xpart = 0;  // its fp32 slabs [lsplit][T][L]
   bool y32 = false;  // tiles of block-scaled experts: the experts' rows Y are kept in fp32
+  size_t z_lo = 0;   // ... and, without a shared expert, what rounding z to bf16 left over [T][L]
   int ssplit = 1;    // K ranges of the shared expert's down projection on the decode path (plain
                      // layer): fp32 slabs [ssplit][T][H] after the pair rows of Y
 };
@@ -143,8 +144,11 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
       // (1001 tokens, H 4096, L 1024: 64 tiles, 62 us uncut)
       router_split(p.T, p.L, p.H, &p.lsplit, &p.lchunk);
       if (p.lsplit > 1) p.xpart = take((size_t)p.lsplit * Tz * (size_t)p.L * 4);
-      // the gated sum z is rounded to bf16 on its way to W_out: its terms are not rounded as well
+      // the gated sum z is rounded to bf16 on its way to W_out: its terms are not rounded as well.
+      // Without a shared expert the product's second operand pair is free and takes what that
+      // rounding left over (1001 tokens, L 1024: y 2.8e-3 -> 2.4e-3 off, 295 -> 309 us).
       p.y32 = true;
+      if (!p.Is) p.z_lo = take(Tz * (size_t)p.L * 2);
     }
   }
   p.h = take(P * (size_t)p.I * ea);
@@ -632,9 +636,14 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
                            (int64_t)T * H));
   } else {
     void* z = base + pl.z;
+    void* z_lo = pl.z_lo ? base + pl.z_lo : nullptr;
     {
       MOE_SPAN("combine:z");
-      MOE_TRY(launch_combine(Y, y_elt, D, nullptr, 0, pos, gates, T, L, k, z, act, L, s));
+      if (z_lo)
+        MOE_TRY(launch_combine_pair((const float*)Y, pos, gates, T, L, k, (uint16_t*)z,
+                                    (uint16_t*)z_lo, s));
+      else
+        MOE_TRY(launch_combine(Y, y_elt, D, nullptr, 0, pos, gates, T, L, k, z, act, L, s));
     }
     if (Is) {
       {
@@ -647,6 +656,10 @@ int32_t forward(const moe_desc_t* d, const moe_weights_t* w, void* y, void* ws, 
     } else if (stream_path) {
       MOE_SPAN("stream:latent_out");
       MOE_TRY(stream_dense(z, L, w->W_out, H, L, T, y, H, kStoreBF16, s));
+    } else if (z_lo) {
+      MOE_SPAN("gemm_bf16_store:latent_out");
+      MOE_TRY(dense(act, act, Epi::Store, z, L, w->W_out, L, y, H, T, H, L, s, z_lo, L, w->W_out, L,
+                    L));
     } else {
       MOE_SPAN(act == Elt::F32 ? "gemm_f32_store:latent_out" : "gemm_bf16_store:latent_out");
       MOE_TRY(dense(act, act, Epi::Store, z, L, w->W_out, L, y, H, T, H, L, s));

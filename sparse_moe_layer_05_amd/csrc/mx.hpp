@@ -45,6 +45,10 @@ struct MxGemmParams {
 // (every expert's last tile is partly empty): LatentMoE, 47 rows an expert, 308 us per layer
 // against 317 on 128; Nano, 384 rows, 1480 against 1261.
 inline int mx_group_bm(int P, int E) { return P <= 96 * (int64_t)E ? 64 : 128; }
+// The gated sum of the experts' fp32 rows, out[t] + out_lo[t] = sum_j gates[t, j] Y[pos[t, j]] (all
+// of D columns): rounded to bf16, and what that left over, in bf16 too.
+hipError_t launch_combine_pair(const float* Y, const int32_t* pos, const float* gates, int T,
+                               int D, int k, uint16_t* out, uint16_t* out_lo, hipStream_t s);
 hipError_t launch_mx_gemm(Elt a, Elt w, const MxGemmParams& p, int max_mtiles, hipStream_t s);
 
 }  // namespace moe

@@ -419,14 +419,15 @@ __global__ __launch_bounds__(CH) void dispatch_scatter(const int32_t* __restrict
 // ---------------------------------------------------------------------------------- combine
 // One workgroup per token; each thread owns 8 consecutive columns (one 16-byte bf16 load or two
 // fp32 loads per source row). Sum order: S (fp32; its ns slabs in order) first, then j = 0..k-1.
-template <Elt YT, Elt OT>
+// LO: what the rounding of a bf16 result left over goes to out_lo, in bf16 too.
+template <Elt YT, Elt OT, bool LO = false>
 __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ Y, int64_t ldy,
                                                       const float* __restrict__ S, int64_t lds,
                                                       int ns, int64_t s_slab,
                                                       const int32_t* __restrict__ pos,
                                                       const float* __restrict__ gates, int T,
                                                       int D, int k, void* __restrict__ out,
-                                                      int64_t ldo) {
+                                                      int64_t ldo, uint16_t* __restrict__ out_lo) {
   // workgroup (t, y) covers columns [y * cpb, (y + 1) * cpb) of token t, cpb = D / gridDim.y
   // rounded up to whole 8-column groups of the block
   const int t = blockIdx.x;
@@ -491,6 +492,15 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ Y
       q.z = pack_bf16x2(acc[4], acc[5]);
       q.w = pack_bf16x2(acc[6], acc[7]);
       *(uint4*)((uint16_t*)out + (int64_t)t * ldo + c) = q;
+      if constexpr (LO) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          r[i] = pack_bf16x2(acc[2 * i] - bf16_bits_to_f32(w[i] & 0xFFFF),
+                             acc[2 * i + 1] - bf16_bits_to_f32(w[i] >> 16));
+        *(uint4*)(out_lo + (int64_t)t * ldo + c) = make_uint4(r[0], r[1], r[2], r[3]);
+      }
     } else {
       float* o = (float*)out + (int64_t)t * ldo + c;
       *(float4*)o = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -668,24 +678,41 @@ hipError_t launch_dispatch(const int32_t* idx, int T, int E, int k, int32_t* cou
   return hipGetLastError();
 }
 
+namespace {
+// Many tokens: one workgroup per token. Few tokens (decode): a token's columns are split over
+// workgroups of one wave, 512 columns each, so that enough of them run at once.
+void combine_launch_shape(int T, int D, dim3* grid, dim3* block) {
+  const bool few = T < 1024;
+  *block = dim3(few ? 64 : (D / 8 >= 256 ? 256 : ((D / 8 + 63) / 64) * 64));
+  *grid = dim3(T, few ? cdiv(D, 512) : 1);
+}
+}  // namespace
+
 hipError_t launch_combine(const void* Y, Elt y_elt, int64_t ldy, const float* S, int64_t lds,
                           const int32_t* pos, const float* gates, int T, int D, int k, void* out,
                           Elt out_elt, int64_t ldo, hipStream_t s, int ns, int64_t s_slab) {
   if (T <= 0) return hipSuccess;
   if (ns < 1 || (ns > 1 && !S)) return hipErrorInvalidValue;
-  // Many tokens: one workgroup per token. Few tokens (decode): a token's columns are split over
-  // workgroups of one wave, 512 columns each, so that enough of them run at once.
-  const bool few = T < 1024;
-  const int threads = few ? 64 : (D / 8 >= 256 ? 256 : ((D / 8 + 63) / 64) * 64);
-  const dim3 grid(T, few ? cdiv(D, 512) : 1), block(threads);
+  dim3 grid, block;
+  combine_launch_shape(T, D, &grid, &block);
   if (y_elt == Elt::BF16 && out_elt == Elt::BF16)
-    hipLaunchKernelGGL((combine_kernel<Elt::BF16, Elt::BF16>), grid, block, 0, s, Y, ldy, S, lds, ns, s_slab, pos, gates, T, D, k, out, ldo);
+    hipLaunchKernelGGL((combine_kernel<Elt::BF16, Elt::BF16>), grid, block, 0, s, Y, ldy, S, lds, ns, s_slab, pos, gates, T, D, k, out, ldo, nullptr);
   else if (y_elt == Elt::F32 && out_elt == Elt::BF16)
-    hipLaunchKernelGGL((combine_kernel<Elt::F32, Elt::BF16>), grid, block, 0, s, Y, ldy, S, lds, ns, s_slab, pos, gates, T, D, k, out, ldo);
+    hipLaunchKernelGGL((combine_kernel<Elt::F32, Elt::BF16>), grid, block, 0, s, Y, ldy, S, lds, ns, s_slab, pos, gates, T, D, k, out, ldo, nullptr);
   else if (y_elt == Elt::F32 && out_elt == Elt::F32)
-    hipLaunchKernelGGL((combine_kernel<Elt::F32, Elt::F32>), grid, block, 0, s, Y, ldy, S, lds, ns, s_slab, pos, gates, T, D, k, out, ldo);
+    hipLaunchKernelGGL((combine_kernel<Elt::F32, Elt::F32>), grid, block, 0, s, Y, ldy, S, lds, ns, s_slab, pos, gates, T, D, k, out, ldo, nullptr);
   else
     return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_pair(const float* Y, const int32_t* pos, const float* gates, int T,
+                               int D, int k, uint16_t* out, uint16_t* out_lo, hipStream_t s) {
+  if (T <= 0) return hipSuccess;
+  dim3 grid, block;
+  combine_launch_shape(T, D, &grid, &block);
+  hipLaunchKernelGGL((combine_kernel<Elt::F32, Elt::BF16, true>), grid, block, 0, s, Y, D, nullptr,
+                     0, 1, 0, pos, gates, T, D, k, out, D, out_lo);
   return hipGetLastError();
 }
 

@@ -302,3 +302,83 @@ def test_weights_quantised_on_the_gpu_through_the_layer_and_the_product():
     bound = (288 * 2.0 ** -23 + 7 * 2.0 ** -13) * (xv.abs() @ wv.abs().t()) \
         + 2.0 ** -8 * (xv @ wv.t()).abs()
     assert bool(((a.double() - xv @ wv.t()).abs() <= bound).all())
+
+
+# ------------------------------------------------------------------- other ways and sizes to call
+
+def test_layer_on_tiles_captured_on_another_stream_and_without_a_workspace():
+    cfg = mi.LayerConfig("cap", T=600, H=1056, E=8, k=3, I=1056, I_shared=96, expert_dtype="mxfp4")
+    dev = moe.to_device(mi.make_layer(cfg, seed=9))
+    layer, eager = (moe.layer_from(dev, 3, path="grouped_mx", expert_dtype="mxfp4") for _ in range(2))
+    want = eager().clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    layer(s)
+    s.synchronize()
+    assert torch.equal(layer.y, want)
+    static = moe.layer_from(dev, 3, path="grouped_mx", expert_dtype="mxfp4", no_alloc=True)
+    assert torch.equal(static(), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for i in range(4):
+        dev["x"].copy_(torch.randn(600, 1056, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.y, eager.y), i
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_conversion_past_32_bit_offsets(fmt):
+    """More than 2^31 elements: the last rows as when they are converted alone."""
+    rows, cols = (1 << 31) // 2048 + 3, 2048
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x[-5:] = torch.randn(5, cols, generator=g, device="cuda")
+    codes, scales = moe.mx_quantize(x, fmt)
+    c, s = moe.mx_quantize(x[-5:], fmt)
+    assert torch.equal(codes[-5:], c) and torch.equal(scales[-5:], s)
+    assert not bool(scales[:-5].any()) and not bool(codes[:5].any())
+    x.fill_(1.0)
+    moe.mx_dequantize(codes, scales, dtype=torch.bfloat16, out=x)
+    assert torch.equal(x[-5:], moe.mx_dequantize(c, s, dtype=torch.bfloat16))
+    assert not bool(x[:-5].any())
+
+
+@pytest.mark.parametrize("M,N", [(65535, 16), (1, 65520), (100, 65520)])
+def test_product_of_operands_near_2_gib(M, N):
+    """The bound of the accumulation as at the head of the file, on the last rows and columns."""
+    K = 32768
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def operand(rows):
+        c, s = moe.mx_quantize(torch.randn(min(rows, 64), K, generator=g, device="cuda"), "mxfp8")
+        n = -(-rows // c.shape[0])
+        c, s = c.repeat(n, 1)[:rows], s.repeat(n, 1)[:rows]
+        tail = moe.mx_quantize(torch.randn(min(rows, 48), K, generator=g, device="cuda"), "mxfp8")
+        c[-tail[0].shape[0]:], s[-tail[0].shape[0]:] = tail
+        return c, s
+
+    a, w = operand(M), operand(N)
+    out = moe.mx_gemm(*a, *w)[-48:, -48:].double()
+    x, v = (moe.mx_dequantize(c[-48:], s[-48:]).double() for c, s in (a, w))
+    exact = x @ v.t()
+    bound = (K * 2.0 ** -23 + 7 * 2.0 ** -13) * (x.abs() @ v.abs().t()) + 2.0 ** -8 * exact.abs()
+    assert bool(((out - exact).abs() <= bound).all())
+    assert float((out - exact).norm() / exact.norm()) <= 5e-3
+
+
+def test_experts_rows_near_2_gib():
+    """h of 2.1 GB in e4m3: the last tokens as in a call of their own with the same selection."""
+    cfg = mi.LayerConfig("long", T=131072, H=32, E=8, k=8, I=2016, expert_dtype="mxfp4")
+    dev = moe.to_device(mi.make_layer(cfg, seed=3))
+    rt = moe.alloc_routing(cfg.T, cfg.E, cfg.k, "cuda")
+    y = moe.layer_from(dev, 8, path="grouped_mx", routing=rt, expert_dtype="mxfp4")()[-70:]
+    given = {n: rt[n][-70:].contiguous() for n in ("idx", "gates")}
+    z = moe.layer_from(dict(dev, x=dev["x"][-70:].contiguous()), 8, path="grouped_mx",
+                       routing=given, routing_given=True, expert_dtype="mxfp4")()
+    y, z = y.double().cpu().numpy(), z.double().cpu().numpy()
+    assert np.abs(z).max() > 0 and rel(y, z) <= 5e-3
