@@ -10,7 +10,8 @@
 //
 // A lane takes 16 bytes at a time, so a block is shared by four lanes (bf16) or eight (fp32); its
 // maximum comes from two or three lane permutations, no LDS. Rows are contiguous, so a matrix is
-// one run of blocks. Each thread takes kIter such loads, all in flight together.
+// one run of blocks. Each thread takes kIter such loads, all in flight together. HBM bound: 29696 x
+// 2688 fp32 to MXFP4 (362 MB) 82 to 90 us, back 67 to 72 us (4.0 to 5.4 TB/s; a large copy 4.8).
 // Included once, by backward.hip: these kernels are part of that object, so that the library stays the
 // objects that its parts are linked from elsewhere (host code under the sanitizers).
 #pragma once
