@@ -281,7 +281,8 @@ __device__ __forceinline__ bool tile_of(const MxGemmParams& p, int L, int& g, in
 // scales, a dword per row. mid() is what a wave issues for later (the loads of a stage ahead): between
 // the two halves of K, where it goes out while the matrix core works on the first (with the scales'
 // layout: 8192 tokens of 128 MXFP4 experts 1218 -> 1202 us, 512 x 3712 x 2688 in 4 bits 15.0 -> 13.5
-// to 14.5), but before them where both halves' fragments would not fit beside the accumulators (256 x 256 in 8 bits: spills).
+// to 14.5), but before them where both halves' fragments would not fit beside the accumulators
+// (256 x 256 in 8 bits: spills).
 template <int B>
 __device__ __forceinline__ i32x8_t read_frag(const uint8_t* base, int row, int s, int lg) {
   constexpr int SL = B * 16;
