@@ -418,9 +418,11 @@ def bias_update(counts, b, gamma: float, target=None, stream=None) -> None:
 
 
 def _float_code(dtype: torch.dtype) -> int:
-    if dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"dtype {dtype} is neither float32 nor bfloat16")
-    return MOE_F32 if dtype == torch.float32 else MOE_BF16
+    if dtype is torch.bfloat16:
+        return MOE_BF16
+    if dtype is torch.float32:
+        return MOE_F32
+    raise ValueError(f"dtype {dtype} is neither float32 nor bfloat16")
 
 
 def _launch(fn, name, device, stream, *args):
@@ -436,7 +438,7 @@ def _launch(fn, name, device, stream, *args):
         raise ValueError(f"{name}: tensors are on {device}, the stream is on {stream.device}")
     else:
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == i:
+    if torch._C._cuda_getDevice() == i:     # (tensors on a GPU: it is initialised)
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(i):
@@ -449,17 +451,19 @@ def _mx_format(codes, scales, what):
     """(moe_dtype_t, element columns) of a block-scaled matrix, read off its shapes: one scale per
     32 columns, two MXFP4 elements or one MXFP8 element per byte."""
     cs, ss = codes.shape, scales.shape
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise ValueError(f"{what} and its scales must be uint8 tensors")
-    if not cs or cs[:-1] != ss[:-1] or scales.device != codes.device:
+    # (two dimensions without slices: a call's time is host time where rows are few)
+    same = cs[0] == ss[0] if len(cs) == len(ss) == 2 else cs[:-1] == ss[:-1]
+    if not cs or len(cs) != len(ss) or not same or scales.device != codes.device:
         raise ValueError(f"{what} {tuple(cs)} on {codes.device} and its scales {tuple(ss)} on "
                          f"{scales.device} do not belong together")
-    cols = MX_BLOCK * ss[-1]
-    if cols and cs[-1] * 2 == cols:
+    n, cols = cs[-1], MX_BLOCK * ss[-1]
+    if cols and n * 2 == cols:
         return MOE_MXFP4, cols
-    if cols and cs[-1] == cols:
+    if cols and n == cols:
         return MOE_MXFP8, cols
-    raise ValueError(f"{what}: {cs[-1]} bytes and {ss[-1]} scales a row are neither MXFP4 nor MXFP8")
+    raise ValueError(f"{what}: {n} bytes and {ss[-1]} scales a row are neither MXFP4 nor MXFP8")
 
 
 def mx_quantize(x, fmt="mxfp4", *, codes=None, scales=None, stream=None):
@@ -476,12 +480,12 @@ def mx_quantize(x, fmt="mxfp4", *, codes=None, scales=None, stream=None):
     sshape = lead + (cols // MX_BLOCK,)
     made = []
     if codes is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
+        codes = x.new_empty(cshape, dtype=torch.uint8)
         made.append(codes)
     else:
         _need(codes, cshape, "codes", torch.uint8, dev)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
+        scales = x.new_empty(sshape, dtype=torch.uint8)
         made.append(scales)
     else:
         _need(scales, sshape, "scales", torch.uint8, dev)
@@ -499,7 +503,7 @@ def mx_dequantize(codes, scales, *, dtype=torch.float32, out=None, stream=None):
     shape, dev = codes.shape[:-1] + (cols,), codes.device
     made = out is None
     if made:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = codes.new_empty(shape, dtype=dtype)
     else:
         _need(out, shape, "out", dtype, dev)
     _launch(lib().moe_mx_dequantize, "moe_mx_dequantize", dev, stream, _p(codes), _p(scales), fmt,
@@ -522,7 +526,7 @@ def mx_gemm(a, a_scales, w, w_scales, *, out_dtype=torch.bfloat16, out=None, str
     dt, M, N = _float_code(out_dtype), a.shape[0], w.shape[0]
     made = out is None
     if made:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = a.new_empty((M, N), dtype=out_dtype)
     else:
         _need(out, (M, N), "out", out_dtype, dev)
     _launch(lib().moe_mx_gemm, "moe_mx_gemm", dev, stream, _p(a), _p(a_scales), fa, _p(w),

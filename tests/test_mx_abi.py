@@ -73,7 +73,7 @@ def test_grouped_block_scaled_descriptors():
 
 def test_binding_refuses_what_is_not_block_scaled():
     u8 = torch.uint8
-    z = lambda *s: torch.zeros(*s, dtype=u8)  # noqa: E731
+    z = lambda *s: torch.zeros(s, dtype=u8)  # noqa: E731
     for call in (
             lambda: moe.mx_quantize(torch.zeros(4, 48)),                       # no whole blocks
             lambda: moe.mx_quantize(torch.zeros(4, 0)),
@@ -83,6 +83,8 @@ def test_binding_refuses_what_is_not_block_scaled():
             lambda: moe.mx_dequantize(z(4, 33), z(4, 1)),                      # 33 bytes a block
             lambda: moe.mx_dequantize(z(4, 32), z(3, 1)),
             lambda: moe.mx_dequantize(z(4, 32), z(4, 1)),                      # not on a GPU
+            lambda: moe.mx_dequantize(z(32), z()),                             # no scale dimension
+            lambda: moe.mx_dequantize(z(4, 32), z(4)),
             lambda: moe.mx_dequantize(torch.zeros(4, 32), z(4, 1)),
             lambda: moe.mx_dequantize(z(4, 32), z(4, 1), dtype=torch.float16),
             lambda: moe.mx_gemm(z(4, 32), z(4, 1), z(16, 64), z(16, 2)),       # K differs
