@@ -815,7 +815,11 @@ constexpr int tile_bn(int bm, int w_bits) { return bm == 256 ? 256 : (bm == 128 
 template <int FA, int FW, int BM>
 hipError_t run_shape(const MxGemmParams& p, int mtiles, hipStream_t s) {
   constexpr int BN = tile_bn(BM, kBits<FW>);
-  constexpr int NS = stages<FA, FW>(BM, BN, BM == 256 ? kLds : kLds / 2);
+  // Workgroups of a CU: one of 8 waves, two, or, for the short K of expert products on 64 rows (few
+  // steps to wait for between a tile's first loads and its result), three of fewer stages: 24024
+  // rows of 512 MXFP8 experts, K 512, N 1024: 106 us with 2 stages each, 114 as two with 3.
+  constexpr int CU = BM == 256 ? 1 : FA == kE4Row && BM == 64 ? 3 : 2;
+  constexpr int NS = stages<FA, FW>(BM, BN, kLds / CU);
   return run_tile<BM, BN, 2, BM == 256 ? 4 : 2, NS, FA, FW>(p, mtiles, s);
 }
 
@@ -869,7 +873,7 @@ constexpr int persist_stages(int BM) {
 // the next tile needs too). Microseconds, persistent / a workgroup per tile: 49152 rows of 128
 // MXFP4 experts, K 2688, N 1856 365 / 393 and K 1856, N 2688 404 / 433; 24024 rows of 512 MXFP8
 // experts, K 1024, N 512 81 / 90, but K 512, N 1024 (4 steps, with the lookups after the last) 115
-// / 113.
+// / 106.
 template <int FW>
 hipError_t run_grouped(const MxGemmParams& p, int mtiles, hipStream_t s) {
   const bool walk = cdiv(p.K, 128) >= kPersistSteps;
