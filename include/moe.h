@@ -22,6 +22,7 @@
  *   expert  f_e(u) = relu(u W_up[e]^T)^2 W_down[e]^T        (squared-ReLU, no gate, no bias)
  *   routed  r = sum_j g_j f_{idx_j}(u)                      (fixed j order: deterministic)
  *   y_t     = r, or r W_out^T (LatentMoE);  y_t += relu(x_t Ws_up^T)^2 Ws_down^T if I_shared > 0
+ * A NaN in x_t makes y_t NaN and no other row (relu keeps NaN).
  *
  * Conventions shared by every entry point:
  *   - Tensor pointers are DEVICE pointers to row-major, contiguous arrays, 16-byte aligned, owned
@@ -70,8 +71,10 @@ extern "C" {
  * 2^(code - 127); the elements are E2M1 (values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives;
  * two per byte, element 2i in the low nibble of byte i) or E4M3. They are the gfx950-native
  * counterpart of the micro-block scaled FP4 of "NVIDIA Nemotron 3: Efficient and Open
- * Intelligence", section 2.4. Scale code 255 (NaN) is not supported: a block carrying it makes
- * its outputs undefined. */
+ * Intelligence", section 2.4. A block of scale code 255 (what moe_mx_quantize makes of a block that
+ * holds a NaN or an infinity) stands for NaN: y is NaN wherever the block enters it, all of y of a
+ * token that selects the expert for W_up (and for W_down under LatentMoE), the block's own column
+ * of it for W_down. */
 typedef enum {
   MOE_F32 = 0,      /* IEEE binary32 */
   MOE_BF16 = 1,     /* bfloat16 */

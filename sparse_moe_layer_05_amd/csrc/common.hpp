@@ -34,7 +34,8 @@ __device__ __forceinline__ uint32_t cvt_fp8x2(float a, float b) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
 }
 
-__device__ __forceinline__ float sqrelu(float a) { return a > 0.f ? a * a : 0.f; }
+// relu(a)^2; NaN stays NaN (a > 0 ? a * a : 0 would make it 0).
+__device__ __forceinline__ float sqrelu(float a) { return a <= 0.f ? 0.f : a * a; }
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
