@@ -51,9 +51,10 @@
  *   - Expert weights of 8 or 4 bits (MOE_FP8_E4M3, MOE_MXFP4, MOE_MXFP8): the expert input rows
  *     and the rows of h = relu(u W_up^T)^2 (rounded to bf16) are quantised per row to e4m3 with
  *     scale amax / 448 before they meet the weights, as in "Nemotron 3 Nano：開放高效的 MoE 混合
- *     Mamba-Transformer 智能體推理模型", section 4 (FP8 expert weights). MOE_MXFP4 / MOE_MXFP8
- *     run on the decode (stream) path, whatever T is, unless MOE_MX_GROUPED asks for their
- *     matrix-core tiles; MOE_PATH_GROUPED is unsupported for them.
+ *     Mamba-Transformer 智能體推理模型", section 4 (FP8 expert weights); the scale is 2^-127 where
+ *     448 / amax is past fp32. MOE_MXFP4 / MOE_MXFP8 run on the decode (stream) path, whatever T
+ *     is, unless MOE_MX_GROUPED asks for their matrix-core tiles; MOE_PATH_GROUPED is unsupported
+ *     for them.
  */
 #ifndef MOE_MI355X_H
 #define MOE_MI355X_H

@@ -34,6 +34,20 @@ __device__ __forceinline__ uint32_t cvt_fp8x2(float a, float b) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
 }
 
+// How a row whose largest magnitude is m meets 8- and 4-bit experts: codes e4m3(v * up), values
+// code * down; up = 448 / m and down = m / 448, or 1 and 1 for a row of zeros. Below m = 1.3e-36
+// 448 / m is past fp32 (a zero times it would be NaN): 2^127 and 2^-127 there, codes up to 224, and
+// the smallest bf16 value, 2^-133, still has a normal code.
+struct RowScale {
+  float up, down;
+};
+__device__ __forceinline__ RowScale row_scale_e4m3(float m) {
+  if (!(m > 0.f)) return {1.f, 1.f};
+  const float up = 448.f / m;
+  if (up == __builtin_inff()) return {0x1p127f, 0x1p-127f};
+  return {up, m / 448.f};
+}
+
 // relu(a)^2; NaN stays NaN (a > 0 ? a * a : 0 would make it 0).
 __device__ __forceinline__ float sqrelu(float a) { return a <= 0.f ? 0.f : a * a; }
 

@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
       select_topk<NPER, true>(key, sc, lane, p.E, p.k, idx_l + tk * p.k, gates_l + tk * p.k);
     }
     if (ok) atomicOr(&emask[idx_l[tk * p.k + lane]], 1u << tk);
-    // its row: bf16 as it is, or e4m3 codes with scale amax / 448 (1 for a zero row)
+    // its row: bf16 as it is, or e4m3 codes
     const uint16_t* row = in + (int64_t)tk * p.D;
     float inv = 1.f;
     if constexpr (M::narrow) {
@@ -369,8 +369,9 @@ __global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
       }
 #pragma unroll
       for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-      inv = m > 0.f ? 448.f / m : 1.f;
-      if (lane == 0) row_scale[tk] = m > 0.f ? m / 448.f : 1.f;
+      const RowScale rs = row_scale_e4m3(m);
+      inv = rs.up;
+      if (lane == 0) row_scale[tk] = rs.down;
     }
     if constexpr (XLDS)
       for (int c = lane * 8; c < ldx / 2 - 8; c += 512) {
@@ -626,8 +627,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
     x.wx = M::mx ? (const uint8_t*)p.s_down + (int64_t)x.row * (p.I / 32) : nullptr;
     x.scale = p.gate_m[x.slot * TB + r];
     if constexpr (M::narrow) {
-      const float m = __uint_as_float(p.hmax[x.slot * TB + src]);
-      x.scale *= m > 0.f ? m / 448.f : 1.f;
+      x.scale *= row_scale_e4m3(__uint_as_float(p.hmax[x.slot * TB + src])).down;
       x.a = (const uint16_t*)(hq + (first_row[x.slot - pass_slot] +
                                     __popc(mask & ((1u << src) - 1))) * ldh);
       x.a2 = nullptr;
@@ -742,8 +742,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
         for (uint32_t m = mask; m; m &= m - 1, ++j) {   // rows dealt to the waves
           if (j % kDownWaves != wave) continue;
           const int tk = __ffs(m) - 1;
-          const float top = __uint_as_float(p.hmax[s * TB + tk]);
-          const float inv = top > 0.f ? 448.f / top : 1.f;
+          const float inv = row_scale_e4m3(__uint_as_float(p.hmax[s * TB + tk])).up;
           const uint16_t* h = p.h + ((int64_t)s * p.T + tk) * p.I;
           for (int c = lane * 8; c < ldh / 2 - 8; c += 512) {
             uint4 v = make_uint4(0, 0, 0, 0);

@@ -543,9 +543,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const uint16_t* __restr
   for (int c = (kQuantRegs * 64 + lane) * 8; c < H; c += 64 * 8) amax8(*(const uint4*)(row + c));
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  const float amax = m;
-  const float inv = amax > 0.f ? 448.f / amax : 1.f;   // codes = e4m3(x * inv)
-  if (lane == 0) scale[t] = amax > 0.f ? amax / 448.f : 1.f;
+  const RowScale rs = row_scale_e4m3(m);
+  const float inv = rs.up;   // codes = e4m3(x * inv)
+  if (lane == 0) scale[t] = rs.down;
   auto codes8 = [&](const uint4 v, int c) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[2];
