@@ -145,6 +145,8 @@ def _used_on(stream, *tensors):
         return
     for t in tensors:
         if t is not None:
+            if not isinstance(stream, torch.Stream):   # another library's: see _launch
+                stream = torch.cuda.ExternalStream(stream.cuda_stream, device=t.device)
             t.record_stream(stream)
 
 
@@ -427,16 +429,18 @@ def _float_code(dtype: torch.dtype) -> int:
 
 def _launch(fn, name, device, stream, *args):
     """fn(*args, stream) on `device`, whatever device is current, on `stream` (None: the device's
-    current stream). The stream's raw handle is read directly: a torch.cuda.Stream object per call
+    current stream; else a torch stream, or any object whose `cuda_stream` is the raw handle of a
+    stream of that device). The raw handle is read directly: a torch.cuda.Stream object per call
     costs more host time than the launch."""
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors are on {device}, expected a GPU")
     i = device.index
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(i)
-    elif stream.device.index != i:
-        raise ValueError(f"{name}: tensors are on {device}, the stream is on {stream.device}")
     else:
+        at = getattr(stream, "device", device)
+        if at.index != i:
+            raise ValueError(f"{name}: tensors are on {device}, the stream is on {at}")
         raw = stream.cuda_stream
     if torch._C._cuda_getDevice() == i:     # (tensors on a GPU: it is initialised)
         rc = fn(*args, raw)
