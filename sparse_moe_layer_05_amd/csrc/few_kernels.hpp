@@ -776,13 +776,18 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       __hip_atomic_store(slab + mine * 256 + i, v[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // the slab is written through to memory (agent scope); wait for that, then count (a release
-    // fence would write back the whole L2 instead: 18 us more on a Nano-shaped token)
+    // Release by hand: an agent-scope store is written through to where every die reads it, so the
+    // slab is there once the wait below is over, and the statement keeps the compiler from moving
+    // the stores past it; then the part is counted. (A release fence would write back the whole
+    // L2 too: 18 us more on a Nano-shaped token.) The acquire is the part that reads the slabs: no
+    // load of them may go before the count, and none may be served from what this die's caches
+    // held earlier.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     int before = 0;
     if (lane == 0)
       before = __hip_atomic_fetch_add(p.joined + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (__builtin_amdgcn_readfirstlane(before) != parts - 1) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = 0.f;
     for (int q = 0; q < parts; ++q)
