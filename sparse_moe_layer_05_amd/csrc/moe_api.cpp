@@ -36,7 +36,7 @@ struct Plan {
   int lchunk = 0;    // columns of a range (tiles)
   size_t xpart = 0;  // its fp32 slabs [lsplit][T][L]
   bool y32 = false;  // tiles of block-scaled experts: the experts' rows Y are kept in fp32
-  size_t z_lo = 0;   // ... and, without a shared expert, what rounding z to bf16 left over [T][L]
+  size_t z_lo = 0;   // ... and, LatentMoE without a shared expert, what rounding z left over [T][L]
   int ssplit = 1;    // K ranges of the shared expert's down projection on the decode path (plain
                      // layer): fp32 slabs [ssplit][T][H] after the pair rows of Y
 };
@@ -99,7 +99,13 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
   }
   // fp32 grouped launches: 16-row tiles when experts average at most 16 rows, else 64
   p.bm = p.act == Elt::F32 ? ((int64_t)p.T * p.k <= 16LL * p.E ? 16 : 64) : kGroupBM;
-  if (mx_grouped) p.bm = mx_group_bm(p.P, p.E);
+  if (mx_grouped) {
+    p.bm = mx_group_bm(p.P, p.E);
+    // The terms of the gated sum are not rounded, as on the decode path: in bf16 they cost as much
+    // precision as y's own rounding (2048 Nano tokens without a shared expert, MXFP4: y 2.47e-3 off,
+    // 1.82e-3 with fp32 rows and on the decode path alike; 8192 tokens 1226 -> 1335 us).
+    p.y32 = true;
+  }
 
   const size_t ea = p.act == Elt::F32 ? 4 : 2;  // activation / intermediate element bytes
   size_t off = 0;
@@ -144,10 +150,9 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
       // (1001 tokens, H 4096, L 1024: 64 tiles, 62 us uncut)
       router_split(p.T, p.L, p.H, &p.lsplit, &p.lchunk);
       if (p.lsplit > 1) p.xpart = take((size_t)p.lsplit * Tz * (size_t)p.L * 4);
-      // the gated sum z is rounded to bf16 on its way to W_out: its terms are not rounded as well.
-      // Without a shared expert the product's second operand pair is free and takes what that
-      // rounding left over (1001 tokens, L 1024: y 2.8e-3 -> 2.4e-3 off, 295 -> 309 us).
-      p.y32 = true;
+      // The gated sum z is rounded to bf16 on its way to W_out. Without a shared expert the
+      // product's second operand pair is free and takes what that rounding left over (1001 tokens,
+      // L 1024: y 2.8e-3 -> 2.4e-3 off, 295 -> 309 us).
       if (!p.Is) p.z_lo = take(Tz * (size_t)p.L * 2);
     }
   }
