@@ -19,7 +19,7 @@
 //
 // Products: the weights are the matrix core's first operand (16 rows), loaded from HBM straight to
 // registers and multiplied as bf16: e4m3 and E2M1 elements times their block scales are bf16
-// numbers, and so are e4m3 activation codes, while the 8- and 4-bit instructions cut products (13
+// numbers (but for E4M3 elements below 2^-133, in blocks of scale code 2 or less, which round), and so are e4m3 activation codes, while the 8- and 4-bit instructions cut products (13
 // bits below the largest of eight) and thereby move roundings of h, one in some hundred rows its
 // quantisation scale and with it 4% of the row. The conversions hide under the loads. Waves split
 // K and join in LDS in wave order: results are deterministic.
@@ -27,7 +27,12 @@
 // Formats as on the decode path: 8- and 4-bit experts meet rows quantised per row to e4m3 (scale
 // amax / 448), h rounded to bf16 first. Where the definition does not round, intermediates are
 // kept as the sum of two bf16 (16 bits; the shared expert's h, a bf16 expert's h, LatentMoE's z),
-// multiplied in two instructions by the weights that are in registers anyway.
+// multiplied in two instructions by the weights that are in registers anyway. Where it rounds to bf16
+// and a row's largest element then sets its e4m3 scale (h of 8- and 4-bit experts, LatentMoE's u), the
+// sum is widened to fp64 every 256 products and rounded once: in fp32 some hundred rows held one
+// whose scale, and with it most of its codes, fell on the other side of a bf16 border (6 tokens
+// through LatentMoE with e4m3 experts: y 4.8e-3 off, 1.66e-3 now; 0 to 1 us a call). What fp32 sums
+// of 256 leave makes that rarer, not impossible.
 //
 // Router: logits are summed in fp64 and rounded to fp32, so that the selection does not depend on
 // the order of the sum; scores and keys as in the router kernels.
@@ -36,6 +41,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "few.hpp"
@@ -135,13 +141,30 @@ __device__ __forceinline__ void store_pair(uint16_t* hi, uint16_t* lo, int64_t a
                  pack_bf16x2(v[2] - bf16_bits_to_f32(h.y & 0xFFFF), v[3] - bf16_bits_to_f32(h.y >> 16)));
 }
 
-// acc += W[row, steps s0 .. s1) * (A + A2) of bf16 rows in memory, U steps of loads in flight.
+// Four sums of one lane. A Sum of doubles takes the matrix core's fp32 sums of a batch of steps at a
+// time, each batch from zero: where a value is rounded to bf16 and the largest of them sets its
+// row's scale, a sum that rounds with every instruction now and then falls on the other side of a
+// bf16 border, and most codes of the row move with it.
+template <class T> struct Sum {
+  T v[4] = {0, 0, 0, 0};
+  __device__ __forceinline__ f32x4_t start() const {   // what a batch begins with
+    if constexpr (sizeof(T) == 4) return f32x4_t{v[0], v[1], v[2], v[3]};
+    else return f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void take(f32x4_t acc) {   // and what it ends with
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = sizeof(T) == 4 ? (T)acc[i] : v[i] + (T)acc[i];
+  }
+};
+__device__ __forceinline__ double sqrelu(double a) { return a <= 0.0 ? 0.0 : a * a; }
+using moe::sqrelu;
+
+// sum += W[row, steps s0 .. s1) * (A + A2) of bf16 rows in memory, U steps of loads in flight.
 // No branch on the steps past the end: loads whose use is conditional are moved to it, one by
 // one, instead of being in flight together.
-template <int U, bool LO>
-__device__ __forceinline__ f32x4_t dot_rows(const uint16_t* w, const uint16_t* a,
-                                            const uint16_t* a2, int K, int s0, int s1, int g,
-                                            f32x4_t acc) {
+template <int U, bool LO, class T>
+__device__ __forceinline__ void dot_rows(const uint16_t* w, const uint16_t* a, const uint16_t* a2,
+                                         int K, int s0, int s1, int g, Sum<T>& sum) {
   const int kend = min(K, s1 * 32);
   for (int s = s0; s < s1; s += U) {
     uint4 wf[U], af[U], bf[LO ? U : 1];
@@ -152,48 +175,50 @@ __device__ __forceinline__ f32x4_t dot_rows(const uint16_t* w, const uint16_t* a
       af[q] = *(const uint4*)(a + at);
       if constexpr (LO) bf[q] = *(const uint4*)(a2 + at);
     }
+    f32x4_t acc = sum.start();
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       if ((s + q) * 32 + 8 * g >= kend) wf[q] = make_uint4(0, 0, 0, 0);
       acc = mul(__builtin_bit_cast(bf16x8_t, wf[q]), af[q], acc);
       if constexpr (LO) acc = mul(__builtin_bit_cast(bf16x8_t, wf[q]), bf[q], acc);
     }
+    sum.take(acc);
   }
-  return acc;
 }
 
 // out[t][n0 .. n0 + 15] = act(A1[t] . W1[n] + A2[t] . W2[n]) by the NW waves of a workgroup, each
-// over a contiguous share of the steps. LO: the activations are pairs. out_lo: so is the result.
+// over a contiguous share of the steps, summed in S. LO: the activations are pairs. out_lo: so is the
+// result.
 struct Dense {
   const uint16_t *A1, *A1lo, *W1, *A2, *A2lo, *W2;
   int K1, K2, N, T, sq;
   uint16_t *out, *out_lo;
 };
-template <int NW, int U, bool LO>
-__device__ __forceinline__ void dense_unit(const Dense& d, int n0, float (*part)[16][17]) {
+template <int NW, int U, bool LO, class S>
+__device__ __forceinline__ void dense_unit(const Dense& d, int n0, S (*part)[16][17]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int t = min(r, d.T - 1);
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  Sum<S> acc;
   const int st1 = cdiv(d.K1, 32), st = st1 + cdiv(d.K2, 32), per = cdiv(st, NW);
   const int lo = min(st, wave * per), hi = min(st, lo + per);
   if (lo < st1)
-    acc = dot_rows<U, LO>(d.W1 + (int64_t)(n0 + r) * d.K1, d.A1 + (int64_t)t * d.K1,
-                          d.A1lo + (int64_t)t * d.K1, d.K1, lo, min(hi, st1), g, acc);
+    dot_rows<U, LO>(d.W1 + (int64_t)(n0 + r) * d.K1, d.A1 + (int64_t)t * d.K1,
+                    d.A1lo + (int64_t)t * d.K1, d.K1, lo, min(hi, st1), g, acc);
   if (hi > st1)
-    acc = dot_rows<U, LO>(d.W2 + (int64_t)(n0 + r) * d.K2, d.A2 + (int64_t)t * d.K2,
-                          d.A2lo + (int64_t)t * d.K2, d.K2, max(lo, st1) - st1, hi - st1, g, acc);
+    dot_rows<U, LO>(d.W2 + (int64_t)(n0 + r) * d.K2, d.A2 + (int64_t)t * d.K2,
+                    d.A2lo + (int64_t)t * d.K2, d.K2, max(lo, st1) - st1, hi - st1, g, acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) part[wave][r][4 * g + i] = acc[i];
+  for (int i = 0; i < 4; ++i) part[wave][r][4 * g + i] = acc.v[i];
   __syncthreads();
   if (threadIdx.x < 64 && r < d.T) {
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i] = part[0][r][4 * g + i];
+      S x = part[0][r][4 * g + i];
 #pragma unroll
-      for (int q = 1; q < NW; ++q) v[i] += part[q][r][4 * g + i];
-      if (d.sq) v[i] = sqrelu(v[i]);
+      for (int q = 1; q < NW; ++q) x += part[q][r][4 * g + i];
+      v[i] = (float)(d.sq ? sqrelu(x) : x);
     }
     const int64_t at = (int64_t)r * d.N + n0 + 4 * g;
     if (d.out_lo)
@@ -208,7 +233,7 @@ __device__ __forceinline__ void dense_unit(const Dense& d, int n0, float (*part)
 // of W_in. Also clears what the later launches raise or count.
 template <int TT>
 __global__ __launch_bounds__(256) void few_front(FewParams p) {
-  __shared__ float part[4][16][17];
+  __shared__ double part[4][16][17];   // u is rounded to bf16
   __shared__ double red[4][TT];
   const int tid = threadIdx.x;
   const int nr = p.given ? 0 : p.E;
@@ -431,7 +456,10 @@ __global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
       }
       from = min(shi, slo + SS);
     }
-    acc = dot_rows<4, false>(p.Ws_up + (int64_t)(16 * n + r) * p.H, srow, srow, p.H, from, shi, g, acc);
+    Sum<float> sum;
+    sum.take(acc);
+    dot_rows<4, false>(p.Ws_up + (int64_t)(16 * n + r) * p.H, srow, srow, p.H, from, shi, g, sum);
+    acc = sum.start();
     constexpr int half = NWV / 2;   // the upper half's sums, then the lower's added to them
     if (wave >= half)
 #pragma unroll
@@ -476,7 +504,7 @@ __global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
   bool more = u + stride < total;
   if (more) nxt = resolve(u + stride);
   int b = 0;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  Sum<std::conditional_t<M::narrow, double, float>> sum;   // (bf16 experts' h is kept as a pair)
   // none: the same number of loads, all of the row's start
   auto issue = [&](const Unit& x, int bb, WStep<F>* w, bool none) {
     const int s = none ? 0 : bb * U, to = none ? 0 : p.D;
@@ -489,6 +517,7 @@ __global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
     if (last && more) src = nxt;
     // always the same number of loads, so that the wait for a batch leaves the next in flight
     issue(src, last ? 0 : b + 1, wn, last && !more);
+    f32x4_t acc = sum.start();
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       mask_step<F>(wc[q], b * U + q, p.D, g);
@@ -500,6 +529,7 @@ __global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
         acc = mul(wfrag<F>(wc[q], j), a, acc);
       }
     }
+    sum.take(acc);
     if (!last) {
       ++b;
       return true;
@@ -509,13 +539,11 @@ __global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i] = acc[i];
-      if constexpr (F == Elt::FP8)
-        v[i] *= row_scale[t] * ((const float*)p.s_up)[(int64_t)cur.e * p.I + cur.n0 + 4 * g + i];
-      else if constexpr (M::mx)
-        v[i] *= row_scale[t];
-      v[i] = sqrelu(v[i]);
-      acc[i] = 0.f;
+      auto x = sum.v[i];
+      if constexpr (M::narrow) x *= row_scale[t];
+      if constexpr (F == Elt::FP8) x *= ((const float*)p.s_up)[(int64_t)cur.e * p.I + cur.n0 + 4 * g + i];
+      v[i] = (float)sqrelu(x);
+      sum.v[i] = 0;
     }
     if constexpr (!M::narrow) {
       if (sel) store_pair(p.h, p.h_lo, at, v);
@@ -599,7 +627,10 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
       sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), *(const uint4*)(shrow + at), sum);
       sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), *(const uint4*)(slrow + at), sum);
     }
-    sum = dot_rows<2, true>(swrow, shrow, slrow, p.Is, min(shi, slo + kDownShared), shi, g, sum);
+    Sum<float> rest;
+    rest.take(sum);
+    dot_rows<2, true>(swrow, shrow, slrow, p.Is, min(shi, slo + kDownShared), shi, g, rest);
+    sum = rest.start();
   };
 
   // one wave's steps [at, stop), in batches of up to U steps of one slot
