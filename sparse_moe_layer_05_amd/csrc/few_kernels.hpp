@@ -308,19 +308,22 @@ __global__ __launch_bounds__(256) void few_front(FewParams p) {
 // and leave an uneven second round: 16 waves (MXFP4, 4 tokens: 58.8 us against 61.3; e4m3, 16
 // tokens: 164 against 165). A plain read of the same 80 MB takes 14.5 us, in this pattern (16 rows
 // of 64 bytes an instruction) 16 to 18.
-template <Elt F> constexpr int kUpWaves = F == Elt::BF16 ? 8 : 16;
+// More than 512 experts: 8 waves whatever the weights, as 16 scores and keys a lane beside the shared
+// expert's loads need more than the 128 registers of 16 waves (E 1024, k 8, H 2048, I 512, MXFP4: 4
+// tokens 43.5 us against 53 with 80 registers in scratch, 16 tokens 88 against 96).
+template <Elt F, int NPER> constexpr int kUpWaves = F == Elt::BF16 || NPER > 8 ? 8 : 16;
 constexpr size_t kUpRowsLds = 130 * 1024;   // of the staged activations
 // steps of the shared unit in flight per wave
-template <Elt F> constexpr int kSharedSteps = F == Elt::BF16 ? 12 : 6;
+template <Elt F, int NPER> constexpr int kSharedSteps = kUpWaves<F, NPER> == 8 ? 12 : 6;
 
 // LDS row stride in bytes of K staged elements, whole steps of 128 and an odd number of 16-byte
 // chunks (16 rows at one chunk index then fall on distinct banks).
 __host__ __device__ inline int lds_stride(int K) { return (K + 127) / 128 * 256 + 16; }
 
 template <Elt F, int NPER, bool XLDS>
-__global__ __launch_bounds__(64 * kUpWaves<F>) void few_up(FewParams p) {
+__global__ __launch_bounds__((64 * kUpWaves<F, NPER>)) void few_up(FewParams p) {
   using M = Fmt<F>;
-  constexpr int NWV = kUpWaves<F>, NTH = 64 * NWV, SS = kSharedSteps<F>;
+  constexpr int NWV = kUpWaves<F, NPER>, NTH = 64 * NWV, SS = kSharedSteps<F, NPER>;
   __shared__ int idx_l[TB * 64];
   __shared__ float gates_l[TB * 64];
   __shared__ uint32_t emask[NPER * 64];     // tokens that selected expert e
@@ -842,13 +845,16 @@ __global__ __launch_bounds__(512) void few_out(FewParams p) {
                                0, p.y, nullptr}, 16 * blockIdx.x, part);
 }
 
+template <Elt F, int NPER, bool XLDS>
+hipError_t run_up(const FewParams& p, int grid, size_t lds, hipStream_t s) {
+  hipLaunchKernelGGL((few_up<F, NPER, XLDS>), dim3(grid), dim3(64 * kUpWaves<F, NPER>), lds, s, p);
+  return hipGetLastError();
+}
 template <Elt F, bool XLDS>
 hipError_t run_up(const FewParams& p, int grid, size_t lds, hipStream_t s) {
-  const dim3 block(64 * kUpWaves<F>);
-  if (p.E <= 128) hipLaunchKernelGGL((few_up<F, 2, XLDS>), dim3(grid), block, lds, s, p);
-  else if (p.E <= 512) hipLaunchKernelGGL((few_up<F, 8, XLDS>), dim3(grid), block, lds, s, p);
-  else hipLaunchKernelGGL((few_up<F, 16, XLDS>), dim3(grid), block, lds, s, p);
-  return hipGetLastError();
+  if (p.E <= 128) return run_up<F, 2, XLDS>(p, grid, lds, s);
+  if (p.E <= 512) return run_up<F, 8, XLDS>(p, grid, lds, s);
+  return run_up<F, 16, XLDS>(p, grid, lds, s);
 }
 
 template <Elt F>
