@@ -52,7 +52,11 @@
  *     and the rows of h = relu(u W_up^T)^2 (rounded to bf16) are quantised per row to e4m3 with
  *     scale amax / 448 before they meet the weights, as in "Nemotron 3 Nano：開放高效的 MoE 混合
  *     Mamba-Transformer 智能體推理模型", section 4 (FP8 expert weights); the scale is 2^-127 where
- *     448 / amax is past fp32. MOE_MXFP4 / MOE_MXFP8 run on the decode (stream) path, whatever T
+ *     448 / amax is past fp32. The matrix core cuts these products (of e4m3 rows with 8- and 4-bit
+ *     weights) as stated at moe_mx_gemm, on every path but moe_few_forward, which multiplies them
+ *     exactly. An element of h next to a bf16 border may so round the other way; where it is its
+ *     row's largest, the row's scale and most of its codes move, about 4% of that row of h (one row
+ *     in some hundred with E4M3 weights, in some thousand with E2M1). MOE_MXFP4 / MOE_MXFP8 run on the decode (stream) path, whatever T
  *     is, unless MOE_MX_GROUPED asks for their matrix-core tiles; MOE_PATH_GROUPED is unsupported
  *     for them.
  */
@@ -107,7 +111,8 @@ typedef enum {
                                     inference calls reject it with MOE_ERR_INVALID_ARG) */
 #define MOE_MX_GROUPED 32u       /* forward calls with MXFP4 / MXFP8 experts: the grouped path's
                                     tile list and matrix-core tiles (many tokens) instead of the
-                                    decode stream. Path bits must be MOE_PATH_AUTO (else
+                                    decode stream; formats, roundings and cut products as there,
+                                    sums in another order. Path bits must be MOE_PATH_AUTO (else
                                     MOE_ERR_INVALID_ARG); other expert types:
                                     MOE_ERR_UNSUPPORTED */
 
@@ -306,11 +311,14 @@ int32_t moe_mx_dequantize(const void *codes, const uint8_t *scales, moe_dtype_t 
 
 /* C [M, N] (c_dt: MOE_BF16 or MOE_F32) = A W^T of two block-scaled matrices, A [M, K] and
  * W [N, K], each MOE_MXFP4 or MOE_MXFP8: products and block scales on the matrix cores, fp32
- * accumulation in a fixed order (deterministic), one rounding at the end. With an MXFP8 operand
- * the matrix core keeps, of each eight consecutive products, 13 bits below the largest (about
- * 1.5e-5 of the result, far inside a bf16 step): c_dt MOE_F32 is offered for two MXFP4 operands,
- * whose sums are exact to fp32, and is MOE_ERR_UNSUPPORTED otherwise. A block of scale code
- * 255 makes the outputs it enters NaN. N is a multiple of 16, K of 32, M >= 0; A and W each span
+ * accumulation in a fixed order (deterministic), one rounding at the end. Precision before that
+ * rounding: two MXFP4 operands, that of fp32 sums. With an MXFP8 operand the matrix core cuts the
+ * products of each eight consecutive k (8i .. 8i + 7) toward zero to multiples of 2^(e - 13), e the
+ * exponent of the group's largest: a group loses up to 7 * 2^-13 of its largest product. Normal
+ * random data ends about 1.5e-5 off (MXFP8 x MXFP8; 4.5e-6 with one MXFP4), inside a bf16 step; but
+ * the loss is relative to the products, not to the result, and where large products cancel it can
+ * be all of the result. c_dt MOE_F32 is therefore offered for two MXFP4 operands alone, and is
+ * MOE_ERR_UNSUPPORTED otherwise. A block of scale code 255 makes the outputs it enters NaN. N is a multiple of 16, K of 32, M >= 0; A and W each span
  * less than 2 GiB. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
  * MOE_ERR_UNSUPPORTED (formats). */
 int32_t moe_mx_gemm(const void *A, const uint8_t *a_scales, moe_dtype_t a_fmt, const void *W,
