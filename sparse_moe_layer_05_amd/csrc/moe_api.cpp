@@ -100,7 +100,7 @@ int32_t make_plan(const moe_desc_t* d, bool latent_call, Plan* pl) {
   // fp32 grouped launches: 16-row tiles when experts average at most 16 rows, else 64
   p.bm = p.act == Elt::F32 ? ((int64_t)p.T * p.k <= 16LL * p.E ? 16 : 64) : kGroupBM;
   if (mx_grouped) {
-    p.bm = mx_group_bm(p.P, p.E);
+    p.bm = mx_group_bm(p.P, p.E, p.D, p.I, p.ex == Elt::MXFP4);
     // The terms of the gated sum are not rounded, as on the decode path: in bf16 they cost as much
     // precision as y's own rounding (2048 Nano tokens without a shared expert, MXFP4: y 2.47e-3 off,
     // 1.82e-3 with fp32 rows and on the decode path alike; 8192 tokens 1226 -> 1335 us).

@@ -41,10 +41,17 @@ struct MxGemmParams {
   int G = 0;
   int bm = 0;                        // grouped: 64 or 128 (mx_group_bm)
 };
-// Rows of the grouped launches' M-tiles. Tiles of 64 rows where experts hold at most 96 on average
-// (every expert's last tile is partly empty): LatentMoE, 47 rows an expert, 307 us per layer
-// against 318 on 128; Nano, 384 rows, 1480 against 1220.
-inline int mx_group_bm(int P, int E) { return P <= 96 * (int64_t)E ? 64 : 128; }
+// Rows of the grouped launches' M-tiles: 64 where experts hold few rows on average (every expert's
+// last tile is partly empty), else 128, which read the weights half as often; and 64 where tiles of
+// 128 are fewer than CUs. Microseconds per layer, 64 / 128: Nano (128 experts) MXFP4 at 38 rows an
+// expert 397 / 395, 48 408 / 407, 56 449 / 418, 96 562 / 502, 384 1637 / 1355; MXFP8 at 48 rows 491 /
+// 540, 80 581 / 617, 112 692 / 703, 131 761 / 738, 384 1812 / 1589. LatentMoE (512 experts) MXFP4 at
+// 47 rows 257 / 261, 56 287 / 282, 96 391 / 372; MXFP8 at 47 rows 296 / 317, 112 476 / 490, 131 542 /
+// 541. H 288, I 160, 24 experts of 125 rows: MXFP4 49 / 61, MXFP8 50 / 54.
+inline int mx_group_bm(int P, int E, int D, int I, bool mxfp4) {
+  const int64_t tiles = ((int64_t)P / 128 + E / 2) * (((D < I ? D : I) + 255) / 256);
+  return P <= (mxfp4 ? 48 : 112) * (int64_t)E || tiles < 256 ? 64 : 128;
+}
 // The gated sum of the experts' fp32 rows, out[t] + out_lo[t] = sum_j gates[t, j] Y[pos[t, j]] (all
 // of D columns): rounded to bf16, and what that left over, in bf16 too.
 hipError_t launch_combine_pair(const float* Y, const int32_t* pos, const float* gates, int T,
