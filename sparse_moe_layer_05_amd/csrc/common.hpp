@@ -15,18 +15,20 @@ typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
 constexpr int kWave = 64;
 constexpr int kXcds = 8;  // MI355X: 8 accelerator complex dies, 32 CUs each, one L2 per die
 
-// bf16 <-> fp32. bf16 is the upper half of a binary32; the narrowing rounds to nearest even
-// (inputs are finite).
+// bf16 <-> fp32. bf16 is the upper half of a binary32; the narrowing is the hardware's: to nearest
+// even, subnormals kept, NaN stays NaN. (As integer arithmetic, u + 0x7FFF + bit 16, it gives the same
+// for all 2^32 patterns but NaN, of which one of all ones carries into the sign and becomes 0.)
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t u16) {
   return __uint_as_float(u16 << 16);
 }
-__device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
-  uint32_t u = __float_as_uint(f);
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
 // Two fp32 -> packed bf16x2 (lo in bits 0..15).
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+__device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
+  return pack_bf16x2(f, f) & 0xFFFFu;
 }
 
 // Two fp32 -> two OCP e4m3 codes (round to nearest even) in the low 16 bits.

@@ -148,14 +148,9 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint8_t* 
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = v[j >> 1][j & 1] * s;
     if constexpr (XT == Elt::BF16) {
-      // exact for every normal bf16; NaN must not be carried over the sign by the rounding
-      uint32_t w[4];
+      uint32_t w[4];   // exact for every normal bf16
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float lo = o[2 * j], hi = o[2 * j + 1];
-        w[j] = (lo == lo ? f32_to_bf16_bits(lo) : 0x7FC0u) |
-               (hi == hi ? f32_to_bf16_bits(hi) : 0x7FC0u) << 16;
-      }
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
       *(uint4*)((uint16_t*)x + g * 8) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       float* d = (float*)x + g * 8;

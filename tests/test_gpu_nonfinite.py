@@ -124,3 +124,17 @@ def test_the_smallest_block_scales(w, path):
     got = out(cfg, dev, rt, path).double()
     assert float(want.abs().max()) > 0
     assert float((got - want).norm() / want.norm()) <= 5e-3
+
+
+@pytest.mark.parametrize("w,path", PATHS)
+@pytest.mark.parametrize("kw", [dict(H=288, I=160, I_shared=128), dict(H=288, I=96, latent=160)])
+@pytest.mark.parametrize("bits", [0x7FFFFFFF, -1, 0x7F800001])
+def test_a_nan_gate_of_any_payload_reaches_its_token(w, path, kw, bits):
+    """Memory of all ones is a NaN whose rounding to bf16 must not carry into the sign."""
+    cfg, dev, rt = setup(w, **kw)
+    clean = out(cfg, dev, rt, path).clone()
+    rt["gates"].view(torch.int32)[7, 1] = bits
+    bad = out(cfg, dev, rt, path)
+    where = torch.zeros_like(bad, dtype=torch.bool)
+    where[7] = True
+    only(bad, clean, where)
