@@ -8,14 +8,15 @@
 // What the instruction rounds (measured with two nonzero products at chosen distances): of each
 // eight consecutive k, products are cut toward zero to multiples of 2^(e - 13), e the exponent of
 // the largest of them; the groups of eight are then added in fp32. Two E2M1 operands lose nothing
-// (products are multiples of 1/4 up to 36). With an E4M3 operand random data ends 4.5e-6 (E2M1 on
-// the other side) or 1.5e-5 off, which a bf16 result (2^-9) does not see; fp32 results are
-// offered for two E2M1 operands alone.
+// (products are multiples of 1/4 up to 36). With an E4M3 operand a group loses up to 7 * 2^-13 of its
+// largest product: random data ends 4.5e-6 (E2M1 on the other side) or 1.5e-5 off, inside a bf16
+// result's half step, but where large products cancel it can be all of the result. fp32 results
+// are offered for two E2M1 operands alone.
 //
 // Three kernels:
 //  - mx_rows_kernel, few rows: the weights are the matrix core's first operand, 16 weight rows
 //    against 16, 32 or 64 rows of A, and the workgroup's waves split K and join in LDS, so that
-//    the launch is one pass over W with every CU reading.
+//    the launch is one pass over W by N / 16 workgroups.
 //  - mx_tile_kernel, many rows: BM x BN tiles staged through LDS, dense or grouped by expert.
 //  - mx_persist_kernel, expert products over longer K: the same tiles as one pipeline per CU.
 //
@@ -873,7 +874,8 @@ constexpr int persist_stages(int BM) {
 // the next tile needs too). Microseconds, persistent / a workgroup per tile: 49152 rows of 128
 // MXFP4 experts, K 2688, N 1856 365 / 393 and K 1856, N 2688 404 / 433; 24024 rows of 512 MXFP8
 // experts, K 1024, N 512 81 / 90, but K 512, N 1024 (4 steps, with the lookups after the last) 115
-// / 106.
+// / 106. (Nano's figures with bf16 results; its second product with the fp32 rows it stores: 461 under
+// the profiler.)
 template <int FW>
 hipError_t run_grouped(const MxGemmParams& p, int mtiles, hipStream_t s) {
   const bool walk = cdiv(p.K, 128) >= kPersistSteps;
