@@ -95,6 +95,10 @@ __device__ __forceinline__ void mask_step(WStep<F>& x, int s, int kend, int g) {
   for (int c = 0; c < M::CW; ++c)
     if (s * M::KS + M::kw(c, g) >= kend) x.c[c] = make_uint4(0, 0, 0, 0);
 }
+// Both sides of a product past the end are zeroed: zero times an infinity is NaN.
+__device__ __forceinline__ void zero_if(bool past, uint4& v) {
+  if (past) v = make_uint4(0, 0, 0, 0);
+}
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t bits_of(bf16x2_t v) { return __builtin_bit_cast(uint32_t, v); }
 // Instruction j's weight fragment in bf16.
@@ -178,7 +182,10 @@ __device__ __forceinline__ void dot_rows(const uint16_t* w, const uint16_t* a, c
     f32x4_t acc = sum.start();
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      if ((s + q) * 32 + 8 * g >= kend) wf[q] = make_uint4(0, 0, 0, 0);
+      const bool past = (s + q) * 32 + 8 * g >= kend;
+      zero_if(past, wf[q]);
+      zero_if(past, af[q]);
+      if constexpr (LO) zero_if(past, bf[q]);
       acc = mul(__builtin_bit_cast(bf16x8_t, wf[q]), af[q], acc);
       if constexpr (LO) acc = mul(__builtin_bit_cast(bf16x8_t, wf[q]), bf[q], acc);
     }
@@ -402,7 +409,7 @@ __global__ __launch_bounds__((64 * kUpWaves<F, NPER>)) void few_up(FewParams p) 
       if (lane == 0) row_scale[tk] = rs.down;
     }
     if constexpr (XLDS)
-      for (int c = lane * 8; c < ldx / 2 - 8; c += 512) {
+      for (int c = lane * 8; c < ldx / 2; c += 512) {   // the last chunk: zeros for steps past the end
         uint4 v = make_uint4(0, 0, 0, 0);
         if (c < p.D) v = *(const uint4*)(row + c);
         *(uint4*)(xl + tk * ldx + 2 * c) = M::narrow ? codes8(v, inv) : v;
@@ -454,7 +461,9 @@ __global__ __launch_bounds__((64 * kUpWaves<F, NPER>)) void few_up(FewParams p) 
     if (n == (int)blockIdx.x && slo < shi) {
 #pragma unroll
       for (int q = 0; q < SS; ++q) {
-        if ((slo + q) * 32 + 8 * g >= send) sw[q] = make_uint4(0, 0, 0, 0);
+        const bool past = (slo + q) * 32 + 8 * g >= send;
+        zero_if(past, sw[q]);
+        zero_if(past, sa[q]);
         acc = mul(__builtin_bit_cast(bf16x8_t, sw[q]), sa[q], acc);
       }
       from = min(shi, slo + SS);
@@ -526,9 +535,14 @@ __global__ __launch_bounds__((64 * kUpWaves<F, NPER>)) void few_up(FewParams p) 
       mask_step<F>(wc[q], b * U + q, p.D, g);
 #pragma unroll
       for (int j = 0; j < M::MF; ++j) {
-        const int el = min((b * U + q), steps - 1) * M::KS + M::k_of(j, g);
-        const uint4 a = XLDS ? *(const uint4*)(xl + t * ldx + 2 * el)
-                             : *(const uint4*)(in + (int64_t)t * p.D + (el < p.D ? el : 0));
+        const int el = (b * U + q) * M::KS + M::k_of(j, g);
+        uint4 a;
+        if constexpr (XLDS) {
+          a = *(const uint4*)(xl + t * ldx + 2 * (b * U + q < steps ? el : ldx / 2 - 8));
+        } else {
+          a = *(const uint4*)(in + (int64_t)t * p.D + (el < p.D ? el : 0));
+          zero_if(el >= p.D, a);
+        }
         acc = mul(wfrag<F>(wc[q], j), a, acc);
       }
     }
@@ -626,9 +640,12 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
 #pragma unroll
     for (int q = 0; q < kDownShared; ++q) {
       const int el = (slo + q) * 32 + 8 * g, at = el < send ? el : 0;
-      if (el >= send) sw[q] = make_uint4(0, 0, 0, 0);
-      sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), *(const uint4*)(shrow + at), sum);
-      sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), *(const uint4*)(slrow + at), sum);
+      uint4 hi = *(const uint4*)(shrow + at), lo = *(const uint4*)(slrow + at);
+      zero_if(el >= send, sw[q]);
+      zero_if(el >= send, hi);
+      zero_if(el >= send, lo);
+      sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), hi, sum);
+      sum = mul(__builtin_bit_cast(bf16x8_t, sw[q]), lo, sum);
     }
     Sum<float> rest;
     rest.take(sum);
@@ -717,6 +734,9 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down(FewParams p, int cap
             const int el = min(cur.s + q, spe - 1) * M::KS + M::k_of(j, g);
             acc = mul(w, *(const uint4*)(cur.a + el), acc);
           } else {
+            const bool past = (cur.s + q) * M::KS + M::k_of(0, g) >= kend;
+            zero_if(past, bc.a[q]);
+            zero_if(past, bc.b[q]);
             acc = mul(w, bc.a[q], acc);
             acc = mul(w, bc.b[q], acc);
           }

@@ -138,3 +138,21 @@ def test_a_nan_gate_of_any_payload_reaches_its_token(w, path, kw, bits):
     where = torch.zeros_like(bad, dtype=torch.bool)
     where[7] = True
     only(bad, clean, where)
+
+
+@pytest.mark.parametrize("path", ["few", "stream", "grouped"])
+@pytest.mark.parametrize("kw", [dict(), dict(I_shared=128), dict(H=8192, T=16, I=48),
+                                dict(H=272, I=144), dict(H=2080, I=160, I_shared=16)])
+@pytest.mark.parametrize("at", [0, 9, -1])
+def test_an_infinity_that_relu_takes(path, kw, at):
+    """x holds one infinity and every weight that meets it is negative: u is -infinity, h and y are 0.
+    Nothing else may meet the infinity, as the padding of a row whose width ends inside a step."""
+    cfg, dev, rt = setup("bf16", **{**dict(T=3, H=288, I=160), **kw})
+    dev["x"][1] = 0.0
+    dev["x"][1, at] = float("inf")
+    dev["W_up"][:, :, at] = -1.0
+    if cfg.I_shared:
+        dev["Ws_up"][:, at] = -1.0
+    y = out(cfg, dev, rt, path)
+    assert bool((y[1] == 0).all())
+    assert bool(torch.isfinite(y).all())
