@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bf16_pair.hpp"
 #include "common.hpp"
 #include "few.hpp"
 #include "topk.hpp"
@@ -140,9 +141,7 @@ __device__ __forceinline__ uint4 codes8(uint4 v, float inv) {
 __device__ __forceinline__ void store_pair(uint16_t* hi, uint16_t* lo, int64_t at, const float* v) {
   const uint2 h = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   *(uint2*)(hi + at) = h;
-  *(uint2*)(lo + at) =
-      make_uint2(pack_bf16x2(v[0] - bf16_bits_to_f32(h.x & 0xFFFF), v[1] - bf16_bits_to_f32(h.x >> 16)),
-                 pack_bf16x2(v[2] - bf16_bits_to_f32(h.y & 0xFFFF), v[3] - bf16_bits_to_f32(h.y >> 16)));
+  *(uint2*)(lo + at) = make_uint2(bf16x2_rest(v[0], v[1], h.x), bf16x2_rest(v[2], v[3], h.y));
 }
 
 // Four sums of one lane. A Sum of doubles takes the matrix core's fp32 sums of a batch of steps at a

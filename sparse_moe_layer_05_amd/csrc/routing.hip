@@ -5,6 +5,7 @@
 // "混合Mamba Transformer MoE架构") with an aux-loss-free per-expert bias that only steers the
 // selection ("Nemotron 3 Nano：開放高效的 MoE 混合 Mamba-Transformer 智能體推理模型", section
 // 2.2); sigmoid scores renormalised over the selected experts are the gate weights.
+#include "bf16_pair.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 #include "topk.hpp"
@@ -497,8 +498,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ Y
         uint32_t r[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          r[i] = pack_bf16x2(acc[2 * i] - bf16_bits_to_f32(w[i] & 0xFFFF),
-                             acc[2 * i + 1] - bf16_bits_to_f32(w[i] >> 16));
+          r[i] = bf16x2_rest(acc[2 * i], acc[2 * i + 1], w[i]);
         *(uint4*)(out_lo + (int64_t)t * ldo + c) = make_uint4(r[0], r[1], r[2], r[3]);
       }
     } else {

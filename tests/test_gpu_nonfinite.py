@@ -156,3 +156,47 @@ def test_an_infinity_that_relu_takes(path, kw, at):
     y = out(cfg, dev, rt, path)
     assert bool((y[1] == 0).all())
     assert bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("path", ["few", "stream", "grouped"])
+@pytest.mark.parametrize("kw,value", [
+    (dict(), float("inf")), (dict(), 1e25), (dict(), 2.0 ** 65),
+    (dict(latent=160), 1e25), (dict(latent=160), 2.0 ** 65),
+    (dict(I_shared=128), float("inf")), (dict(I_shared=128), 1e25)])
+def test_an_infinite_h_stays_infinite(path, kw, value):
+    """One element of h is infinite (2^65 squared is past fp32), the others are zero: every output is
+    infinite with the sign of its weight, not NaN, also where h or z is kept as a pair of bf16. bf16
+    weights, whose rows are not rescaled."""
+    cfg, dev, rt = setup("bf16", T=3, H=288, I=160, **kw)
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def up(rows, cols):      # row 7 alone is positive where x is not zero
+        w = torch.zeros(rows, cols, device="cuda")
+        w[:, 9] = -1.0
+        w[7, 9] = 1.0
+        return w.bfloat16()
+
+    def signed(*shape):      # no zeros: zero times infinity is NaN
+        w = torch.rand(shape, generator=g, device="cuda") + 0.1
+        return (w * (torch.rand(shape, generator=g, device="cuda") - 0.5).sign()).bfloat16()
+
+    dev["x"].zero_()
+    dev["x"][1, 9] = value
+    if cfg.I_shared:         # through the shared expert; the routed ones give zero
+        dev["W_up"].fill_(-1.0)
+        dev["Ws_up"] = up(128, 288)
+        dev["Ws_down"] = signed(288, 128)
+        sign = dev["Ws_down"][:, 7].sign()
+    elif cfg.latent:         # u = x's first columns, z of one sign, W_out of one sign a row
+        dev["W_in"] = torch.eye(160, 288, device="cuda").bfloat16()
+        dev["W_up"][:] = up(160, 160)
+        dev["W_down"][:] = signed(1, 160, 160).abs()
+        dev["W_out"] = signed(288, 1).expand(288, 160).contiguous()
+        sign = dev["W_out"][:, 0].sign()
+    else:
+        dev["W_up"][:] = up(160, 288)
+        dev["W_down"][:] = signed(1, 288, 160)
+        sign = dev["W_down"][0, :, 7].sign()
+    y = out(cfg, dev, rt, path)
+    assert bool((y[1].float() == sign.float() * float("inf")).all())
+    assert bool(torch.isfinite(y[[0, 2]]).all())
