@@ -22,7 +22,7 @@
  *   expert  f_e(u) = relu(u W_up[e]^T)^2 W_down[e]^T        (squared-ReLU, no gate, no bias)
  *   routed  r = sum_j g_j f_{idx_j}(u)                      (fixed j order: deterministic)
  *   y_t     = r, or r W_out^T (LatentMoE);  y_t += relu(x_t Ws_up^T)^2 Ws_down^T if I_shared > 0
- * A NaN in x_t makes y_t NaN and no other row (relu keeps NaN).
+ * relu keeps NaN: a NaN in x_t makes NaN of what it enters of y_t, and of no other row.
  *
  * Conventions shared by every entry point:
  *   - Tensor pointers are DEVICE pointers to row-major, contiguous arrays, 16-byte aligned, owned
@@ -56,9 +56,9 @@
  *     weights) as stated at moe_mx_gemm, on every path but moe_few_forward, which multiplies them
  *     exactly. An element of h next to a bf16 border may so round the other way; where it is its
  *     row's largest, the row's scale and most of its codes move, about 4% of that row of h (one row
- *     in some hundred with E4M3 weights, in some thousand with E2M1). MOE_MXFP4 / MOE_MXFP8 run on the decode (stream) path, whatever T
- *     is, unless MOE_MX_GROUPED asks for their matrix-core tiles; MOE_PATH_GROUPED is unsupported
- *     for them.
+ *     in some hundred with E4M3 weights, in some thousand with E2M1). MOE_MXFP4 / MOE_MXFP8 run on
+ *     the decode (stream) path, whatever T is, unless MOE_MX_GROUPED asks for their matrix-core
+ *     tiles; MOE_PATH_GROUPED is unsupported for them.
  */
 #ifndef MOE_MI355X_H
 #define MOE_MI355X_H
@@ -318,8 +318,8 @@ int32_t moe_mx_dequantize(const void *codes, const uint8_t *scales, moe_dtype_t 
  * random data ends about 1.5e-5 off (MXFP8 x MXFP8; 4.5e-6 with one MXFP4), inside a bf16 step; but
  * the loss is relative to the products, not to the result, and where large products cancel it can
  * be all of the result. c_dt MOE_F32 is therefore offered for two MXFP4 operands alone, and is
- * MOE_ERR_UNSUPPORTED otherwise. A block of scale code 255 makes the outputs it enters NaN. N is a multiple of 16, K of 32, M >= 0; A and W each span
- * less than 2 GiB. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
+ * MOE_ERR_UNSUPPORTED otherwise. A block of scale code 255 makes the outputs it enters NaN. N is a
+ * multiple of 16, K of 32, M >= 0; A and W each span less than 2 GiB. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
  * MOE_ERR_UNSUPPORTED (formats). */
 int32_t moe_mx_gemm(const void *A, const uint8_t *a_scales, moe_dtype_t a_fmt, const void *W,
                     const uint8_t *w_scales, moe_dtype_t w_fmt, int32_t M, int32_t N, int32_t K,
