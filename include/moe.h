@@ -319,8 +319,8 @@ int32_t moe_mx_dequantize(const void *codes, const uint8_t *scales, moe_dtype_t 
  * the loss is relative to the products, not to the result, and where large products cancel it can
  * be all of the result. c_dt MOE_F32 is therefore offered for two MXFP4 operands alone, and is
  * MOE_ERR_UNSUPPORTED otherwise. A block of scale code 255 makes the outputs it enters NaN. N is a
- * multiple of 16, K of 32, M >= 0; A and W each span less than 2 GiB. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
- * MOE_ERR_UNSUPPORTED (formats). */
+ * multiple of 16, K of 32, M >= 0; A and W each span less than 2 GiB. Errors:
+ * MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size), MOE_ERR_UNSUPPORTED (formats). */
 int32_t moe_mx_gemm(const void *A, const uint8_t *a_scales, moe_dtype_t a_fmt, const void *W,
                     const uint8_t *w_scales, moe_dtype_t w_fmt, int32_t M, int32_t N, int32_t K,
                     void *C, moe_dtype_t c_dt, void *stream);
