@@ -325,6 +325,119 @@ int32_t moe_mx_gemm(const void *A, const uint8_t *a_scales, moe_dtype_t a_fmt, c
                     const uint8_t *w_scales, moe_dtype_t w_fmt, int32_t M, int32_t N, int32_t K,
                     void *C, moe_dtype_t c_dt, void *stream);
 
+/* ---- Token rows in expert order, for experts that run outside the layer call (other activations,
+ * moe_mx_gemm on one expert's rows, one rank's share of the experts): the rows of every expert next
+ * to each other, their way back with the gate weights applied, and the gradients of both. idx [T, k]
+ * and pos [T, k] are as in moe_routing_t. A pair (t, j) is dropped where idx is outside [0, E) (an
+ * expert of another rank, so k > E is allowed here) or repeats an expert of its token, and where pos
+ * is outside [0, n_rows): nothing is read or written for it, and its weight's gradient is 0. Rows
+ * behind the last pair are left as they were. weights [T, k] fp32, or NULL for 1; they may be any
+ * values. Sums run in fp32 in slot order and are rounded once; all results are deterministic.
+ * D a multiple of 16 up to 2^20, k <= 64, T * ceil(D / 512) <= 2^25, T * k < 2^31. dt, dx_dt, y_dt,
+ * dy_dt: MOE_BF16 or MOE_F32. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
+ * MOE_ERR_UNSUPPORTED (types), MOE_ERR_WORKSPACE. */
+
+/* rows[pos[t, j]] = weights[t, j] * x[t], rows [T * k, D] and x [T, D] of type dt; also offsets
+ * [E + 1] and pos [T, k], as moe_dispatch makes them (T == 0 writes the offsets alone). */
+int32_t moe_sort_tokens_workspace_size(int32_t T, int32_t E, int32_t k, size_t *bytes);
+int32_t moe_sort_tokens(const void *x, moe_dtype_t dt, const int32_t *idx, const float *weights,
+                        int32_t T, int32_t D, int32_t E, int32_t k, void *rows, int32_t *offsets,
+                        int32_t *pos, void *ws, size_t ws_bytes, void *stream);
+/* Its gradients, given drows [n_rows, D] of type dt: dx[t] = sum_j weights[t, j] drows[pos[t, j]]
+ * (type dx_dt) and, unless dweights is NULL, dweights[t, j] = <x[t], drows[pos[t, j]]> (x of type
+ * dt; only read for them). */
+int32_t moe_sort_tokens_backward(const void *drows, const void *x, moe_dtype_t dt,
+                                 const int32_t *pos, const float *weights, int32_t T, int32_t D,
+                                 int32_t k, int32_t n_rows, void *dx, moe_dtype_t dx_dt,
+                                 float *dweights, void *stream);
+/* The way back: y[t] = add[t] + sum_j weights[t, j] rows[pos[t, j]], rows [n_rows, D] of type dt; y
+ * and add [T, D] of type y_dt (add NULL: 0; y may be add). A token without a row gets add, or 0. */
+int32_t moe_unsort_tokens(const void *rows, moe_dtype_t dt, const int32_t *pos,
+                          const float *weights, const void *add, int32_t T, int32_t D, int32_t k,
+                          int32_t n_rows, void *y, moe_dtype_t y_dt, void *stream);
+/* Its gradients, given dy [T, D]: drows[pos[t, j]] = weights[t, j] * dy[t] (type dt) and, unless
+ * dweights is NULL, dweights[t, j] = <dy[t], rows[pos[t, j]]> (rows of type dt, only read for them;
+ * drows may be rows). The positions of kept pairs must differ. Without dweights dt must be dy_dt. */
+int32_t moe_unsort_tokens_backward(const void *dy, moe_dtype_t dy_dt, const void *rows,
+                                   moe_dtype_t dt, const int32_t *pos, const float *weights,
+                                   int32_t T, int32_t D, int32_t k, int32_t n_rows, void *drows,
+                                   float *dweights, void *stream);
+
+/* ---- The block around the layer: the norm before it, and what follows it (norm, gate, residual
+ * scale, residual, the next block's norm) in one pass, with their gradients. Per row of H elements
+ *   n(v) = v / sqrt(mean(v^2) + eps)
+ *   before:  h = n(x) w
+ *   after:   z = n(f) w with MOE_BLOCK_NORM, else f w (w: a learned scale per channel);
+ *            y = x + scale a z, a = 1, a gate per token ([T] fp32, MOE_GATE_TOKEN) or per element
+ *            ([T, H] of type dt, MOE_GATE_ELEMENT), or its sigmoid (MOE_GATE_SIGMOID);
+ *            h = n(y) w_next, of y as it is stored (h NULL: not wanted).
+ * x, f, y, h [T, H] of type dt (MOE_BF16 or MOE_F32); w, w_next [H] of type w_dt, or NULL for 1.
+ * y may be x or f, and h may be x (before). Sums run in fp32 (in fp64 where squares pass it), each
+ * result is rounded once. A row that holds a NaN or an infinity reaches no other row of y and h.
+ * H a multiple of 16 up to 16384, T <= 2^23, eps > 0. Errors: MOE_ERR_INVALID_ARG (null or
+ * misaligned pointer, bad size or flags, a gate without its flag), MOE_ERR_UNSUPPORTED (types). */
+#define MOE_BLOCK_NORM 1u
+#define MOE_GATE_TOKEN 2u
+#define MOE_GATE_ELEMENT 4u
+#define MOE_GATE_SIGMOID 8u
+int32_t moe_block_norm(const void *x, const void *w, void *h, int32_t T, int32_t H, moe_dtype_t dt,
+                       moe_dtype_t w_dt, float eps, void *stream);
+int32_t moe_block_residual(const void *x, const void *f, const void *w, const void *gate,
+                           const void *w_next, void *y, void *h, int32_t T, int32_t H,
+                           moe_dtype_t dt, moe_dtype_t w_dt, uint32_t flags, float scale,
+                           float eps, void *stream);
+/* Gradients. before: dx = dres + gradient of h at x (dres [T, H] of type dt, or NULL; dx may be
+ * dres). after: d = dy + gradient of h at y; dx = d, df, dgate (as the gate is given; fp32 [T] or
+ * type dt [T, H]), dw, dw_next. dy may be NULL where dh is given, dh (with y, of type dt) where there
+ * was no next norm. dh has type dh_dt: dt, or MOE_F32 (what moe_layer_backward makes of the layer's
+ * input). dw, dw_next [H] fp32, dgate: NULL where not wanted. The weights' gradients are summed over
+ * the rows in fp32 in a fixed order (deterministic), through the workspace
+ * (moe_block_backward_workspace_size bytes; only needed for them); T == 0 makes them 0. */
+int32_t moe_block_backward_workspace_size(int32_t T, int32_t H, size_t *bytes);
+int32_t moe_block_norm_backward(const void *dh, moe_dtype_t dh_dt, const void *x, const void *w,
+                                const void *dres, void *dx, float *dw, int32_t T, int32_t H,
+                                moe_dtype_t dt, moe_dtype_t w_dt, float eps, void *ws,
+                                size_t ws_bytes, void *stream);
+int32_t moe_block_residual_backward(const void *dy, const void *f, const void *w,
+                                    const void *gate, const void *y, const void *dh,
+                                    moe_dtype_t dh_dt, const void *w_next, void *dx, void *df,
+                                    float *dw, void *dgate, float *dw_next, int32_t T, int32_t H,
+                                    moe_dtype_t dt, moe_dtype_t w_dt, uint32_t flags, float scale,
+                                    float eps, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- The global norm of many gradients (what moe_layer_backward and the calls above leave), and
+ * their clipping by it, in two launches whatever their number:
+ *   norm = sqrt(sum over all tensors of g^2)       (summed in fp64, in a fixed order)
+ *   coef = min(1, max_norm / (norm + 1e-6)), and 1 where the norm is not finite
+ *   out = coef g, rounded once; norm[0] = norm, norm[1] = coef (fp32, device; a norm past fp32 is
+ *   stored as infinity, the coefficient still divides by it)
+ * A norm that is not finite thus leaves the gradients as they are: the caller reads it and skips the
+ * step. In place (out NULL or grad for every tensor) nothing is written where coef is 1.
+ * Tensors are contiguous runs of n elements (MOE_F32 or MOE_BF16), aligned to their element; n may
+ * be 0; at most 65536 of them. Outputs must overlap neither each other nor another tensor's grad.
+ * moe_clip_plan writes their table into `plan` (device, moe_clip_plan_size bytes, 16-byte aligned)
+ * by kernels on `stream` and fills `clip` (host). moe_clip_grads, on that stream or ordered behind
+ * it, may then be called any number of times while the tensors and the plan stay in place; calls
+ * that share a plan must not overlap. It reads `plan` for scratch too. Errors: MOE_ERR_INVALID_ARG
+ * (null or misaligned pointer, bad size, max_norm < 0 or NaN), MOE_ERR_UNSUPPORTED (types),
+ * MOE_ERR_WORKSPACE (plan missing, misaligned or too small). */
+typedef struct {
+  void *grad;        /* device */
+  void *out;         /* device; NULL: grad */
+  int64_t n;         /* elements */
+  moe_dtype_t dt;
+} moe_clip_tensor_t;
+typedef struct {     /* filled by moe_clip_plan */
+  void *plan;
+  int64_t chunks;
+  int32_t entries;
+  int32_t in_place;
+} moe_clip_t;
+int32_t moe_clip_plan_size(const moe_clip_tensor_t *tensors, int32_t count, size_t *bytes);
+int32_t moe_clip_plan(const moe_clip_tensor_t *tensors, int32_t count, void *plan,
+                      size_t plan_bytes, moe_clip_t *clip, void *stream);
+int32_t moe_clip_grads(const moe_clip_t *clip, float max_norm, float *norm, void *stream);
+
 /* Static text for a status code. */
 const char *moe_status_str(int32_t code);
 

@@ -33,6 +33,11 @@ EXPORTS = ("moe_workspace_size", "moe_layer_forward", "latent_moe_forward", "moe
            "moe_backward_workspace_size", "moe_layer_forward_train", "moe_layer_backward",
            "moe_layer_forward_static", "moe_few_workspace_size", "moe_few_forward",
            "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
+           "moe_sort_tokens_workspace_size", "moe_sort_tokens", "moe_sort_tokens_backward",
+           "moe_unsort_tokens", "moe_unsort_tokens_backward",
+           "moe_block_norm", "moe_block_residual", "moe_block_backward_workspace_size",
+           "moe_block_norm_backward", "moe_block_residual_backward",
+           "moe_clip_plan_size", "moe_clip_plan", "moe_clip_grads",
            "moe_status_str",
            "moe_trace_enable",
            "moe_trace_count", "moe_trace_read", "moe_trace_reset")
@@ -57,6 +62,15 @@ class MoeRouting(C.Structure):
 class MoeGrads(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("dx", "dW_r", "dW_up", "dW_down", "dWs_up",
                                           "dWs_down", "dW_in", "dW_out")]
+
+
+class MoeClipTensor(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dt", C.c_int32)]
+
+
+class MoeClip(C.Structure):
+    _fields_ = [("plan", C.c_void_p), ("chunks", C.c_int64), ("entries", C.c_int32),
+                ("in_place", C.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -98,6 +112,25 @@ def lib() -> C.CDLL:
             L.moe_mx_quantize.argtypes = [vp, i32, C.c_int64, i32, i32, vp, vp, vp]
             L.moe_mx_dequantize.argtypes = [vp, vp, i32, C.c_int64, i32, vp, i32, vp]
             L.moe_mx_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp]
+            f32, u32 = C.c_float, C.c_uint32
+            L.moe_sort_tokens_workspace_size.argtypes = [i32, i32, i32, C.POINTER(sz)]
+            L.moe_sort_tokens.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+            L.moe_sort_tokens_backward.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, i32,
+                                                   vp, vp]
+            L.moe_unsort_tokens.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp]
+            L.moe_unsort_tokens_backward.argtypes = [vp, i32, vp, i32, vp, vp, i32, i32, i32, i32,
+                                                     vp, vp, vp]
+            L.moe_block_norm.argtypes = [vp, vp, vp, i32, i32, i32, i32, f32, vp]
+            L.moe_block_residual.argtypes = [vp] * 7 + [i32, i32, i32, i32, u32, f32, f32, vp]
+            L.moe_block_backward_workspace_size.argtypes = [i32, i32, C.POINTER(sz)]
+            L.moe_block_norm_backward.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                                  f32, vp, sz, vp]
+            L.moe_block_residual_backward.argtypes = [vp] * 6 + [i32] + [vp] * 6 + [
+                i32, i32, i32, i32, u32, f32, f32, vp, sz, vp]
+            L.moe_clip_plan_size.argtypes = [C.POINTER(MoeClipTensor), i32, C.POINTER(sz)]
+            L.moe_clip_plan.argtypes = [C.POINTER(MoeClipTensor), i32, vp, sz, C.POINTER(MoeClip),
+                                        vp]
+            L.moe_clip_grads.argtypes = [C.POINTER(MoeClip), f32, vp, vp]
             L.moe_status_str.argtypes = [i32]
             L.moe_trace_enable.argtypes = [i32, C.c_char_p]
             L.moe_trace_count.argtypes = []

@@ -357,3 +357,5 @@ hipError_t launch_pairs_to_tokens(const float* du, const int32_t* pos, int T, in
 
 #include "mx_convert.hpp"
 #include "mx_tiles.hpp"
+#include "block_norm_kernels.hpp"
+#include "grad_clip_kernels.hpp"

@@ -10,10 +10,13 @@
 
 #include "moe.h"
 #include "backward.hpp"
+#include "block_norm.hpp"
 #include "few.hpp"
 #include "gemm_kt.hpp"
+#include "grad_clip.hpp"
 #include "kernels.hpp"
 #include "mx.hpp"
+#include "token_rows.hpp"
 
 using namespace moe;
 
@@ -1439,3 +1442,5 @@ const char* moe_status_str(int32_t code) {
 }
 
 }  // extern "C"
+
+#include "block_api.hpp"

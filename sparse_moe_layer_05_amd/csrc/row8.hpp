@@ -1,0 +1,85 @@
+// Rows of bf16 or fp32 values taken eight elements at a time (one 16-byte load or two), and sums
+// over the lanes that hold a row.
+#pragma once
+
+#include "common.hpp"
+#include "gemm.hpp"
+
+namespace moe {
+
+// Eight consecutive elements as they lie in memory.
+template <Elt T> struct Raw8;
+template <> struct Raw8<Elt::BF16> { uint4 q; };
+template <> struct Raw8<Elt::F32> { float4 a, b; };
+
+template <Elt T>
+__device__ __forceinline__ Raw8<T> load8(const void* p, int64_t i) {
+  if constexpr (T == Elt::BF16) {
+    return {*(const uint4*)((const uint16_t*)p + i)};
+  } else {
+    return {*(const float4*)((const float*)p + i), *(const float4*)((const float*)p + i + 4)};
+  }
+}
+
+template <Elt T>
+__device__ __forceinline__ Raw8<T> zero8() {
+  if constexpr (T == Elt::BF16) return {make_uint4(0, 0, 0, 0)};
+  else return {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+}
+
+template <Elt T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
+  if constexpr (T == Elt::BF16) {
+    const uint32_t w[4] = {r.q.x, r.q.y, r.q.z, r.q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+  }
+}
+
+template <Elt T>
+__device__ __forceinline__ Raw8<T> pack8(const float (&v)[8]) {
+  if constexpr (T == Elt::BF16)
+    return {make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]))};
+  else
+    return {make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
+}
+
+template <Elt T>
+__device__ __forceinline__ void store8(void* p, int64_t i, const Raw8<T>& r) {
+  if constexpr (T == Elt::BF16) {
+    *(uint4*)((uint16_t*)p + i) = r.q;
+  } else {
+    *(float4*)((float*)p + i) = r.a;
+    *(float4*)((float*)p + i + 4) = r.b;
+  }
+}
+
+// Sum over the 64 lanes of a wave, in every lane: rows of 16 lanes by shifts of 1, 2, 4 and 8, then
+// the rows' last lanes passed on; lane 63 ends with the total (a lane without a source adds 0).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111, 0xF>(v);   // row_shr:1
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+}  // namespace moe
