@@ -9,8 +9,8 @@
 // neither pass keeps statistics for the other. A row is held by 64 lanes (up to 2048 columns) or by
 // a workgroup of 128 to 512, at most 32 columns a lane. y is rounded before the next norm reads it:
 // the backward pass, which has y as it is stored, then differentiates the same function.
-// Sums run in fp32; where a sum of squares passes fp32 (values beyond 1e18) it is taken again in
-// fp64, a branch that no ordinary row takes.
+// Sums run in fp32; where a sum of squares passes fp32 it is taken again of smaller values, a branch
+// that no ordinary row takes.
 // Included once, by backward.hip.
 #pragma once
 
@@ -18,35 +18,42 @@
 #include "common.hpp"
 #include "row8.hpp"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace moe {
 namespace {
 namespace block_norm {
 
-// Sums of N values over the TPR lanes of a row (waves of a workgroup add through LDS in order).
-template <int TPR, int N, typename F>
-__device__ __forceinline__ void row_sum(F (&v)[N], double* lds) {
+// Sums over the TPR lanes of a row, in every lane. Where a row has several waves each adds all waves'
+// sums, one a lane. Two slots take turns, so one barrier a sum is enough: whoever writes a slot again
+// has passed the barrier of the other one, behind which nobody still reads it.
+template <int TPR>
+struct RowSum {
+  static constexpr int W = TPR / 64, kSlot = 3 * W;
+  float* lds;     // 2 * kSlot
+  int slot = 0;
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    static_assert(N <= 3 && W <= 16);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (TPR > 64) {
-    constexpr int W = TPR / 64;
-    F* red = (F*)lds;
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();   // the last sums' reads are done
-    if ((threadIdx.x & 63) == 0)
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    if constexpr (W > 1) {
+      const int lane = threadIdx.x & 63;
+      float* const at = lds + slot;
+      slot = kSlot - slot;
+      if (lane == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) red[wave * N + i] = v[i];
-    __syncthreads();
+        for (int i = 0; i < N; ++i) at[i * W + (threadIdx.x >> 6)] = v[i];
+      // (LDS alone is waited for: loads of the next row stay in flight)
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      F s = red[i];
-#pragma unroll
-      for (int q = 1; q < W; ++q) s += red[q * N + i];
-      v[i] = s;
+      for (int i = 0; i < N; ++i) v[i] = row16_sum(lane < W ? at[i * W + lane] : 0.f);
     }
   }
-}
+};
 
 __device__ __forceinline__ void load_w8(const void* w, Elt t, int c, float (&v)[8]) {
   if (!w) {
@@ -66,7 +73,13 @@ struct GateValue {
 };
 __device__ __forceinline__ GateValue gate_value(float q, bool sigmoid) {
   if (!sigmoid) return {q, 1.f};
-  const float e = expf(-fabsf(q)), inv = 1.f / (1.f + e);
+  // exp(-|q|) = 2^t (1 + r ln 2), t + r = -|q| log2(e) to 48 bits; below 2^-149 it is 0 (a NaN stays)
+  const float x = q < -104.f || q > 104.f ? -104.f : -fabsf(q);
+  const float t = x * 1.44269502f;
+  const float r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));
+  const float p2 = __builtin_amdgcn_exp2f(t), e = fmaf(p2 * r, 0.693147182f, p2);
+  // 1 / (1 + e), 1 + e in [1, 2]: the hardware's reciprocal and one Newton step
+  const float u = 1.f + e, v = __builtin_amdgcn_rcpf(u), inv = fmaf(v, fmaf(-u, v, 1.f), v);
   return q < 0.f ? GateValue{e * inv, inv} : GateValue{inv, e * inv};
 }
 
@@ -75,31 +88,44 @@ __device__ __forceinline__ float inv_rms(float ss, int H, float eps) {
 }
 __device__ __forceinline__ bool too_big(float s) { return fabsf(s) == __builtin_inff(); }
 
+// Rows whose sum of squares passes fp32 (values beyond 2^57) are summed again with their values times
+// kFar: 2^48 at most, while values that then underflow are below 2^-60 of the row's largest.
+constexpr float kFar = 0x1p-80f;
+__device__ __forceinline__ float inv_rms_far(float ss, int H, float eps) {   // of the values times kFar
+  return 1.f / sqrtf(ss / (float)H + eps * kFar * kFar);
+}
+
 // 1 / rms of the row held in v; ss: its fp32 sum of squares.
-template <int TPR, int NC>
-__device__ __forceinline__ float row_inv_rms(const float (&v)[NC][8], float ss, int H, float eps,
-                                             double* lds) {
+template <int TPR, Elt T, int NC>
+__device__ __forceinline__ float row_inv_rms(Raw8<T> (&v)[NC], float ss, int H, float eps,
+                                             RowSum<TPR>& sum) {
   if (__builtin_expect(too_big(ss), 0)) {   // the same in every lane of the row
-    double d[1] = {0.0};
+    float d[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+      float u[8];
+      forget(v[i]);
+      unpack8<T>(v[i], u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[0] += (double)v[i][e] * v[i][e];
-    row_sum<TPR, 1>(d, lds);
-    return (float)(1.0 / sqrt(d[0] / H + eps));
+      for (int e = 0; e < 8; ++e) d[0] = fmaf(u[e] * kFar, u[e] * kFar, d[0]);
+    }
+    sum(d);
+    return inv_rms_far(d[0], H, eps) * kFar;
   }
   return inv_rms(ss, H, eps);
 }
 
-template <int TPR> constexpr int kThreadsOf = TPR < 256 ? (TPR == 64 ? 256 : TPR) : TPR;
+template <int TPR> constexpr int kThreadsOf = TPR == 64 ? 256 : TPR;
 template <int TPR> constexpr int kRowsOf = kThreadsOf<TPR> / TPR;
 
 template <Elt T, int TPR, int NC, bool RES>
 __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockShape b,
                                                                         BlockForward p) {
-  __shared__ double lds[TPR > 64 ? TPR / 64 : 1];
-  const int lane = threadIdx.x % TPR;
-  const int row = blockIdx.x * kRowsOf<TPR> + threadIdx.x / TPR;
+  __shared__ float lds[2 * RowSum<TPR>::kSlot];
+  RowSum<TPR> sum{lds};
+  const int lane = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int row = TPR == 64 ? blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
+                            : blockIdx.x;
   if (row >= b.T) return;   // whole waves, and workgroups where a row has a barrier
   const int64_t base = (int64_t)row * b.H;
   int col[NC];
@@ -117,21 +143,19 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockSha
       if (b.gate_kind == Gate::Element) gr[i] = load8<T>(p.gate, base + col[i]);
     }
   }
-  float v[NC][8];
-#pragma unroll
-  for (int i = 0; i < NC; ++i) unpack8<T>(xr[i], v[i]);
   if constexpr (RES) {
     float rf = 1.f;
     if (b.norm) {
-      float fv[NC][8], ss[1] = {0.f};
+      float ss[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        unpack8<T>(fr[i], fv[i]);
+        float f[8];
+        unpack8<T>(fr[i], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] = fmaf(fv[i][e], fv[i][e], ss[0]);
+        for (int e = 0; e < 8; ++e) ss[0] = fmaf(f[e], f[e], ss[0]);
       }
-      row_sum<TPR, 1>(ss, lds);
-      rf = row_inv_rms<TPR, NC>(fv, ss[0], b.H, b.eps, lds);
+      sum(ss);
+      rf = row_inv_rms<TPR, T, NC>(fr, ss[0], b.H, b.eps, sum);
     }
     float at = b.scale;   // scale, times the row's gate
     if (b.gate_kind == Gate::Token) {
@@ -141,200 +165,285 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockSha
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       if (!ok[i]) continue;
-      float w[8], f[8], g[8];
+      float v[8], w[8], f[8], g[8];
       load_w8(p.w, b.w_t, col[i], w);
+      unpack8<T>(xr[i], v);
       unpack8<T>(fr[i], f);
       unpack8<T>(gr[i], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float z = f[e] * rf * w[e] * at;
         if (b.gate_kind == Gate::Element) z *= gate_value(g[e], b.sigmoid).a;
-        v[i][e] += z;
+        v[e] += z;
       }
-      const Raw8<T> out = pack8<T>(v[i]);
-      store8<T>(p.y, base + col[i], out);
-      unpack8<T>(out, v[i]);
+      xr[i] = pack8<T>(v);
+      store8<T>(p.y, base + col[i], xr[i]);
     }
     if (!p.h) return;
   }
   float ss[1] = {0.f};
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
+  for (int i = 0; i < NC; ++i) {
+    float v[8];
+    unpack8<T>(xr[i], v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss[0] = fmaf(v[i][e], v[i][e], ss[0]);
-  row_sum<TPR, 1>(ss, lds);
-  const float r = row_inv_rms<TPR, NC>(v, ss[0], b.H, b.eps, lds);
+    for (int e = 0; e < 8; ++e) ss[0] = fmaf(v[e], v[e], ss[0]);
+  }
+  sum(ss);
+  const float r = row_inv_rms<TPR, T, NC>(xr, ss[0], b.H, b.eps, sum);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     if (!ok[i]) continue;
-    float w[8], o[8];
+    float v[8], w[8], o[8];
     load_w8(p.w_next, b.w_t, col[i], w);
+    unpack8<T>(xr[i], v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = v[i][e] * r * w[e];
+    for (int e = 0; e < 8; ++e) o[e] = v[e] * r * w[e];
     store8<T>(p.h, base + col[i], pack8<T>(o));
   }
 }
 
-// Rows walker, walker + walkers, .. of one walker (a wave, or a workgroup where a row needs one);
-// its sums of dw and dw_next over its rows go to rows `walker` of two slabs [walkers][H].
+// A weight of one lane group's columns, kept in LDS as fp32 for every row of the walk: group g's eight
+// values as two 16-byte halves, each half of neighbouring groups side by side.
+template <int GROUPS>
+struct LdsWeight {
+  float4 v[2][GROUPS];
+  __device__ void fill(const void* w, Elt t, int H) {
+    for (int g = threadIdx.x; g < GROUPS; g += blockDim.x) {
+      float u[8] = {};
+      if (g * 8 < H) load_w8(w, t, g * 8, u);
+      put(g, u);
+    }
+  }
+  __device__ void put(int g, const float (&u)[8]) {
+    v[0][g] = make_float4(u[0], u[1], u[2], u[3]);
+    v[1][g] = make_float4(u[4], u[5], u[6], u[7]);
+  }
+  __device__ void add(int g, float (&u)[8]) const {
+    float w[8];
+    get(g, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] += w[e];
+  }
+  __device__ void get(int g, float (&u)[8]) const {
+    const float4 a = v[0][g], b = v[1][g];
+    u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
+    u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+  }
+};
+
+// Rows walker, walker + walkers, .. of one walker (a wave, or a workgroup where a row needs one). Sums
+// of dw and dw_next over a workgroup's rows go to its row of two slabs [workgroups][H].
 template <Elt T, Elt DH, int TPR, int NC, bool RES>
 __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockShape b,
                                                                          BlockBackward p,
-                                                                         int walkers,
                                                                          float* part_w,
                                                                          float* part_n) {
-  __shared__ double lds[TPR > 64 ? 3 * TPR / 64 : 1];
-  const int lane = threadIdx.x % TPR;
-  const int walker = blockIdx.x * kRowsOf<TPR> + threadIdx.x / TPR;
-  if (walker >= walkers) return;
-  int col[NC];
+  constexpr int kEs = T == Elt::BF16 ? 2 : 4, kHs = DH == Elt::BF16 ? 2 : 4;
+  __shared__ float lds[2 * RowSum<TPR>::kSlot];
+  RowSum<TPR> sum{lds};
+  __shared__ LdsWeight<TPR * NC> lw_next;
+  __shared__ LdsWeight<RES ? TPR * NC : 1> lw;
+  lw_next.fill(p.w_next, b.w_t, b.H);
+  if constexpr (RES) lw.fill(p.w, b.w_t, b.H);
+  __syncthreads();
+  // (the walker is the same in every lane of a wave: addresses are a scalar row and a lane's column)
+  const int lane = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int walker = TPR == 64 ? blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
+                               : blockIdx.x;
+  const int walkers = gridDim.x * kRowsOf<TPR>;
+  uint32_t col[NC];
   bool ok[NC];
   float sw[NC][8] = {}, sn[NC][8] = {};
+  const float inv_h = 1.f / (float)b.H;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     col[i] = (lane + i * TPR) * 8;
-    ok[i] = col[i] < b.H;
+    ok[i] = col[i] < (uint32_t)b.H;
   }
-  for (int row = walker; row < b.T; row += walkers) {
-    const int64_t base = (int64_t)row * b.H;
-    Raw8<T> yr[NC], dr[NC], fr[NC], gr[NC];
-    Raw8<DH> hr[NC];
+  // A row's operands are loaded into the registers of the row before as soon as that row is done
+  // with them, so that loads are in flight during the sums, whose barriers wait for LDS alone.
+  Raw8<T> yr[NC], dr[NC], fr[NC], gr[NC];
+  Raw8<DH> hr[NC];
+  const bool element = b.gate_kind == Gate::Element, token = b.gate_kind == Gate::Token;
+  const void* const gates = element ? p.gate : nullptr;
+  auto load_y = [&](int row) {
+    const RowBuffer<T> y(p.y, row, b.H, row < b.T && p.dh);
+    const RowBuffer<DH> h(p.dh, row, b.H, row < b.T);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      yr[i] = dr[i] = fr[i] = gr[i] = zero8<T>();
-      hr[i] = zero8<DH>();
-      if (!ok[i]) continue;
-      if (p.dh) {
-        yr[i] = load8<T>(p.y, base + col[i]);
-        hr[i] = load8<DH>(p.dh, base + col[i]);
-      }
-      if (p.dy) dr[i] = load8<T>(p.dy, base + col[i]);
-      if constexpr (RES) {
-        fr[i] = load8<T>(p.f, base + col[i]);
-        if (b.gate_kind == Gate::Element) gr[i] = load8<T>(p.gate, base + col[i]);
-      }
+      yr[i] = y.load(col[i]);
+      hr[i] = h.load(col[i]);
     }
+  };
+  auto load_row = [&](Raw8<T>(&r)[NC], const void* base, int row) {
+    const RowBuffer<T> rb(base, row, b.H, row < b.T);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) r[i] = rb.load(col[i]);
+  };
+  load_y(walker);
+  if constexpr (RES) load_row(fr, p.f, walker);
+  load_row(dr, p.dy, walker);
+  if constexpr (RES) load_row(gr, gates, walker);
+  for (int row = walker; row < b.T; row += walkers) {
+    const int next = row + walkers;   // (T and the walkers are far below 2^30)
     // sum y^2, sum (dh w_next) y, sum f^2
     float s[3] = {0.f, 0.f, 0.f};
     float d[NC][8];   // d, the gradient reaching y
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      float y[8], h[8], w[8] = {}, f[8];
+      float y[8], h[8], w[8], f[8];
       unpack8<T>(yr[i], y);
       unpack8<DH>(hr[i], h);
-      unpack8<T>(fr[i], f);
-      if (p.dh && ok[i]) load_w8(p.w_next, b.w_t, col[i], w);
+      lw_next.get(lane + i * TPR, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         d[i][e] = h[e] * w[e];
         s[0] = fmaf(y[e], y[e], s[0]);
         s[1] = fmaf(d[i][e], y[e], s[1]);
-        s[2] = fmaf(f[e], f[e], s[2]);
       }
+      if constexpr (RES) {
+        unpack8<T>(fr[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[2] = fmaf(f[e], f[e], s[2]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    row_sum<TPR, 3>(s, lds);
+    sum(s);
     if (p.dh) {
-      float r = inv_rms(s[0], b.H, b.eps), m = s[1] * r / (float)b.H;
-      if (__builtin_expect(too_big(s[0]) || too_big(s[1]), 0)) {   // both sums again, in fp64
-        double q[2] = {0.0, 0.0};
+      float r = inv_rms(s[0], b.H, b.eps), m = s[1] * r * inv_h;
+      if (__builtin_expect(too_big(s[0]), 0)) {
+        float q[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           float y[8];
+          forget(yr[i]);
           unpack8<T>(yr[i], y);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            q[0] += (double)y[e] * y[e];
-            q[1] += (double)d[i][e] * y[e];
+            q[0] = fmaf(y[e] * kFar, y[e] * kFar, q[0]);
+            q[1] = fmaf(d[i][e], y[e] * kFar, q[1]);
           }
         }
-        row_sum<TPR, 2>(q, lds);
-        const double rd = 1.0 / sqrt(q[0] / b.H + b.eps);
-        r = (float)rd;
-        m = (float)(q[1] * rd / b.H);
+        sum(q);
+        const float far = inv_rms_far(q[0], b.H, b.eps);
+        r = far * kFar;
+        m = q[1] * far * inv_h;
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         float y[8], h[8];
+        forget(yr[i]);
+        forget(hr[i]);
         unpack8<T>(yr[i], y);
         unpack8<DH>(hr[i], h);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float n = y[e] * r;
-          d[i][e] = r * (d[i][e] - n * m);
+          d[i][e] = r * fmaf(-n, m, d[i][e]);
           sn[i][e] = fmaf(h[e], n, sn[i][e]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    load_y(next);
+    {
+      const RowBuffer<T> xo(p.dx, row, b.H, true);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      float dy[8];
-      unpack8<T>(dr[i], dy);
+      for (int i = 0; i < NC; ++i) {
+        float dy[8];
+        unpack8<T>(dr[i], dy);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[i][e] += dy[e];
-      if (ok[i]) store8<T>(p.dx, base + col[i], pack8<T>(d[i]));
+        for (int e = 0; e < 8; ++e) d[i][e] += dy[e];
+        xo.store(col[i], pack8<T>(d[i]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    load_row(dr, p.dy, next);
     if constexpr (RES) {
-      float rf = 1.f;
-      if (b.norm) {
-        rf = inv_rms(s[2], b.H, b.eps);
-        if (__builtin_expect(too_big(s[2]), 0)) {
-          float fv[NC][8];
-#pragma unroll
-          for (int i = 0; i < NC; ++i) unpack8<T>(fr[i], fv[i]);
-          rf = row_inv_rms<TPR, NC>(fv, s[2], b.H, b.eps, lds);
-        }
-      }
+      const float rf = b.norm ? row_inv_rms<TPR, T, NC>(fr, s[2], b.H, b.eps, sum) : 1.f;
       GateValue gt = {1.f, 1.f};   // the row's gate
-      if (b.gate_kind == Gate::Token) gt = gate_value(((const float*)p.gate)[row], b.sigmoid);
+      if (token) gt = gate_value(((const float*)p.gate)[row], b.sigmoid);
       // sum d a w n(f): the mean in the norm's gradient and, with a = 1, the token gate's gradient
       float q[1] = {0.f};
+      const RowBuffer<T> go(p.dgate, row, b.H, element);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        if (!ok[i]) continue;
-        float w[8], f[8], g[8], o[8];
-        load_w8(p.w, b.w_t, col[i], w);
+        float w[8], f[8];
+        lw.get(lane + i * TPR, w);
+        forget(fr[i]);
         unpack8<T>(fr[i], f);
-        unpack8<T>(gr[i], g);
+        if (element) {
+          float g[8], o[8];
+          unpack8<T>(gr[i], g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = f[e] * rf;
-          const float ds = d[i][e] * b.scale;
-          float a = gt.a;
-          if (b.gate_kind == Gate::Element) {
+          for (int e = 0; e < 8; ++e) {
             const GateValue ge = gate_value(g[e], b.sigmoid);
-            a = ge.a;
-            o[e] = ds * n * w[e] * ge.rest * (b.sigmoid ? a : 1.f);
+            const float n = f[e] * rf, ds = d[i][e] * b.scale, dz = ds * ge.a;
+            o[e] = (b.sigmoid ? dz : ds) * ge.rest * (n * w[e]);
+            sw[i][e] = fmaf(dz, n, sw[i][e]);
+            d[i][e] = dz * w[e];
+            q[0] = fmaf(d[i][e], n, q[0]);
           }
-          const float dz = ds * a;
-          sw[i][e] = fmaf(dz, n, sw[i][e]);
-          d[i][e] = dz * w[e];
-          // (a token's gate is taken out again: its own gradient needs the sum without it)
-          q[0] = fmaf(b.gate_kind == Gate::Token ? ds * w[e] : d[i][e], n, q[0]);
+          go.store(col[i], pack8<T>(o));
+        } else {
+          // (the sum is of the values without the token's gate, whose own gradient needs it so)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float n = f[e] * rf, ds = d[i][e] * b.scale;
+            sw[i][e] = fmaf(ds * gt.a, n, sw[i][e]);
+            const float dw = ds * w[e];
+            q[0] = fmaf(dw, n, q[0]);
+            d[i][e] = dw * gt.a;
+          }
         }
-        if (b.gate_kind == Gate::Element && p.dgate)
-          store8<T>(p.dgate, base + col[i], pack8<T>(o));
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (b.norm || b.gate_kind == Gate::Token) row_sum<TPR, 1>(q, lds);
-      if (b.gate_kind == Gate::Token && lane == 0 && p.dgate)
+      load_row(gr, gates, next);
+      if (b.norm || token) sum(q);
+      if (token && lane == 0 && p.dgate)
         ((float*)p.dgate)[row] = q[0] * gt.rest * (b.sigmoid ? gt.a : 1.f);
-      const float m = b.norm ? (b.gate_kind == Gate::Token ? q[0] * gt.a : q[0]) / (float)b.H : 0.f;
+      const float m = b.norm ? q[0] * gt.a * inv_h : 0.f;   // (gt.a is 1 but for a token's gate)
+      const RowBuffer<T> fo(p.df, row, b.H, true);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        if (!ok[i]) continue;
         float f[8], o[8];
+        forget(fr[i]);
         unpack8<T>(fr[i], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          o[e] = b.norm ? rf * (d[i][e] - f[e] * rf * m) : d[i][e];
-        store8<T>(p.df, base + col[i], pack8<T>(o));
+          o[e] = b.norm ? rf * fmaf(-f[e] * rf, m, d[i][e]) : d[i][e];
+        fo.store(col[i], pack8<T>(o));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      load_row(fr, p.f, next);
+    }
+  }
+  const int64_t mine = (int64_t)blockIdx.x * b.H;
+  if constexpr (TPR == 64) {   // the workgroup's four walkers, one after another
+    const int wave = threadIdx.x >> 6;
+    for (int q = 0; q < 4; ++q) {
+      __syncthreads();
+      if (wave != q) continue;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if (q) {
+          lw_next.add(lane + i * TPR, sn[i]);
+          if constexpr (RES) lw.add(lane + i * TPR, sw[i]);
+        }
+        if (q < 3) {
+          lw_next.put(lane + i * TPR, sn[i]);
+          if constexpr (RES) lw.put(lane + i * TPR, sw[i]);
+        }
       }
     }
+    if (wave != 3) return;
   }
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     if (!ok[i]) continue;
-    if (part_w) store8<Elt::F32>(part_w, (int64_t)walker * b.H + col[i], pack8<Elt::F32>(sw[i]));
-    if (part_n) store8<Elt::F32>(part_n, (int64_t)walker * b.H + col[i], pack8<Elt::F32>(sn[i]));
+    if (part_w) store8<Elt::F32>(part_w, mine + col[i], pack8<Elt::F32>(sw[i]));
+    if (part_n) store8<Elt::F32>(part_n, mine + col[i], pack8<Elt::F32>(sn[i]));
   }
 }
 
@@ -342,7 +451,7 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
 constexpr int kRedCols = 16, kRedRows = 64;
 __global__ __launch_bounds__(kRedCols * kRedRows) void block_reduce_kernel(const float* part_w,
                                                                            const float* part_n,
-                                                                           int walkers, int H,
+                                                                           int rows, int H,
                                                                            float* dw,
                                                                            float* dw_next) {
   __shared__ float red[kRedRows][kRedCols + 1];
@@ -352,8 +461,16 @@ __global__ __launch_bounds__(kRedCols * kRedRows) void block_reduce_kernel(const
   const int c = threadIdx.x % kRedCols, g = threadIdx.x / kRedCols;
   const int col = blockIdx.x * kRedCols + c;
   float s = 0.f;
-  if (col < H)
-    for (int r = g; r < walkers; r += kRedRows) s += part[(int64_t)r * H + col];
+  if (col < H) {
+    for (int r = g; r < rows; r += 8 * kRedRows) {   // eight rows in flight
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = r + i * kRedRows < rows ? part[(int64_t)(r + i * kRedRows) * H + col] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+  }
   red[g][c] = s;
   __syncthreads();
 #pragma unroll
@@ -364,9 +481,9 @@ __global__ __launch_bounds__(kRedCols * kRedRows) void block_reduce_kernel(const
   if (g == 0 && col < H) out[col] = red[0][c];
 }
 
-// Rows are held by the fewest lanes that take at most 32 columns each.
+// Lanes of a row and groups of eight columns a lane, forward and backward.
 template <typename Fn>
-hipError_t with_shape(int H, Fn&& fn) {
+void with_forward_shape(int H, Fn&& fn) {
   const int g = (H + 7) / 8;
 #define MOE_SHAPE(TPR, NC) fn(std::integral_constant<int, TPR>(), std::integral_constant<int, NC>())
   if (g <= 64) MOE_SHAPE(64, 1);
@@ -379,15 +496,33 @@ hipError_t with_shape(int H, Fn&& fn) {
   else if (g <= 1024) MOE_SHAPE(256, 4);
   else if (g <= 1536) MOE_SHAPE(512, 3);
   else MOE_SHAPE(512, 4);
+}
+template <typename Fn>
+void with_backward_shape(int H, Fn&& fn) {
+  const int g = (H + 7) / 8;
+  if (g <= 64) MOE_SHAPE(64, 1);
+  else if (g <= 128) MOE_SHAPE(64, 2);
+  else if (g <= 256) MOE_SHAPE(128, 2);
+  else if (g <= 384) MOE_SHAPE(192, 2);
+  else if (g <= 512) MOE_SHAPE(256, 2);
+  else if (g <= 768) MOE_SHAPE(384, 2);
+  else if (g <= 1024) MOE_SHAPE(512, 2);
+  else if (g <= 1536) MOE_SHAPE(768, 2);
+  else MOE_SHAPE(1024, 2);
 #undef MOE_SHAPE
-  return hipGetLastError();
 }
 
-// Walkers of the backward pass: each ends with a row of partial sums, so many rows get few.
-int block_walkers(int T, int H) {
-  const int most = 1024;
-  (void)H;
-  return T < most ? T : most;
+// Workgroups of the backward pass: as many on each of the 256 CUs as its registers hold, since each
+// ends with a row of partial sums and a second round would leave most CUs idle.
+int backward_groups(int T, int H) {
+  int groups = 0;
+  with_backward_shape(H, [&](auto tpr, auto nc) {
+    constexpr int TPR = tpr(), waves = kThreadsOf<TPR> / 64;
+    constexpr int most = TPR == 192 ? 9 : nc() == 1 ? 16 : 12;
+    constexpr int per_cu = most / waves > 0 ? most / waves : 1;
+    groups = std::min((T + kRowsOf<TPR> - 1) / kRowsOf<TPR>, 256 * per_cu);
+  });
+  return groups;
 }
 
 }  // namespace block_norm
@@ -398,7 +533,7 @@ using namespace block_norm;
 hipError_t launch_block_forward(const BlockShape& b, const BlockForward& p, hipStream_t s) {
   if (b.T <= 0) return hipSuccess;
   if (b.H > kBlockMaxH) return hipErrorInvalidValue;
-  return with_shape(b.H, [&](auto tpr, auto nc) {
+  with_forward_shape(b.H, [&](auto tpr, auto nc) {
     constexpr int TPR = tpr(), NC = nc();
     const dim3 grid((unsigned)((b.T + kRowsOf<TPR> - 1) / kRowsOf<TPR>)), block(kThreadsOf<TPR>);
     if (b.t == Elt::BF16) {
@@ -409,21 +544,22 @@ hipError_t launch_block_forward(const BlockShape& b, const BlockForward& p, hipS
       else hipLaunchKernelGGL((block_forward_kernel<Elt::F32, TPR, NC, false>), grid, block, 0, s, b, p);
     }
   });
+  return hipGetLastError();
 }
 
-size_t block_part_floats(int T, int H) { return 2 * (size_t)block_walkers(T, H) * H; }
+size_t block_part_floats(int T, int H) { return 2 * (size_t)backward_groups(T, H) * H; }
 
 hipError_t launch_block_backward(const BlockShape& b, const BlockBackward& p, hipStream_t s) {
   if (b.H > kBlockMaxH) return hipErrorInvalidValue;
-  const int walkers = block_walkers(b.T, b.H);
+  const int groups = backward_groups(b.T, b.H);
   float* part_w = p.dw ? p.part : nullptr;
-  float* part_n = p.dw_next ? p.part + (size_t)walkers * b.H : nullptr;
+  float* part_n = p.dw_next ? p.part + (size_t)groups * b.H : nullptr;
   if (b.T > 0) {
-    const hipError_t e = with_shape(b.H, [&](auto tpr, auto nc) {
+    with_backward_shape(b.H, [&](auto tpr, auto nc) {
       constexpr int TPR = tpr(), NC = nc();
-      const dim3 grid((unsigned)((walkers + kRowsOf<TPR> - 1) / kRowsOf<TPR>)), block(kThreadsOf<TPR>);
+      const dim3 grid((unsigned)groups), block(kThreadsOf<TPR>);
 #define MOE_BWD(X, DH, RES) \
-  hipLaunchKernelGGL((block_backward_kernel<X, DH, TPR, NC, RES>), grid, block, 0, s, b, p, walkers, part_w, part_n)
+  hipLaunchKernelGGL((block_backward_kernel<X, DH, TPR, NC, RES>), grid, block, 0, s, b, p, part_w, part_n)
       if (b.t == Elt::F32) {
         if (p.f) MOE_BWD(Elt::F32, Elt::F32, true); else MOE_BWD(Elt::F32, Elt::F32, false);
       } else if (p.dh_t == Elt::F32) {
@@ -433,11 +569,12 @@ hipError_t launch_block_backward(const BlockShape& b, const BlockBackward& p, hi
       }
 #undef MOE_BWD
     });
-    if (e != hipSuccess) return e;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!p.dw && !p.dw_next)) return e;
   }
   if (!p.dw && !p.dw_next) return hipSuccess;
   hipLaunchKernelGGL(block_reduce_kernel, dim3((b.H + kRedCols - 1) / kRedCols, 2),
-                     dim3(kRedCols * kRedRows), 0, s, part_w, part_n, walkers, b.H, p.dw, p.dw_next);
+                     dim3(kRedCols * kRedRows), 0, s, part_w, part_n, groups, b.H, p.dw, p.dw_next);
   return hipGetLastError();
 }
 

@@ -42,6 +42,43 @@ __device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
   }
 }
 
+// One row as a buffer of its own: columns past its end, and every column of an absent row, load as
+// zeros and store nothing, so that lanes need no branch.
+template <Elt T>
+struct RowBuffer {
+  static constexpr uint32_t kElt = T == Elt::BF16 ? 2 : 4;
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ RowBuffer(const void* base, int64_t row, int n, bool present)
+      : r(__builtin_amdgcn_make_buffer_rsrc((char*)base + row * n * kElt, (short)0,
+                                            present && base ? (int)(n * kElt) : 0, 0x00020000)) {}
+  __device__ __forceinline__ Raw8<T> load(uint32_t col) const {
+    Raw8<T> out;
+    if constexpr (T == Elt::BF16) {
+      out.q = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt, 0, 0));
+    } else {
+      out.a = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt, 0, 0));
+      out.b = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt + 16, 0, 0));
+    }
+    return out;
+  }
+  __device__ __forceinline__ void store(uint32_t col, const Raw8<T>& v) const {
+    if constexpr (T == Elt::BF16) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.q), r, col * kElt, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.a), r, col * kElt, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.b), r, col * kElt + 16, 0, 0);
+    }
+  }
+};
+
+// Hides from the compiler that r was unpacked before, so that a later pass over a row unpacks it again
+// instead of keeping both forms in registers.
+__device__ __forceinline__ void forget(Raw8<Elt::BF16>& r) {
+  asm volatile("" : "+v"(r.q.x), "+v"(r.q.y), "+v"(r.q.z), "+v"(r.q.w));
+}
+__device__ __forceinline__ void forget(Raw8<Elt::F32>&) {}
+
 template <Elt T>
 __device__ __forceinline__ Raw8<T> pack8(const float (&v)[8]) {
   if constexpr (T == Elt::BF16)
@@ -75,6 +112,14 @@ __device__ __forceinline__ float wave_sum(float v) {
   v = dpp_add<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
   v = dpp_add<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// Sum over the first 16 lanes, in every lane.
+__device__ __forceinline__ float row16_sum(float v) {
+  v = dpp_add<0x111, 0xF>(v);
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 15));
 }
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
