@@ -30,14 +30,17 @@ namespace block_norm {
 // has passed the barrier of the other one, behind which nobody still reads it.
 template <int TPR>
 struct RowSum {
-  static constexpr int W = TPR / 64, kSlot = 3 * W;
+  static constexpr int W = TPR > 64 ? TPR / 64 : 1, kSlot = 3 * W;
   float* lds;     // 2 * kSlot
   int slot = 0;
   template <int N>
   __device__ __forceinline__ void operator()(float (&v)[N]) {
     static_assert(N <= 3 && W <= 16);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    for (int i = 0; i < N; ++i) {
+      if constexpr (TPR < 64) v[i] = group_sum<TPR>(v[i]);
+      else v[i] = wave_sum(v[i]);
+    }
     if constexpr (W > 1) {
       const int lane = threadIdx.x & 63;
       float* const at = lds + slot;
@@ -115,32 +118,53 @@ __device__ __forceinline__ float row_inv_rms(Raw8<T> (&v)[NC], float ss, int H, 
   return inv_rms(ss, H, eps);
 }
 
-template <int TPR> constexpr int kThreadsOf = TPR == 64 ? 256 : TPR;
-template <int TPR> constexpr int kRowsOf = kThreadsOf<TPR> / TPR;
+// Where a lane works: rows of TPR lanes each, several of them side by side in a wave where they are
+// short, and four waves a workgroup unless a row needs a workgroup of its own.
+template <int TPR> constexpr int kThreadsOf = TPR <= 64 ? 256 : TPR;
+template <int TPR> constexpr int kRowsOf = kThreadsOf<TPR> / TPR;         // rows of a workgroup
+template <int TPR> constexpr int kRowsOfWave = TPR < 64 ? 64 / TPR : 1;
+template <int TPR, int NC>
+struct Place {
+  int lane, sub;       // lane of its row, row of the wave's
+  int row0;            // the wave's first row: the same in every lane, so that addresses are scalar
+  uint32_t at[NC];     // the lane's elements, counted from the first row; kAway past the row
+  __device__ __forceinline__ explicit Place(int H) {
+    lane = TPR <= 64 ? threadIdx.x & (TPR - 1) : threadIdx.x;
+    sub = TPR < 64 ? (threadIdx.x & 63) / TPR : 0;
+    row0 = blockIdx.x * kRowsOf<TPR>;
+    if constexpr (TPR <= 64)
+      row0 += __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kRowsOfWave<TPR>;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int col = group(i) * 8;
+      at[i] = col < H ? (uint32_t)(sub * H + col) : kAway;
+    }
+  }
+  __device__ __forceinline__ int group(int i) const { return lane + i * TPR; }
+  __device__ __forceinline__ bool in_row(int i) const { return at[i] != kAway; }
+  // rows of the wave at `row` that there are
+  __device__ __forceinline__ static int rows(int row, int T) { return min(T - row, kRowsOfWave<TPR>); }
+};
 
 template <Elt T, int TPR, int NC, bool RES>
 __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockShape b,
                                                                         BlockForward p) {
   __shared__ float lds[2 * RowSum<TPR>::kSlot];
   RowSum<TPR> sum{lds};
-  const int lane = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const int row = TPR == 64 ? blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
-                            : blockIdx.x;
-  if (row >= b.T) return;   // whole waves, and workgroups where a row has a barrier
-  const int64_t base = (int64_t)row * b.H;
-  int col[NC];
-  bool ok[NC];
+  const Place<TPR, NC> me(b.H);
+  const int rows = me.rows(me.row0, b.T), row = me.row0 + me.sub;
+  if (rows <= 0) return;   // whole waves, and workgroups where a row has a barrier
   Raw8<T> xr[NC], fr[NC], gr[NC];
+  {
+    const RowBuffer<T> x(p.x, me.row0, rows, b.H), f(p.f, me.row0, rows, b.H);
+    const RowBuffer<T> g(b.gate_kind == Gate::Element ? p.gate : nullptr, me.row0, rows, b.H);
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    col[i] = (lane + i * TPR) * 8;
-    ok[i] = col[i] < b.H;
-    xr[i] = fr[i] = gr[i] = zero8<T>();
-    if (!ok[i]) continue;
-    xr[i] = load8<T>(p.x, base + col[i]);
-    if constexpr (RES) {
-      fr[i] = load8<T>(p.f, base + col[i]);
-      if (b.gate_kind == Gate::Element) gr[i] = load8<T>(p.gate, base + col[i]);
+    for (int i = 0; i < NC; ++i) {
+      xr[i] = x.load(me.at[i]);
+      if constexpr (RES) {
+        fr[i] = f.load(me.at[i]);
+        gr[i] = g.load(me.at[i]);
+      }
     }
   }
   if constexpr (RES) {
@@ -158,15 +182,14 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockSha
       rf = row_inv_rms<TPR, T, NC>(fr, ss[0], b.H, b.eps, sum);
     }
     float at = b.scale;   // scale, times the row's gate
-    if (b.gate_kind == Gate::Token) {
-      const float q = ((const float*)p.gate)[row];
-      at *= gate_value(q, b.sigmoid).a;
-    }
+    if (b.gate_kind == Gate::Token)
+      at *= gate_value(row < b.T ? ((const float*)p.gate)[row] : 0.f, b.sigmoid).a;
+    const RowBuffer<T> y(p.y, me.row0, rows, b.H);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      if (!ok[i]) continue;
+      if (!me.in_row(i)) continue;
       float v[8], w[8], f[8], g[8];
-      load_w8(p.w, b.w_t, col[i], w);
+      load_w8(p.w, b.w_t, me.group(i) * 8, w);
       unpack8<T>(xr[i], v);
       unpack8<T>(fr[i], f);
       unpack8<T>(gr[i], g);
@@ -177,7 +200,7 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockSha
         v[e] += z;
       }
       xr[i] = pack8<T>(v);
-      store8<T>(p.y, base + col[i], xr[i]);
+      y.store(me.at[i], xr[i]);
     }
     if (!p.h) return;
   }
@@ -191,15 +214,16 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockSha
   }
   sum(ss);
   const float r = row_inv_rms<TPR, T, NC>(xr, ss[0], b.H, b.eps, sum);
+  const RowBuffer<T> h(p.h, me.row0, rows, b.H);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    if (!ok[i]) continue;
+    if (!me.in_row(i)) continue;
     float v[8], w[8], o[8];
-    load_w8(p.w_next, b.w_t, col[i], w);
+    load_w8(p.w_next, b.w_t, me.group(i) * 8, w);
     unpack8<T>(xr[i], v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = v[e] * r * w[e];
-    store8<T>(p.h, base + col[i], pack8<T>(o));
+    h.store(me.at[i], pack8<T>(o));
   }
 }
 
@@ -232,35 +256,21 @@ struct LdsWeight {
   }
 };
 
-// Rows walker, walker + walkers, .. of one walker (a wave, or a workgroup where a row needs one). Sums
-// of dw and dw_next over a workgroup's rows go to its row of two slabs [workgroups][H].
+// A workgroup takes every gridDim.x-th kRowsOf rows; sums of dw and dw_next over its rows go to its row
+// of two slabs [workgroups][H].
 template <Elt T, Elt DH, int TPR, int NC, bool RES>
 __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockShape b,
                                                                          BlockBackward p,
                                                                          float* part_w,
                                                                          float* part_n) {
-  constexpr int kEs = T == Elt::BF16 ? 2 : 4, kHs = DH == Elt::BF16 ? 2 : 4;
   __shared__ float lds[2 * RowSum<TPR>::kSlot];
-  RowSum<TPR> sum{lds};
   __shared__ LdsWeight<TPR * NC> lw_next;
   __shared__ LdsWeight<RES ? TPR * NC : 1> lw;
-  lw_next.fill(p.w_next, b.w_t, b.H);
-  if constexpr (RES) lw.fill(p.w, b.w_t, b.H);
-  __syncthreads();
-  // (the walker is the same in every lane of a wave: addresses are a scalar row and a lane's column)
-  const int lane = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const int walker = TPR == 64 ? blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
-                               : blockIdx.x;
-  const int walkers = gridDim.x * kRowsOf<TPR>;
-  uint32_t col[NC];
-  bool ok[NC];
-  float sw[NC][8] = {}, sn[NC][8] = {};
+  RowSum<TPR> sum{lds};
+  const Place<TPR, NC> me(b.H);
+  const int step = gridDim.x * kRowsOf<TPR>;
   const float inv_h = 1.f / (float)b.H;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    col[i] = (lane + i * TPR) * 8;
-    ok[i] = col[i] < (uint32_t)b.H;
-  }
+  float sw[NC][8] = {}, sn[NC][8] = {};
   // A row's operands are loaded into the registers of the row before as soon as that row is done
   // with them, so that loads are in flight during the sums, whose barriers wait for LDS alone.
   Raw8<T> yr[NC], dr[NC], fr[NC], gr[NC];
@@ -268,25 +278,28 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
   const bool element = b.gate_kind == Gate::Element, token = b.gate_kind == Gate::Token;
   const void* const gates = element ? p.gate : nullptr;
   auto load_y = [&](int row) {
-    const RowBuffer<T> y(p.y, row, b.H, row < b.T && p.dh);
-    const RowBuffer<DH> h(p.dh, row, b.H, row < b.T);
+    const RowBuffer<T> y(p.dh ? p.y : nullptr, row, me.rows(row, b.T), b.H);
+    const RowBuffer<DH> h(p.dh, row, me.rows(row, b.T), b.H);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      yr[i] = y.load(col[i]);
-      hr[i] = h.load(col[i]);
+      yr[i] = y.load(me.at[i]);
+      hr[i] = h.load(me.at[i]);
     }
   };
   auto load_row = [&](Raw8<T>(&r)[NC], const void* base, int row) {
-    const RowBuffer<T> rb(base, row, b.H, row < b.T);
+    const RowBuffer<T> rb(base, row, me.rows(row, b.T), b.H);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) r[i] = rb.load(col[i]);
+    for (int i = 0; i < NC; ++i) r[i] = rb.load(me.at[i]);
   };
-  load_y(walker);
-  if constexpr (RES) load_row(fr, p.f, walker);
-  load_row(dr, p.dy, walker);
-  if constexpr (RES) load_row(gr, gates, walker);
-  for (int row = walker; row < b.T; row += walkers) {
-    const int next = row + walkers;   // (T and the walkers are far below 2^30)
+  load_y(me.row0);
+  if constexpr (RES) load_row(fr, p.f, me.row0);
+  load_row(dr, p.dy, me.row0);
+  if constexpr (RES) load_row(gr, gates, me.row0);
+  lw_next.fill(p.w_next, b.w_t, b.H);
+  if constexpr (RES) lw.fill(p.w, b.w_t, b.H);
+  __syncthreads();
+  for (int row0 = me.row0; row0 < b.T; row0 += step) {
+    const int next = row0 + step, rows = me.rows(row0, b.T);   // (T and the step are far below 2^30)
     // sum y^2, sum (dh w_next) y, sum f^2
     float s[3] = {0.f, 0.f, 0.f};
     float d[NC][8];   // d, the gradient reaching y
@@ -295,7 +308,7 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
       float y[8], h[8], w[8], f[8];
       unpack8<T>(yr[i], y);
       unpack8<DH>(hr[i], h);
-      lw_next.get(lane + i * TPR, w);
+      lw_next.get(me.group(i), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         d[i][e] = h[e] * w[e];
@@ -348,14 +361,14 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
     }
     load_y(next);
     {
-      const RowBuffer<T> xo(p.dx, row, b.H, true);
+      const RowBuffer<T> xo(p.dx, row0, rows, b.H);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         float dy[8];
         unpack8<T>(dr[i], dy);
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[i][e] += dy[e];
-        xo.store(col[i], pack8<T>(d[i]));
+        xo.store(me.at[i], pack8<T>(d[i]));
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -363,14 +376,15 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
     if constexpr (RES) {
       const float rf = b.norm ? row_inv_rms<TPR, T, NC>(fr, s[2], b.H, b.eps, sum) : 1.f;
       GateValue gt = {1.f, 1.f};   // the row's gate
-      if (token) gt = gate_value(((const float*)p.gate)[row], b.sigmoid);
+      const int row = row0 + me.sub;
+      if (token) gt = gate_value(row < b.T ? ((const float*)p.gate)[row] : 0.f, b.sigmoid);
       // sum d a w n(f): the mean in the norm's gradient and, with a = 1, the token gate's gradient
       float q[1] = {0.f};
-      const RowBuffer<T> go(p.dgate, row, b.H, element);
+      const RowBuffer<T> go(element ? p.dgate : nullptr, row0, rows, b.H);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         float w[8], f[8];
-        lw.get(lane + i * TPR, w);
+        lw.get(me.group(i), w);
         forget(fr[i]);
         unpack8<T>(fr[i], f);
         if (element) {
@@ -385,7 +399,7 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
             d[i][e] = dz * w[e];
             q[0] = fmaf(d[i][e], n, q[0]);
           }
-          go.store(col[i], pack8<T>(o));
+          go.store(me.at[i], pack8<T>(o));
         } else {
           // (the sum is of the values without the token's gate, whose own gradient needs it so)
 #pragma unroll
@@ -401,10 +415,10 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
       }
       load_row(gr, gates, next);
       if (b.norm || token) sum(q);
-      if (token && lane == 0 && p.dgate)
+      if (token && me.lane == 0 && row < b.T && p.dgate)
         ((float*)p.dgate)[row] = q[0] * gt.rest * (b.sigmoid ? gt.a : 1.f);
       const float m = b.norm ? q[0] * gt.a * inv_h : 0.f;   // (gt.a is 1 but for a token's gate)
-      const RowBuffer<T> fo(p.df, row, b.H, true);
+      const RowBuffer<T> fo(p.df, row0, rows, b.H);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         float f[8], o[8];
@@ -413,37 +427,45 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           o[e] = b.norm ? rf * fmaf(-f[e] * rf, m, d[i][e]) : d[i][e];
-        fo.store(col[i], pack8<T>(o));
+        fo.store(me.at[i], pack8<T>(o));
         __builtin_amdgcn_sched_barrier(0);
       }
       load_row(fr, p.f, next);
     }
   }
-  const int64_t mine = (int64_t)blockIdx.x * b.H;
-  if constexpr (TPR == 64) {   // the workgroup's four walkers, one after another
+  if constexpr (TPR < 64) {   // the wave's rows
+#pragma unroll
+    for (int o = TPR; o < 64; o *= 2)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sn[0][e] += __shfl_xor(sn[0][e], o);
+        if constexpr (RES) sw[0][e] += __shfl_xor(sw[0][e], o);
+      }
+  }
+  if constexpr (TPR <= 64) {   // the workgroup's waves, one after another
     const int wave = threadIdx.x >> 6;
     for (int q = 0; q < 4; ++q) {
       __syncthreads();
-      if (wave != q) continue;
+      if (wave != q || me.sub) continue;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         if (q) {
-          lw_next.add(lane + i * TPR, sn[i]);
-          if constexpr (RES) lw.add(lane + i * TPR, sw[i]);
+          lw_next.add(me.group(i), sn[i]);
+          if constexpr (RES) lw.add(me.group(i), sw[i]);
         }
         if (q < 3) {
-          lw_next.put(lane + i * TPR, sn[i]);
-          if constexpr (RES) lw.put(lane + i * TPR, sw[i]);
+          lw_next.put(me.group(i), sn[i]);
+          if constexpr (RES) lw.put(me.group(i), sw[i]);
         }
       }
     }
-    if (wave != 3) return;
+    if (wave != 3 || me.sub) return;
   }
+  const RowBuffer<Elt::F32> pw(part_w, blockIdx.x, 1, b.H), pn(part_n, blockIdx.x, 1, b.H);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    if (!ok[i]) continue;
-    if (part_w) store8<Elt::F32>(part_w, mine + col[i], pack8<Elt::F32>(sw[i]));
-    if (part_n) store8<Elt::F32>(part_n, mine + col[i], pack8<Elt::F32>(sn[i]));
+    if (RES) pw.store(me.at[i], pack8<Elt::F32>(sw[i]));
+    pn.store(me.at[i], pack8<Elt::F32>(sn[i]));
   }
 }
 
@@ -486,7 +508,10 @@ template <typename Fn>
 void with_forward_shape(int H, Fn&& fn) {
   const int g = (H + 7) / 8;
 #define MOE_SHAPE(TPR, NC) fn(std::integral_constant<int, TPR>(), std::integral_constant<int, NC>())
-  if (g <= 64) MOE_SHAPE(64, 1);
+  if (g <= 8) MOE_SHAPE(8, 1);
+  else if (g <= 16) MOE_SHAPE(16, 1);
+  else if (g <= 32) MOE_SHAPE(32, 1);
+  else if (g <= 64) MOE_SHAPE(64, 1);
   else if (g <= 128) MOE_SHAPE(64, 2);
   else if (g <= 192) MOE_SHAPE(64, 3);
   else if (g <= 256) MOE_SHAPE(64, 4);
@@ -500,7 +525,10 @@ void with_forward_shape(int H, Fn&& fn) {
 template <typename Fn>
 void with_backward_shape(int H, Fn&& fn) {
   const int g = (H + 7) / 8;
-  if (g <= 64) MOE_SHAPE(64, 1);
+  if (g <= 8) MOE_SHAPE(8, 1);
+  else if (g <= 16) MOE_SHAPE(16, 1);
+  else if (g <= 32) MOE_SHAPE(32, 1);
+  else if (g <= 64) MOE_SHAPE(64, 1);
   else if (g <= 128) MOE_SHAPE(64, 2);
   else if (g <= 256) MOE_SHAPE(128, 2);
   else if (g <= 384) MOE_SHAPE(192, 2);

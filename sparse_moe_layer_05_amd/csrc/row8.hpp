@@ -42,16 +42,19 @@ __device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
   }
 }
 
-// One row as a buffer of its own: columns past its end, and every column of an absent row, load as
-// zeros and store nothing, so that lanes need no branch.
+// Some rows of n elements as a buffer of their own: elements past their end, and every element of
+// absent rows, load as zeros and store nothing, so that lanes need no branch.
+constexpr uint32_t kAway = 1u << 29;   // an element past the end of any buffer
 template <Elt T>
 struct RowBuffer {
   static constexpr uint32_t kElt = T == Elt::BF16 ? 2 : 4;
   typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
   __amdgpu_buffer_rsrc_t r;
-  __device__ __forceinline__ RowBuffer(const void* base, int64_t row, int n, bool present)
+  // rows [row, row + rows); none if rows <= 0 or base is nullptr
+  __device__ __forceinline__ RowBuffer(const void* base, int64_t row, int rows, int n)
       : r(__builtin_amdgcn_make_buffer_rsrc((char*)base + row * n * kElt, (short)0,
-                                            present && base ? (int)(n * kElt) : 0, 0x00020000)) {}
+                                            base && rows > 0 ? (int)(rows * n * kElt) : 0,
+                                            0x00020000)) {}
   __device__ __forceinline__ Raw8<T> load(uint32_t col) const {
     Raw8<T> out;
     if constexpr (T == Elt::BF16) {
@@ -120,6 +123,19 @@ __device__ __forceinline__ float row16_sum(float v) {
   v = dpp_add<0x114, 0xF>(v);
   v = dpp_add<0x118, 0xF>(v);
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 15));
+}
+// Sum over aligned groups of 8, 16 or 32 lanes, in every lane: lane i meets i ^ 1, i ^ 2, then 7 - i
+// and 15 - i of its eight and sixteen, whose sums are those of the other half.
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+  static_assert(LANES == 8 || LANES == 16 || LANES == 32);
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));
+  if constexpr (LANES >= 16)
+    v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));
+  if constexpr (LANES == 32) v += __shfl_xor(v, 16);
+  return v;
 }
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll

@@ -36,7 +36,8 @@ def gate_input(g, kind, T, H, dtype):
 
 SHAPES = [(1, 2688), (3, 16), (65, 48), (7, 512), (5, 520 + 8), (4, 1040), (3, 1552), (2, 2048),
           (3, 2064), (2, 3088), (5, 4096), (2, 4112), (3, 6160), (2, 8192), (1, 8208), (2, 12304),
-          (3, 16384), (1100, 288)]
+          (3, 16384), (1100, 288), (37, 64), (19, 80), (9, 128), (21, 144), (70, 256), (5, 272),
+          (40000, 16)]
 KINDS = [(None, "none"), ("token", "sigmoid"), ("token", "none"), ("element", "sigmoid"),
          ("element", "none")]
 
