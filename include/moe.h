@@ -414,8 +414,8 @@ int32_t moe_block_residual_backward(const void *dy, const void *f, const void *w
  * A norm that is not finite thus leaves the gradients as they are: the caller reads it and skips the
  * step. In place (out NULL or grad for every tensor) nothing is written where coef is 1.
  * Tensors are contiguous runs of n elements (MOE_F32 or MOE_BF16), aligned to their element; n may
- * be 0; at most 65536 of them. Outputs must overlap neither each other nor another tensor's grad.
- * moe_clip_plan writes their table into `plan` (device, moe_clip_plan_size bytes, 16-byte aligned)
+ * be 0; at most 65536 of them, 16 TB in all. Outputs must overlap neither each other nor another tensor's grad.
+ * moe_clip_plan writes their table into `plan` (device, moe_clip_plan_size bytes, 32-byte aligned)
  * by kernels on `stream` and fills `clip` (host). moe_clip_grads, on that stream or ordered behind
  * it, may then be called any number of times while the tensors and the plan stay in place; calls
  * that share a plan must not overlap. It reads `plan` for scratch too. Errors: MOE_ERR_INVALID_ARG
@@ -430,8 +430,8 @@ typedef struct {
 typedef struct {     /* filled by moe_clip_plan */
   void *plan;
   int64_t chunks;
-  int32_t entries;
   int32_t in_place;
+  int32_t reserved;
 } moe_clip_t;
 int32_t moe_clip_plan_size(const moe_clip_tensor_t *tensors, int32_t count, size_t *bytes);
 int32_t moe_clip_plan(const moe_clip_tensor_t *tensors, int32_t count, void *plan,

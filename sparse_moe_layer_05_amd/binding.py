@@ -69,8 +69,8 @@ class MoeClipTensor(C.Structure):
 
 
 class MoeClip(C.Structure):
-    _fields_ = [("plan", C.c_void_p), ("chunks", C.c_int64), ("entries", C.c_int32),
-                ("in_place", C.c_int32)]
+    _fields_ = [("plan", C.c_void_p), ("chunks", C.c_int64), ("in_place", C.c_int32),
+                ("reserved", C.c_int32)]
 
 
 class MoeError(RuntimeError):

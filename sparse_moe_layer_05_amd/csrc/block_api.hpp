@@ -7,6 +7,7 @@ namespace {
 
 bool float_type(moe_dtype_t t) { return t == MOE_F32 || t == MOE_BF16; }
 Elt elt_of(moe_dtype_t t) { return t == MOE_F32 ? Elt::F32 : Elt::BF16; }
+bool aligned32(const void* p) { return ((uintptr_t)p & 31u) == 0; }
 bool absent_or_aligned(const void* p) { return !p || aligned16(p); }
 
 // ---- token rows
@@ -77,24 +78,23 @@ int32_t block_workspace(const BlockShape& b, bool sums, const void* ws, size_t w
 
 // ---- clipping
 constexpr int kClipMaxTensors = 1 << 16;
+constexpr int64_t kClipMaxChunks = (int64_t)1 << 30;            // 16 TB
 constexpr size_t kClipPartial = kClipGroups * sizeof(double);   // at the start of the plan
 
-int32_t clip_check(const moe_clip_tensor_t* t, int32_t count, int64_t* chunks, int32_t* entries) {
+int32_t clip_check(const moe_clip_tensor_t* t, int32_t count, int64_t* chunks) {
   if (count < 0 || count > kClipMaxTensors || (count && !t)) return MOE_ERR_INVALID_ARG;
   int64_t c = 0;
-  int32_t used = 0;
   for (int32_t i = 0; i < count; ++i) {
-    if (t[i].n < 0 || t[i].n > (int64_t)1 << 48) return MOE_ERR_INVALID_ARG;
+    if (t[i].n < 0 || t[i].n > (int64_t)1 << 43) return MOE_ERR_INVALID_ARG;
     if (!float_type(t[i].dt)) return MOE_ERR_UNSUPPORTED;
     if (t[i].n == 0) continue;
     const uintptr_t mask = t[i].dt == MOE_BF16 ? 1 : 3;
     if (!t[i].grad || ((uintptr_t)t[i].grad & mask) || ((uintptr_t)t[i].out & mask))
       return MOE_ERR_INVALID_ARG;
-    c += clip_chunks(t[i].n, elt_of(t[i].dt));
-    ++used;
+    c += clip_chunks(t[i].n, t[i].dt == MOE_BF16);
+    if (c > kClipMaxChunks) return MOE_ERR_INVALID_ARG;
   }
   *chunks = c;
-  *entries = used;
   return MOE_OK;
 }
 
@@ -266,56 +266,55 @@ int32_t moe_block_residual_backward(const void* dy, const void* f, const void* w
 
 int32_t moe_clip_plan_size(const moe_clip_tensor_t* tensors, int32_t count, size_t* bytes) {
   int64_t chunks = 0;
-  int32_t entries = 0;
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  const int32_t rc = clip_check(tensors, count, &chunks, &entries);
-  if (rc == MOE_OK) *bytes = kClipPartial + (size_t)entries * sizeof(ClipTensor);
+  const int32_t rc = clip_check(tensors, count, &chunks);
+  if (rc == MOE_OK) *bytes = kClipPartial + (size_t)chunks * sizeof(ClipChunk);
   return rc;
 }
 
 int32_t moe_clip_plan(const moe_clip_tensor_t* tensors, int32_t count, void* plan,
                       size_t plan_bytes, moe_clip_t* clip, void* stream) {
   int64_t chunks = 0;
-  int32_t entries = 0;
-  const int32_t rc = clip_check(tensors, count, &chunks, &entries);
+  const int32_t rc = clip_check(tensors, count, &chunks);
   if (rc) return rc;
   if (!clip) return MOE_ERR_INVALID_ARG;
-  if (!plan || !aligned16(plan) || plan_bytes < kClipPartial + (size_t)entries * sizeof(ClipTensor))
+  if (!plan || !aligned32(plan) || plan_bytes < kClipPartial + (size_t)chunks * sizeof(ClipChunk))
     return MOE_ERR_WORKSPACE;
-  ClipTensor* table = (ClipTensor*)((char*)plan + kClipPartial);
+  ClipChunk* table = (ClipChunk*)((char*)plan + kClipPartial);
   ClipBatch batch;
   memset(&batch, 0, sizeof(batch));
   int32_t in_place = 1;
-  int at = 0, held = 0;
+  int held = 0;
   int64_t first = 0;
   for (int32_t i = 0; i < count; ++i) {
     const moe_clip_tensor_t& t = tensors[i];
     if (t.n == 0) continue;
     void* out = t.out ? t.out : t.grad;
     if (out != t.grad) in_place = 0;
-    batch.t[held++] = {t.grad, out, t.n, first | (t.dt == MOE_BF16 ? kClipBf16 : 0)};
-    first += clip_chunks(t.n, elt_of(t.dt));
+    const bool bf16 = t.dt == MOE_BF16;
+    batch.t[held++] = {(const char*)t.grad, (char*)out, t.n, first, bf16};
+    first += clip_chunks(t.n, bf16);
     if (held == kClipPerLaunch) {
-      MOE_TRY(launch_clip_table(batch, held, table, at, (hipStream_t)stream));
-      at += held;
+      MOE_TRY(launch_clip_table(batch, held, first - batch.t[0].first, table, (hipStream_t)stream));
       held = 0;
     }
   }
-  if (held) MOE_TRY(launch_clip_table(batch, held, table, at, (hipStream_t)stream));
+  if (held)
+    MOE_TRY(launch_clip_table(batch, held, first - batch.t[0].first, table, (hipStream_t)stream));
   clip->plan = plan;
   clip->chunks = chunks;
-  clip->entries = entries;
   clip->in_place = in_place;
+  clip->reserved = 0;
   return MOE_OK;
 }
 
 int32_t moe_clip_grads(const moe_clip_t* clip, float max_norm, float* norm, void* stream) {
-  if (!clip || !clip->plan || !aligned16(clip->plan) || clip->entries < 0 || clip->chunks < 0 ||
-      !norm || !(max_norm >= 0.f))
+  if (!clip || !clip->plan || !aligned32(clip->plan) || clip->chunks < 0 ||
+      clip->chunks > kClipMaxChunks || !norm || ((uintptr_t)norm & 3) || !(max_norm >= 0.f))
     return MOE_ERR_INVALID_ARG;
-  return hip_status(launch_clip((const ClipTensor*)((const char*)clip->plan + kClipPartial),
-                                clip->entries, clip->chunks, clip->in_place != 0, max_norm,
-                                (double*)clip->plan, norm, (hipStream_t)stream));
+  return hip_status(launch_clip((const ClipChunk*)((const char*)clip->plan + kClipPartial),
+                                clip->chunks, clip->in_place != 0, max_norm, (double*)clip->plan,
+                                norm, (hipStream_t)stream));
 }
 
 }  // extern "C"

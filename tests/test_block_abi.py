@@ -156,6 +156,7 @@ def table(*rows):
     ([(None, None, 0, 0)], 1, OK), ([(None, None, 5, 0)], 1, BAD), ([(0x1002, None, 5, 0)], 1, BAD),
     ([(0x1001, None, 5, 1)], 1, BAD), ([(0x1000, 0x2002, 5, 0)], 1, BAD),
     ([(0x1000, None, -1, 0)], 1, BAD), ([(0x1000, None, 1 << 49, 0)], 1, BAD),
+    ([(0x1000, None, 1 << 43, 0)], 1, BAD),
     ([(0x1000, None, 5, 2)], 1, UNS), ([(0x1000, None, 5, 0)], -1, BAD),
     ([(0x1000, None, 5, 0)], 65537, BAD),
 ])
@@ -173,7 +174,7 @@ def test_clip_plan_argument_errors(rows, count, code):
     assert L.moe_clip_plan(table(*rows), count, FAKE, BIG, None, None) == BAD
     if not any(r[2] for r in rows):      # nothing to write: no launch
         assert L.moe_clip_plan(table(*rows), count, FAKE, n.value, C.byref(clip), None) == OK
-        assert clip.entries == 0 and clip.chunks == 0
+        assert clip.chunks == 0
 
 
 def test_clip_argument_errors():
@@ -186,6 +187,7 @@ def test_clip_argument_errors():
     for bad in (-1.0, NAN):
         assert L.moe_clip_grads(C.byref(clip), bad, FAKE, None) == BAD
     assert L.moe_clip_grads(C.byref(clip), 1.0, None, None) == BAD
+    assert L.moe_clip_grads(C.byref(clip), 1.0, C.c_void_p(0x10002), None) == BAD
     assert L.moe_clip_grads(None, 1.0, FAKE, None) == BAD
     clip.plan = ODD.value
     assert L.moe_clip_grads(C.byref(clip), 1.0, FAKE, None) == BAD
