@@ -332,13 +332,14 @@ int32_t moe_mx_gemm(const void *A, const uint8_t *a_scales, moe_dtype_t a_fmt, c
  * expert of another rank, so k > E is allowed here) or repeats an expert of its token, and where pos
  * is outside [0, n_rows): nothing is read or written for it, and its weight's gradient is 0. Rows
  * behind the last pair are left as they were. weights [T, k] fp32, or NULL for 1; they may be any
- * values. Sums run in fp32 in slot order and are rounded once; all results are deterministic.
+ * values. Sums run in fp32 in a fixed order and are rounded once; all results are deterministic.
  * D a multiple of 16 up to 2^20, k <= 64, T * ceil(D / 512) <= 2^25, T * k < 2^31. dt, dx_dt, y_dt,
  * dy_dt: MOE_BF16 or MOE_F32. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
  * MOE_ERR_UNSUPPORTED (types), MOE_ERR_WORKSPACE. */
 
 /* rows[pos[t, j]] = weights[t, j] * x[t], rows [T * k, D] and x [T, D] of type dt; also offsets
- * [E + 1] and pos [T, k], as moe_dispatch makes them (T == 0 writes the offsets alone). */
+ * [E + 1] and pos [T, k], as moe_dispatch makes them (T == 0 writes the offsets alone). Few pairs
+ * need no workspace: the size is then 0 and ws may be NULL. */
 int32_t moe_sort_tokens_workspace_size(int32_t T, int32_t E, int32_t k, size_t *bytes);
 int32_t moe_sort_tokens(const void *x, moe_dtype_t dt, const int32_t *idx, const float *weights,
                         int32_t T, int32_t D, int32_t E, int32_t k, void *rows, int32_t *offsets,

@@ -63,7 +63,7 @@ def sort_tokens(x, idx, E, *, weights=None, out=None, stream=None):
     offsets = idx.new_empty(E + 1)
     pos = idx.new_empty((T, k))
     n = _sort_workspace(T, E, k)
-    ws = x.new_empty(n, dtype=torch.uint8)
+    ws = x.new_empty(n, dtype=torch.uint8) if n else None
     _launch(lib().moe_sort_tokens, "moe_sort_tokens", dev, stream, _p(x), dt, _p(idx), _p(weights),
             T, D, E, k, _p(rows), _p(offsets), _p(pos), _p(ws), n)
     _used_on(stream, offsets, pos, ws, *made)

@@ -34,6 +34,10 @@ struct SortPlan {
 int32_t make_sort_plan(int32_t T, int32_t E, int32_t k, SortPlan* out) {
   if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || (int64_t)T * k > INT32_MAX)
     return MOE_ERR_INVALID_ARG;
+  if (sort_is_small(T, k)) {   // one launch, no workspace
+    *out = SortPlan();
+    return MOE_OK;
+  }
   size_t off = 0;
   auto take = [&](size_t ints) {
     const size_t at = off;
@@ -121,8 +125,10 @@ int32_t moe_sort_tokens(const void* x, moe_dtype_t dt, const int32_t* idx, const
   if (!offsets || (T && (!x || !idx || !rows || !pos)) || !absent_or_aligned(x) ||
       !absent_or_aligned(rows))
     return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < pl.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
+  if (pl.total == 0)
+    return hip_status(launch_sort_small(idx, weights, T, D, E, k, elt_of(dt), x, rows, offsets, pos, s));
+  if (!ws || ws_bytes < pl.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   char* base = (char*)ws;
   MOE_TRY(launch_dispatch(idx, T, E, k, (int32_t*)(base + pl.counts), offsets,
                           (int32_t*)(base + pl.perm), pos, (int32_t*)(base + pl.scratch), 0, nullptr,

@@ -30,6 +30,7 @@ struct BlockShape {
 struct BlockForward {
   const void *x = nullptr, *f = nullptr, *w = nullptr, *gate = nullptr, *w_next = nullptr;
   void *y = nullptr, *h = nullptr;
+  bool stream = false;   // set by the launcher: operands are read past the caches
 };
 hipError_t launch_block_forward(const BlockShape& b, const BlockForward& p, hipStream_t s);
 
@@ -43,6 +44,7 @@ struct BlockBackward {
   void *dx = nullptr, *df = nullptr, *dgate = nullptr;
   float *dw = nullptr, *dw_next = nullptr;
   float* part = nullptr;
+  bool stream = false;   // as above
 };
 hipError_t launch_block_backward(const BlockShape& b, const BlockBackward& p, hipStream_t s);
 // fp32 partial sums of dw and dw_next.

@@ -55,22 +55,39 @@ struct RowBuffer {
       : r(__builtin_amdgcn_make_buffer_rsrc((char*)base + row * n * kElt, (short)0,
                                             base && rows > 0 ? (int)(rows * n * kElt) : 0,
                                             0x00020000)) {}
+  // LAST: the lines are marked as the first to leave the caches
+  template <bool LAST = false>
   __device__ __forceinline__ Raw8<T> load(uint32_t col) const {
+    constexpr int kAux = LAST ? 2 : 0;
     Raw8<T> out;
     if constexpr (T == Elt::BF16) {
-      out.q = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt, 0, 0));
+      out.q = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt, 0, kAux));
     } else {
-      out.a = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt, 0, 0));
-      out.b = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt + 16, 0, 0));
+      out.a = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt, 0, kAux));
+      out.b = __builtin_bit_cast(float4,
+                                 __builtin_amdgcn_raw_buffer_load_b128(r, col * kElt + 16, 0, kAux));
     }
     return out;
   }
-  __device__ __forceinline__ void store(uint32_t col, const Raw8<T>& v) const {
-    if constexpr (T == Elt::BF16) {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.q), r, col * kElt, 0, 0);
+  template <int N>
+  __device__ __forceinline__ void load(const uint32_t (&col)[N], Raw8<T> (&out)[N], bool last) const {
+    if (last) {   // the same in every lane
+#pragma unroll
+      for (int i = 0; i < N; ++i) out[i] = load<true>(col[i]);
     } else {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.a), r, col * kElt, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.b), r, col * kElt + 16, 0, 0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) out[i] = load<false>(col[i]);
+    }
+  }
+  template <bool LAST = false>
+  __device__ __forceinline__ void store(uint32_t col, const Raw8<T>& v) const {
+    constexpr int kAux = LAST ? 2 : 0;
+    if constexpr (T == Elt::BF16) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.q), r, col * kElt, 0, kAux);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.a), r, col * kElt, 0, kAux);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v.b), r, col * kElt + 16, 0,
+                                             kAux);
     }
   }
 };

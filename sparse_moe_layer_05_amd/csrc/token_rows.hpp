@@ -19,16 +19,27 @@ struct TokenRows {
 // out[pos[t, j]] = weights[t, j] * in[t], both of type t.
 hipError_t launch_spread_rows(const TokenRows& p, Elt t, const void* in, void* out, hipStream_t s);
 
-// out[t] = add[t] + sum_j weights[t, j] * in[pos[t, j]] in j order, rounded once (add, of out's
-// type, may be nullptr). With dot: dweights[t, j] = <other[t], in[pos[t, j]]>, other of in's type
-// (0 for dropped pairs).
-hipError_t launch_gather_rows(const TokenRows& p, Elt in_t, const void* in, const void* add,
-                              Elt out_t, void* out, const void* other, float* dweights,
-                              hipStream_t s);
+// Positions, offsets and the spread of few pairs in one launch (E <= 1024). Every workgroup looks at
+// all pairs for each of its token's slots, so the limit is on pairs times slots as well. Microseconds,
+// one launch / the dispatch and a spread: 64 tokens, 6 slots (2304) 6.4 / 8.8; 1000, 2 (4000) 9.2 / 12.1;
+// 256, 6 (9216) 11.5 / 11.0; 64, 24 (36864) 19.6 / 12.6.
+constexpr int kSortSmallPairs = 2048, kSortSmallWork = 8192;
+inline bool sort_is_small(int64_t T, int k) {
+  return T * k <= kSortSmallPairs && T * k * k <= kSortSmallWork;
+}
+hipError_t launch_sort_small(const int32_t* idx, const float* weights, int T, int D, int E, int k,
+                             Elt t, const void* in, void* out, int32_t* offsets, int32_t* pos,
+                             hipStream_t s);
 
-// out[pos[t, j]] = weights[t, j] * in[t] and dweights[t, j] = <in[t], rows[pos[t, j]]>; rows and
-// out of type rows_t (out may be rows).
-hipError_t launch_spread_dot(const TokenRows& p, Elt in_t, const void* in, Elt rows_t,
+// out[t] = add[t] + sum_j weights[t, j] * rows[pos[t, j]], rounded once (add, of out's type, may be
+// nullptr). With dweights: dweights[t, j] = <a[t], rows[pos[t, j]]>, a of the rows' type (0 for dropped
+// pairs).
+hipError_t launch_gather_rows(const TokenRows& p, Elt rows_t, const void* rows, const void* add,
+                              Elt out_t, void* out, const void* a, float* dweights, hipStream_t s);
+
+// out[pos[t, j]] = weights[t, j] * a[t] and dweights[t, j] = <a[t], rows[pos[t, j]]>; rows and out of
+// type rows_t (out may be rows).
+hipError_t launch_spread_dot(const TokenRows& p, Elt a_t, const void* a, Elt rows_t,
                              const void* rows, void* out, float* dweights, hipStream_t s);
 
 }  // namespace moe

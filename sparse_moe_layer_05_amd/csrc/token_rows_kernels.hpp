@@ -5,7 +5,7 @@
 //   dots        dw[t, j] = <a[t], b[pos[t, j]]>                (gradient of the weights, with either)
 //
 // All are bound by HBM: a token's row is read or written once, its k rows once each. A wave takes
-// 512 columns of one token, eight elements a lane, and walks the token's k rows.
+// 512 columns of one token, eight elements a lane, and walks the token's k rows, eight in flight.
 // Included once, by routing.hip.
 #pragma once
 
@@ -13,14 +13,17 @@
 #include "row8.hpp"
 #include "token_rows.hpp"
 
+#include <algorithm>
+
 namespace moe {
 namespace {
 namespace token_rows {
 
 constexpr int kSeg = 8 * kWave;   // columns of a wave
-constexpr int kBatch = 8;         // rows in flight
+constexpr int kMostBatch = 8;     // rows in flight
 
-// A token's k positions and weights, one a lane; position -1 where the pair is dropped.
+// A token's k positions and weights, one a lane; -1 and 0 where the pair is dropped (its row is then
+// a buffer of no size: it loads as zeros and stores nothing).
 struct Pairs {
   int pos;
   float w;
@@ -30,8 +33,8 @@ __device__ __forceinline__ Pairs load_pairs(const TokenRows& p, int t, int lane)
   if (lane < p.k) {
     const int64_t i = (int64_t)t * p.k + lane;
     const int r = p.pos[i];
-    q.pos = (unsigned)r < (unsigned)p.n_rows ? r : -1;
-    q.w = p.weights ? p.weights[i] : 1.f;
+    const float w = p.weights ? p.weights[i] : 1.f;
+    if ((unsigned)r < (unsigned)p.n_rows) q = {r, w};
   }
   return q;
 }
@@ -42,138 +45,306 @@ __device__ __forceinline__ float weight_of(const Pairs& q, int j) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(q.w), j));
 }
 
-template <Elt T, bool WEIGHTED>
-__global__ __launch_bounds__(256) void spread_kernel(TokenRows p, const void* __restrict__ in,
-                                                     void* __restrict__ out) {
-  const int lane = threadIdx.x & 63;
-  const int nseg = (p.D + kSeg - 1) / kSeg;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int t = (int)(unit / nseg);
-  if (t >= p.T) return;
-  const int c = (int)(unit - (int64_t)t * nseg) * kSeg + lane * 8;
-  const Pairs pr = load_pairs(p, t, lane);
-  const bool in_row = c < p.D;
-  Raw8<T> r = zero8<T>();
-  if (in_row) r = load8<T>(in, (int64_t)t * p.D + c);
+// A wave's unit: 512 columns of one token.
+struct Unit {
+  int t, lane;
+  uint32_t col;   // the lane's first column; past the row's end for the last lanes
+  __device__ __forceinline__ Unit(const TokenRows& p, int64_t unit) {
+    const int nseg = (p.D + kSeg - 1) / kSeg;
+    lane = threadIdx.x & 63;
+    t = (int)(unit / nseg);
+    col = (uint32_t)(unit - (int64_t)t * nseg) * kSeg + lane * 8;
+  }
+};
+__device__ __forceinline__ int64_t unit_of_wave() {
+  return (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+template <Elt T, bool WEIGHTED, bool STREAM>
+__global__ __launch_bounds__(256) void spread_kernel(TokenRows p, const void* in, void* out) {
+  const Unit u(p, unit_of_wave());
+  if (u.t >= p.T) return;
+  const Pairs pr = load_pairs(p, u.t, u.lane);
+  Raw8<T> r = RowBuffer<T>(in, u.t, 1, p.D).load(u.col);
   float v[8];
   if constexpr (WEIGHTED) unpack8<T>(r, v);
   for (int j = 0; j < p.k; ++j) {
     const int row = pos_of(pr, j);
-    if (row < 0) continue;
     if constexpr (WEIGHTED) {
       const float w = weight_of(pr, j);
-      float u[8];
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = w * v[i];
-      r = pack8<T>(u);
+      for (int i = 0; i < 8; ++i) x[i] = w * v[i];
+      r = pack8<T>(x);
     }
-    if (in_row) store8<T>(out, (int64_t)row * p.D + c, r);
+    RowBuffer<T>(out, row, row >= 0, p.D).template store<STREAM>(u.col, r);
   }
 }
 
-template <Elt IN, Elt OUT>
-__global__ __launch_bounds__(256) void gather_kernel(TokenRows p, const void* __restrict__ in,
-                                                     const void* add, void* out) {
+// The rows of the pairs [j0, j0 + B), and acc += their weights times them.
+template <Elt ROWS, int B, bool STREAM>
+__device__ __forceinline__ void load_batch(const TokenRows& p, const Pairs& pr, const void* rows,
+                                           int j0, uint32_t col, Raw8<ROWS> (&r)[B]) {
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const int row = pos_of(pr, j0 + b);   // (j0 + b < 64; lanes past k hold -1 and 0)
+    r[b] = RowBuffer<ROWS>(rows, row, row >= 0, p.D).template load<STREAM>(col);
+  }
+}
+template <Elt ROWS, int B>
+__device__ __forceinline__ void add_rows(const Pairs& pr, int j0, const Raw8<ROWS> (&r)[B],
+                                         float (&acc)[8]) {
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const float w = weight_of(pr, j0 + b);
+    float v[8];
+    unpack8<ROWS>(r[b], v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+  }
+}
+
+template <Elt IN, Elt OUT, int B, bool STREAM>
+__global__ __launch_bounds__(256) void gather_kernel(TokenRows p, const void* in, const void* add,
+                                                     void* out) {
+  const Unit u(p, unit_of_wave());
+  if (u.t >= p.T) return;
+  const Pairs pr = load_pairs(p, u.t, u.lane);
+  float acc[8];
+  unpack8<OUT>(RowBuffer<OUT>(add, u.t, 1, p.D).load(u.col), acc);
+  for (int j0 = 0; j0 < p.k; j0 += B) {
+    Raw8<IN> r[B];
+    load_batch<IN, B, STREAM>(p, pr, in, j0, u.col, r);
+    add_rows<IN, B>(pr, j0, r, acc);
+  }
+  RowBuffer<OUT>(out, u.t, 1, p.D).store(u.col, pack8<OUT>(acc));
+}
+
+// Few pairs: positions and the spread in one launch. Every workgroup finds its own token's positions
+// from all the pairs (a pair's place is the number of kept pairs of lower experts, and of its own
+// expert before it); the workgroup behind the last token counts the offsets.
+template <Elt T, bool WEIGHTED>
+__global__ __launch_bounds__(256) void sort_small_kernel(const int32_t* __restrict__ idx,
+                                                         const float* __restrict__ weights, int Tn,
+                                                         int D, int E, int k,
+                                                         const void* __restrict__ in,
+                                                         void* __restrict__ out,
+                                                         int32_t* __restrict__ offsets,
+                                                         int32_t* __restrict__ pos) {
+  __shared__ int16_t ex[kSortSmallPairs];
+  __shared__ int32_t part[4][64];
+  __shared__ int32_t hist[1024];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int P = Tn * k, t = blockIdx.x;
+  constexpr int kSlots = kSortSmallPairs / 256;
+  // the token's first columns are on their way meanwhile
+  const int first_c = (blockIdx.y * 256 + tid) * 8;
+  Raw8<T> r0 = zero8<T>();
+  if (t < Tn && first_c < D) r0 = load8<T>(in, (int64_t)t * D + first_c);
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int p = q * 256 + tid;
+    const int e = p < P ? idx[p] : -1;
+    ex[p] = (int16_t)((unsigned)e < (unsigned)E ? e : -1);
+  }
+  __syncthreads();
+  int keep[kSlots];
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int p = q * 256 + tid;
+    int e = ex[p];
+    if (p < P && e >= 0) {
+      const int first = p / k * k;
+      bool repeated = false;
+      for (int j = first; j < p; ++j) repeated |= ex[j] == e;
+      if (repeated) e = -1;
+    }
+    keep[q] = e;
+  }
+  if (t == Tn) {
+    if (blockIdx.y) return;
+    // offsets: a count per expert, then their running sum
+    for (int e = tid; e < 1024; e += 256) hist[e] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q)
+      if (keep[q] >= 0) atomicAdd(&hist[keep[q]], 1);   // whole numbers: any order
+    __syncthreads();
+    int c[4], s = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { c[i] = s; s += hist[tid * 4 + i]; }
+    int up = s;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(up, d);
+      if (lane >= d) up += o;
+    }
+    if (lane == 63) part[0][wave] = up;
+    __syncthreads();
+    int base = up - s;
+    for (int w = 0; w < wave; ++w) base += part[0][w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tid * 4 + i < E) offsets[tid * 4 + i] = base + c[i];
+    if (tid == 255) offsets[E] = base + s;
+    return;
+  }
+  // counts of this token's slots: wave by wave, then over the waves
+  for (int j = 0; j < k; ++j) {
+    const int me = t * k + j, e = ex[me];
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      if (q * 256 >= P) break;
+      const int p = q * 256 + tid, v = keep[q];
+      n += __popcll(__ballot(v >= 0 && (v < e || (v == e && p < me))));
+    }
+    if (lane == 0) part[wave][j] = n;
+  }
+  __shared__ int32_t at[64];
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {   // which of the token's pairs are kept
+    const int p = q * 256 + tid;
+    if (p >= t * k && p < t * k + k) at[p - t * k] = keep[q];
+  }
+  __syncthreads();
+  if (tid < k) {
+    const int place = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+    const int row = at[tid] >= 0 ? place : -1;
+    if (blockIdx.y == 0) pos[(int64_t)t * k + tid] = row;
+    at[tid] = row;
+  }
+  __syncthreads();
+  for (int c = first_c; c < D; c += gridDim.y * (256 * 8)) {
+    Raw8<T> r = c == first_c ? r0 : load8<T>(in, (int64_t)t * D + c);
+    float v[8];
+    if constexpr (WEIGHTED) unpack8<T>(r, v);
+    for (int j = 0; j < k; ++j) {
+      const int row = at[j];
+      if (row < 0) continue;
+      if constexpr (WEIGHTED) {
+        const float w = weights[(int64_t)t * k + j];
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = w * v[i];
+        r = pack8<T>(u);
+      }
+      store8<T>(out, (int64_t)row * D + c, r);
+    }
+  }
+}
+
+// A workgroup per token: `segs` waves share its columns (wave v takes v * 512 + n * segs * 512), and
+// `cuts` of each share its pairs (eight at a time in turn), where tokens are too few to fill the chip.
+// What the cuts of a column add up to, and the waves' shares of a dot product, are joined through
+// LDS in wave order.
+enum class Pass { Gather, GatherDot, SpreadDot };
+constexpr int kMostWaves = 16;
+// Gather, GatherDot: out[t] = add[t] + sum_j w rows[pos] (add, out: IN). SpreadDot: out[pos] = w a[t]
+// (a: IN, out: ROWS). Dots: dweights[t, j] = <a[t], rows[pos]> (a: ROWS in GatherDot).
+template <Elt IN, Elt ROWS, Pass PASS, int B, bool STREAM>
+__global__ __launch_bounds__(kMostWaves * 64) void token_kernel(TokenRows p, int segs, int cuts,
+                                                                const void* a, const void* rows,
+                                                                const void* add, void* out,
+                                                                float* dweights) {
+  constexpr bool kDot = PASS != Pass::Gather, kSpread = PASS == Pass::SpreadDot;
+  constexpr Elt AT = kSpread ? IN : ROWS;
+  __shared__ float part[kDot ? kMostWaves : 1][64];
+  extern __shared__ float4 sums[];   // [waves][2][64], where pairs are cut
   const int lane = threadIdx.x & 63;
-  const int nseg = (p.D + kSeg - 1) / kSeg;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int t = (int)(unit / nseg);
-  if (t >= p.T) return;
-  const int c = (int)(unit - (int64_t)t * nseg) * kSeg + lane * 8;
-  const Pairs pr = load_pairs(p, t, lane);
-  if (c >= p.D) return;
-  float acc[8] = {};
-  if (add) unpack8<OUT>(load8<OUT>(add, (int64_t)t * p.D + c), acc);
-  for (int j0 = 0; j0 < p.k; j0 += kBatch) {
-    Raw8<IN> r[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int row = j0 + b < p.k ? pos_of(pr, j0 + b) : -1;
-      if (row >= 0) r[b] = load8<IN>(in, (int64_t)row * p.D + c);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (j0 + b >= p.k || pos_of(pr, j0 + b) < 0) continue;
-      const float w = weight_of(pr, j0 + b);
-      float v[8];
-      unpack8<IN>(r[b], v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
-    }
-  }
-  store8<OUT>(out, (int64_t)t * p.D + c, pack8<OUT>(acc));
-}
-
-constexpr int kDotWaves = 8;   // waves of a workgroup that shares a token's dot products
-
-// A workgroup per token; wave v takes the columns v * 512 + n * waves * 512. SPREAD: writes
-// out[pos] = w a[t] (a: IN, rows and out: ROWS); else out[t] = sum_j w rows[pos] (rows and a: ROWS,
-// out: IN). Dots of a wave go through LDS and are added in wave order.
-template <Elt IN, Elt ROWS, bool SPREAD>
-__global__ __launch_bounds__(kDotWaves * 64) void dot_kernel(TokenRows p, const void* a,
-                                                             const void* rows, void* out,
-                                                             float* __restrict__ dweights) {
-  __shared__ float part[kDotWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int seg = wave % segs, cut = wave / segs;
   const int t = blockIdx.x;
   const Pairs pr = load_pairs(p, t, lane);
   float dot = 0.f;   // of pair `lane`
-  for (int c0 = wave * kSeg; c0 < p.D; c0 += waves * kSeg) {
-    const int c = c0 + lane * 8;
-    const bool in_row = c < p.D;
-    constexpr Elt AT = SPREAD ? IN : ROWS;
-    float av[8] = {}, acc[8] = {};
-    if (in_row) unpack8<AT>(load8<AT>(a, (int64_t)t * p.D + c), av);
-    for (int j0 = 0; j0 < p.k; j0 += kBatch) {
-      Raw8<ROWS> r[kBatch];
+  for (int c0 = 0; c0 < p.D; c0 += segs * kSeg) {
+    const uint32_t col = c0 + seg * kSeg + lane * 8;   // past the row's end: zeros
+    float av[8], acc[8] = {};
+    if constexpr (kDot) unpack8<AT>(RowBuffer<AT>(a, t, 1, p.D).load(col), av);
+    for (int j0 = cut * B; j0 < p.k; j0 += cuts * B) {
+      Raw8<ROWS> r[B];
+      load_batch<ROWS, B, STREAM>(p, pr, rows, j0, col, r);
+      if constexpr (!kSpread) add_rows<ROWS, B>(pr, j0, r, acc);
+      if constexpr (kDot) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int row = j0 + b < p.k ? pos_of(pr, j0 + b) : -1;
-        r[b] = zero8<ROWS>();
-        if (row >= 0 && in_row) r[b] = load8<ROWS>(rows, (int64_t)row * p.D + c);
+        for (int b = 0; b < B; ++b) {
+          float v[8], d = 0.f;
+          unpack8<ROWS>(r[b], v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d = fmaf(av[i], v[i], d);
+          d = wave_sum(d);
+          if (lane == j0 + b) dot += d;
+        }
       }
+      if constexpr (kSpread) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int row = j0 + b < p.k ? pos_of(pr, j0 + b) : -1;
-        if (row < 0) continue;
-        const float w = weight_of(pr, j0 + b);
-        float v[8], d = 0.f;
-        unpack8<ROWS>(r[b], v);
+        for (int b = 0; b < B; ++b) {
+          const int row = pos_of(pr, j0 + b);
+          const float w = weight_of(pr, j0 + b);
+          float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d = fmaf(av[i], v[i], d);
-        d = wave_sum(in_row ? d : 0.f);
-        if (lane == j0 + b) dot += d;
-        if constexpr (SPREAD) {
-          float u[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = w * av[i];
-          if (in_row) store8<ROWS>(out, (int64_t)row * p.D + c, pack8<ROWS>(u));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+          for (int i = 0; i < 8; ++i) v[i] = w * av[i];
+          RowBuffer<ROWS>(out, row, row >= 0, p.D).store(col, pack8<ROWS>(v));
         }
       }
     }
-    if constexpr (!SPREAD)
-      if (in_row) store8<IN>(out, (int64_t)t * p.D + c, pack8<IN>(acc));
+    if constexpr (!kSpread) {
+      if (cuts > 1) {
+        if (cut) {
+          sums[wave * 128 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          sums[wave * 128 + 64 + lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        }
+        __syncthreads();
+        if (cut == 0)
+          for (int q = 1; q < cuts; ++q) {
+            const int from = (seg + q * segs) * 128 + lane;
+            const float4 x = sums[from], y = sums[from + 64];
+            acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+            acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+          }
+        __syncthreads();
+      }
+      if (cut == 0) {
+        float v[8];
+        unpack8<IN>(RowBuffer<IN>(add, t, 1, p.D).load(col), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += v[i];
+        RowBuffer<IN>(out, t, 1, p.D).store(col, pack8<IN>(acc));
+      }
+    }
   }
-  part[wave][lane] = dot;
-  __syncthreads();
-  if (wave == 0 && lane < p.k) {
-    float d = 0.f;
-    for (int v = 0; v < waves; ++v) d += part[v][lane];
-    dweights[(int64_t)t * p.k + lane] = pr.pos >= 0 ? d : 0.f;
+  if constexpr (kDot) {
+    part[wave][lane] = dot;
+    __syncthreads();
+    if (wave == 0 && lane < p.k) {
+      float d = 0.f;
+      for (int v = 0; v < segs * cuts; ++v) d += part[v][lane];
+      dweights[(int64_t)t * p.k + lane] = pr.pos >= 0 ? d : 0.f;
+    }
   }
 }
 
-dim3 seg_grid(const TokenRows& p) {
-  const int64_t units = (int64_t)p.T * ((p.D + kSeg - 1) / kSeg);
-  return dim3((unsigned)((units + 3) / 4));
+int64_t units_of(const TokenRows& p) { return (int64_t)p.T * ((p.D + kSeg - 1) / kSeg); }
+dim3 seg_grid(const TokenRows& p) { return dim3((unsigned)((units_of(p) + 3) / 4)); }
+// Rows loaded together: absent ones cost their instructions, so few slots take a smaller batch
+// (16384 tokens of 2 slots, 2688 columns, eight / two together: 62 / 55 us).
+int batch_of(int k) { return k <= 2 ? 2 : k <= 4 ? 4 : k <= 6 ? 6 : kMostBatch; }
+// What together passes the last-level cache (256 MB) is read, or for the sort written, past it: sort of
+// 8192 tokens to 6 experts, 2688 columns (308 MB) 66 / 76 us, back 55 / 59. Smaller results are left to
+// the call that reads them next.
+bool past_cache(const TokenRows& p, Elt a, Elt rows, int row_passes) {
+  auto bytes = [](Elt t) { return t == Elt::BF16 ? 2 : 4; };
+  return (int64_t)p.T * p.D * (bytes(a) + (int64_t)p.k * bytes(rows) * row_passes) > (int64_t)256 << 20;
 }
-dim3 dot_block(int D) {
-  const int n = (D + kSeg - 1) / kSeg;
-  return dim3(64 * (n < kDotWaves ? n : kDotWaves));
+// Waves that fill the chip (eight a SIMD): with as many, pairs are not cut.
+constexpr int64_t kFull = 8192;
+struct Waves {
+  int segs, cuts;
+};
+Waves token_waves(const TokenRows& p) {
+  const int nseg = (p.D + kSeg - 1) / kSeg, nbatch = (p.k + batch_of(p.k) - 1) / batch_of(p.k);
+  const int segs = std::min(nseg, 8);
+  return {segs, units_of(p) >= kFull ? 1 : std::min(nbatch, kMostWaves / segs)};
 }
 
 }  // namespace token_rows
@@ -183,60 +354,104 @@ using namespace token_rows;
 
 hipError_t launch_spread_rows(const TokenRows& p, Elt t, const void* in, void* out, hipStream_t s) {
   if (p.T <= 0) return hipSuccess;
-#define MOE_SPREAD(X, W) \
-  hipLaunchKernelGGL((spread_kernel<X, W>), seg_grid(p), dim3(256), 0, s, p, in, out)
-  if (t == Elt::BF16) {
-    if (p.weights) MOE_SPREAD(Elt::BF16, true); else MOE_SPREAD(Elt::BF16, false);
+#define MOE_SPREAD(X, W, S) \
+  hipLaunchKernelGGL((spread_kernel<X, W, S>), seg_grid(p), dim3(256), 0, s, p, in, out)
+#define MOE_SPREAD_W(X, S) \
+  if (p.weights) MOE_SPREAD(X, true, S); else MOE_SPREAD(X, false, S)
+  const bool bf = t == Elt::BF16;
+  if (past_cache(p, t, t, 1)) {
+    if (bf) { MOE_SPREAD_W(Elt::BF16, true); } else { MOE_SPREAD_W(Elt::F32, true); }
   } else {
-    if (p.weights) MOE_SPREAD(Elt::F32, true); else MOE_SPREAD(Elt::F32, false);
+    if (bf) { MOE_SPREAD_W(Elt::BF16, false); } else { MOE_SPREAD_W(Elt::F32, false); }
   }
+#undef MOE_SPREAD_W
 #undef MOE_SPREAD
   return hipGetLastError();
 }
 
-hipError_t launch_gather_rows(const TokenRows& p, Elt in_t, const void* in, const void* add,
-                              Elt out_t, void* out, const void* other, float* dweights,
-                              hipStream_t s) {
-  if (p.T <= 0) return hipSuccess;
-  const bool bi = in_t == Elt::BF16, bo = out_t == Elt::BF16;
-  if (dweights) {
-#define MOE_GATHER_DOT(O, I)                                                                     \
-  hipLaunchKernelGGL((dot_kernel<O, I, false>), dim3(p.T), dot_block(p.D), 0, s, p, other, in, out, \
-                     dweights)
-    if (bi) {
-      if (bo) MOE_GATHER_DOT(Elt::BF16, Elt::BF16); else MOE_GATHER_DOT(Elt::F32, Elt::BF16);
-    } else {
-      if (bo) MOE_GATHER_DOT(Elt::BF16, Elt::F32); else MOE_GATHER_DOT(Elt::F32, Elt::F32);
-    }
-#undef MOE_GATHER_DOT
-    return hipGetLastError();
-  }
-#define MOE_GATHER(I, O) \
-  hipLaunchKernelGGL((gather_kernel<I, O>), seg_grid(p), dim3(256), 0, s, p, in, add, out)
-  if (bi) {
-    if (bo) MOE_GATHER(Elt::BF16, Elt::BF16); else MOE_GATHER(Elt::BF16, Elt::F32);
+hipError_t launch_sort_small(const int32_t* idx, const float* weights, int T, int D, int E, int k,
+                             Elt t, const void* in, void* out, int32_t* offsets, int32_t* pos,
+                             hipStream_t s) {
+  if (!sort_is_small(T, k) || E > 1024 || k > 64) return hipErrorInvalidValue;
+  const dim3 grid(T + 1, T < 512 ? (D + 2047) / 2048 : 1);   // a long row is shared by workgroups
+#define MOE_SORT(X, W)                                                                            \
+  hipLaunchKernelGGL((sort_small_kernel<X, W>), grid, dim3(256), 0, s, idx, weights, T, D, E, \
+                     k, in, out, offsets, pos)
+  if (t == Elt::BF16) {
+    if (weights) MOE_SORT(Elt::BF16, true); else MOE_SORT(Elt::BF16, false);
   } else {
-    if (bo) MOE_GATHER(Elt::F32, Elt::BF16); else MOE_GATHER(Elt::F32, Elt::F32);
+    if (weights) MOE_SORT(Elt::F32, true); else MOE_SORT(Elt::F32, false);
   }
-#undef MOE_GATHER
+#undef MOE_SORT
   return hipGetLastError();
 }
 
-hipError_t launch_spread_dot(const TokenRows& p, Elt in_t, const void* in, Elt rows_t,
-                             const void* rows, void* out, float* dweights, hipStream_t s) {
-  if (p.T <= 0) return hipSuccess;
-#define MOE_SPREAD_DOT(I, R)                                                                      \
-  hipLaunchKernelGGL((dot_kernel<I, R, true>), dim3(p.T), dot_block(p.D), 0, s, p, in, rows, out, \
-                     dweights)
-  if (in_t == Elt::BF16) {
-    if (rows_t == Elt::BF16) MOE_SPREAD_DOT(Elt::BF16, Elt::BF16);
-    else MOE_SPREAD_DOT(Elt::BF16, Elt::F32);
-  } else {
-    if (rows_t == Elt::BF16) MOE_SPREAD_DOT(Elt::F32, Elt::BF16);
-    else MOE_SPREAD_DOT(Elt::F32, Elt::F32);
+#define MOE_TOKEN(I, R, B)                                                                         \
+  hipLaunchKernelGGL((token_kernel<I, R, PASS, B, STREAM>), dim3(p.T), dim3(64 * w.segs * w.cuts),         \
+                     PASS != Pass::SpreadDot && w.cuts > 1 ? w.segs * w.cuts * 128 * sizeof(float4) : 0, \
+                     s, p, w.segs, w.cuts, a, rows, add, out, dweights)
+#define MOE_BATCHED(LAUNCH, I, R)                                         \
+  switch (batch_of(p.k)) {                                                \
+    case 2: LAUNCH(I, R, 2); break;                                       \
+    case 4: LAUNCH(I, R, 4); break;                                       \
+    case 6: LAUNCH(I, R, 6); break;                                       \
+    default: LAUNCH(I, R, kMostBatch);                                    \
   }
-#undef MOE_SPREAD_DOT
+#define MOE_TYPED(LAUNCH)                                                 \
+  if (in_t == Elt::BF16) {                                                \
+    if (rows_t == Elt::BF16) MOE_BATCHED(LAUNCH, Elt::BF16, Elt::BF16)    \
+    else MOE_BATCHED(LAUNCH, Elt::BF16, Elt::F32)                         \
+  } else {                                                                \
+    if (rows_t == Elt::BF16) MOE_BATCHED(LAUNCH, Elt::F32, Elt::BF16)     \
+    else MOE_BATCHED(LAUNCH, Elt::F32, Elt::F32)                          \
+  }
+
+namespace {
+template <Pass PASS, bool STREAM>
+void run_tokens(const TokenRows& p, Waves w, Elt in_t, Elt rows_t, const void* a, const void* rows,
+                const void* add, void* out, float* dweights, hipStream_t s) {
+  MOE_TYPED(MOE_TOKEN)
+}
+}  // namespace
+
+hipError_t launch_gather_rows(const TokenRows& p, Elt rows_t, const void* rows, const void* add,
+                              Elt in_t, void* out, const void* a, float* dweights, hipStream_t s) {
+  if (p.T <= 0) return hipSuccess;
+  const bool stream = past_cache(p, in_t, rows_t, 1);
+  const Waves w = token_waves(p);
+  if (dweights) {
+    if (stream) run_tokens<Pass::GatherDot, true>(p, w, in_t, rows_t, a, rows, add, out, dweights, s);
+    else run_tokens<Pass::GatherDot, false>(p, w, in_t, rows_t, a, rows, add, out, dweights, s);
+  } else if (w.cuts > 1) {   // (few tokens)
+    run_tokens<Pass::Gather, false>(p, w, in_t, rows_t, a, rows, add, out, dweights, s);
+  } else {
+#define MOE_GATHER(O, I, B) \
+  hipLaunchKernelGGL((gather_kernel<I, O, B, false>), seg_grid(p), dim3(256), 0, s, p, rows, add, out)
+#define MOE_GATHER_PAST(O, I, B) \
+  hipLaunchKernelGGL((gather_kernel<I, O, B, true>), seg_grid(p), dim3(256), 0, s, p, rows, add, out)
+    if (stream) {
+      MOE_TYPED(MOE_GATHER_PAST)
+    } else {
+      MOE_TYPED(MOE_GATHER)
+    }
+#undef MOE_GATHER_PAST
+#undef MOE_GATHER
+  }
   return hipGetLastError();
 }
+
+hipError_t launch_spread_dot(const TokenRows& p, Elt in_t, const void* a, Elt rows_t,
+                             const void* rows, void* out, float* dweights, hipStream_t s) {
+  if (p.T <= 0) return hipSuccess;
+  const Waves w = token_waves(p);
+  if (past_cache(p, in_t, rows_t, 2))
+    run_tokens<Pass::SpreadDot, true>(p, w, in_t, rows_t, a, rows, nullptr, out, dweights, s);
+  else
+    run_tokens<Pass::SpreadDot, false>(p, w, in_t, rows_t, a, rows, nullptr, out, dweights, s);
+  return hipGetLastError();
+}
+#undef MOE_TYPED
+#undef MOE_BATCHED
+#undef MOE_TOKEN
 
 }  // namespace moe

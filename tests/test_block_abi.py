@@ -31,7 +31,7 @@ SHAPE = [
     (dict(n=64), WS),
 ])
 def test_sort_argument_errors(kw, code):
-    a = dict(x=FAKE, dt=1, idx=ODD, w=None, T=4, D=64, E=8, k=2, rows=FAKE, offsets=ODD, pos=ODD,
+    a = dict(x=FAKE, dt=1, idx=ODD, w=None, T=4000, D=64, E=8, k=2, rows=FAKE, offsets=ODD, pos=ODD,
              ws=FAKE, n=BIG)
     a.update(kw)
     assert moe.lib().moe_sort_tokens(*a.values(), None) == code
@@ -40,7 +40,8 @@ def test_sort_argument_errors(kw, code):
 def test_sort_workspace_size():
     n = C.c_size_t(0)
     L = moe.lib()
-    assert L.moe_sort_tokens_workspace_size(64, 8, 2, C.byref(n)) == OK and n.value >= 64 * 2 * 4
+    assert L.moe_sort_tokens_workspace_size(4000, 8, 2, C.byref(n)) == OK and n.value >= 4000 * 2 * 4
+    assert L.moe_sort_tokens_workspace_size(64, 8, 2, C.byref(n)) == OK and n.value == 0
     assert L.moe_sort_tokens_workspace_size(64, 2, 8, C.byref(n)) == OK   # a rank with few experts
     assert L.moe_sort_tokens_workspace_size(0, 8, 2, C.byref(n)) == OK
     for bad in ((-1, 8, 2), (4, 0, 2), (4, 1025, 2), (4, 8, 0), (4, 8, 65), (1 << 30, 8, 64)):
