@@ -9,25 +9,27 @@ import functools
 
 import torch
 
-from .binding import (MoeClip, MoeClipTensor, _check, _float_code, _launch, _need, _p, _used_on, lib)
+from .binding import (MoeClip, MoeClipTensor, _check, _float_code, _launch, _need, _p, _used_on,
+                      lib)
 
 BLOCK_NORM, GATE_TOKEN, GATE_ELEMENT, GATE_SIGMOID = 1, 2, 4, 8
+_F32, _I32 = torch.float32, torch.int32
+
+# The time of a call on few rows is host time: every tensor is checked and turned into its address
+# in one step, and new outputs, which need no check, are made by the cheapest call.
 
 
-def _rows_of(t, what):
+def _ptr(t, shape, what, dtype, device):
+    """Address of a contiguous tensor that must have this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _need(t, shape, what, dtype, device)
+    return _p(t)
+
+
+def _two(t, what):
     if t.dim() != 2:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected two dimensions")
     return t.shape
-
-
-def _out(given, like, shape, dtype, what, made):
-    """The output tensor: the caller's, checked, or a new one, which is noted in `made`."""
-    if given is None:
-        given = like.new_empty(shape, dtype=dtype)
-        made.append(given)
-    else:
-        _need(given, shape, what, dtype, like.device)
-    return given
 
 
 # ------------------------------------------------------------------------------- token rows
@@ -40,13 +42,12 @@ def _sort_workspace(T, E, k):
     return n.value
 
 
-def _check_pairs(pos, weights, T, dev, what="pos"):
-    if pos.dim() != 2:
-        raise ValueError(f"{what} has shape {tuple(pos.shape)}, expected [tokens, slots]")
-    _need(pos, (T, pos.shape[1]), what, torch.int32, dev)
-    if weights is not None:
-        _need(weights, pos.shape, "weights", torch.float32, dev)
-    return pos.shape[1]
+def _pairs(pos, weights, T, dev, what="pos"):
+    """(slots, address of pos, address of weights or None)."""
+    k = _two(pos, what)[1]
+    shape = pos.shape
+    return (k, _ptr(pos, (T, k), what, _I32, dev),
+            None if weights is None else _ptr(weights, shape, "weights", _F32, dev))
 
 
 def sort_tokens(x, idx, E, *, weights=None, out=None, stream=None):
@@ -55,18 +56,23 @@ def sort_tokens(x, idx, E, *, weights=None, out=None, stream=None):
     None for 1). Expert e's rows are rows[offsets[e]:offsets[e + 1]], tokens ascending; pos is -1
     where a pair is dropped (expert outside [0, E), or repeated in its token). rows has T * k rows;
     those behind offsets[E] are not written. See moe_sort_tokens in moe.h."""
-    T, D = _rows_of(x, "x")
-    dev, made = x.device, []
-    k = _check_pairs(idx, weights, T, dev, "idx")
-    dt = _float_code(x.dtype)
-    rows = _out(out, x, (T * k, D), x.dtype, "out", made)
+    T, D = _two(x, "x")
+    dev, dtype = x.device, x.dtype
+    dt = _float_code(dtype)
+    k, ip, wp = _pairs(idx, weights, T, dev, "idx")
+    if out is None:
+        rows = x.new_empty((T * k, D))
+        rp = rows.data_ptr()
+    else:
+        rows, rp = out, _ptr(out, (T * k, D), "out", dtype, dev)
     offsets = idx.new_empty(E + 1)
-    pos = idx.new_empty((T, k))
+    pos = torch.empty_like(idx)
     n = _sort_workspace(T, E, k)
     ws = x.new_empty(n, dtype=torch.uint8) if n else None
-    _launch(lib().moe_sort_tokens, "moe_sort_tokens", dev, stream, _p(x), dt, _p(idx), _p(weights),
-            T, D, E, k, _p(rows), _p(offsets), _p(pos), _p(ws), n)
-    _used_on(stream, offsets, pos, ws, *made)
+    _launch(lib().moe_sort_tokens, "moe_sort_tokens", dev, stream, _p(x), dt, ip, wp, T, D, E, k, rp,
+            offsets.data_ptr(), pos.data_ptr(), ws.data_ptr() if n else None, n)
+    if stream is not None:
+        _used_on(stream, offsets, pos, ws, rows if out is None else None)
     return rows, offsets, pos
 
 
@@ -74,18 +80,23 @@ def sort_tokens_backward(drows, pos, *, x=None, weights=None, out_dtype=None, st
     """(dx, dweights) of sort_tokens given drows [n, D] and its pos [T, k]: dx [T, D] of out_dtype
     (default: that of drows), dweights [T, k] float32 where x (the sorted rows' source, of drows'
     type) is given, else None. See moe_sort_tokens_backward in moe.h."""
-    n, D = _rows_of(drows, "drows")
-    dev, T, made = drows.device, pos.shape[0], []
-    k = _check_pairs(pos, weights, T, dev)
-    dt = _float_code(drows.dtype)
-    odt = _float_code(out_dtype or drows.dtype)
+    n, D = _two(drows, "drows")
+    dev, dtype, T = drows.device, drows.dtype, pos.shape[0]
+    dt = odt = _float_code(dtype)
+    k, pp, wp = _pairs(pos, weights, T, dev)
+    if out_dtype is None:
+        dx = drows.new_empty((T, D))
+    else:
+        odt = _float_code(out_dtype)
+        dx = drows.new_empty((T, D), dtype=out_dtype)
+    dw = xp = None
     if x is not None:
-        _need(x, (T, D), "x", drows.dtype, dev)
-    dx = _out(None, drows, (T, D), out_dtype or drows.dtype, "dx", made)
-    dw = None if x is None else _out(None, drows, (T, k), torch.float32, "dweights", made)
-    _launch(lib().moe_sort_tokens_backward, "moe_sort_tokens_backward", dev, stream, _p(drows),
-            _p(x), dt, _p(pos), _p(weights), T, D, k, n, _p(dx), odt, _p(dw))
-    _used_on(stream, *made)
+        xp = _ptr(x, (T, D), "x", dtype, dev)
+        dw = torch.empty_like(pos, dtype=_F32)
+    _launch(lib().moe_sort_tokens_backward, "moe_sort_tokens_backward", dev, stream, _p(drows), xp,
+            dt, pp, wp, T, D, k, n, dx.data_ptr(), odt, None if dw is None else dw.data_ptr())
+    if stream is not None:
+        _used_on(stream, dx, dw)
     return dx, dw
 
 
@@ -93,18 +104,23 @@ def unsort_tokens(rows, pos, *, weights=None, add=None, out_dtype=None, out=None
     """y [T, D] of rows [n, D] in expert order: y[t] = add[t] + sum_j weights[t, j] *
     rows[pos[t, j]] (dropped pairs add nothing; weights None: 1). y has out_dtype (default: that
     of out, of add, or of rows), add too; out may be add. See moe_unsort_tokens in moe.h."""
-    n, D = _rows_of(rows, "rows")
-    dev, T, made = rows.device, pos.shape[0], []
-    k = _check_pairs(pos, weights, T, dev)
+    n, D = _two(rows, "rows")
+    dev, T = rows.device, pos.shape[0]
+    dt = _float_code(rows.dtype)
+    k, pp, wp = _pairs(pos, weights, T, dev)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else add.dtype if add is not None else rows.dtype
-    dt, odt = _float_code(rows.dtype), _float_code(out_dtype)
-    if add is not None:
-        _need(add, (T, D), "add", out_dtype, dev)
-    y = _out(out, rows, (T, D), out_dtype, "out", made)
-    _launch(lib().moe_unsort_tokens, "moe_unsort_tokens", dev, stream, _p(rows), dt, _p(pos),
-            _p(weights), _p(add), T, D, k, n, _p(y), odt)
-    _used_on(stream, *made)
+    odt = _float_code(out_dtype)
+    ap = None if add is None else _ptr(add, (T, D), "add", out_dtype, dev)
+    if out is None:
+        y = rows.new_empty((T, D), dtype=out_dtype)
+        yp = y.data_ptr()
+    else:
+        y, yp = out, _ptr(out, (T, D), "out", out_dtype, dev)
+    _launch(lib().moe_unsort_tokens, "moe_unsort_tokens", dev, stream, _p(rows), dt, pp, wp, ap, T,
+            D, k, n, yp, odt)
+    if stream is not None and out is None:
+        _used_on(stream, y)
     return y
 
 
@@ -113,54 +129,61 @@ def unsort_tokens_backward(dy, pos, *, rows=None, weights=None, n_rows=None, out
     and dweights [T, k] float32 where the forward's rows are given, else None. drows is as large and
     of the same type as out or rows (out may be rows), else [n_rows or T * k, D] of dy's type; rows
     that no pair names are not written. See moe_unsort_tokens_backward in moe.h."""
-    T, D = _rows_of(dy, "dy")
-    dev, made = dy.device, []
-    k = _check_pairs(pos, weights, T, dev)
+    T, D = _two(dy, "dy")
+    dev = dy.device
+    dyt = _float_code(dy.dtype)
+    k, pp, wp = _pairs(pos, weights, T, dev)
     like = rows if rows is not None else out
     n = n_rows if n_rows is not None else like.shape[0] if like is not None else T * k
     dtype = like.dtype if like is not None else dy.dtype
+    dt = _float_code(dtype)
+    rp = dw = None
     if rows is not None:
-        _need(rows, (n, D), "rows", dtype, dev)
-    elif dtype != dy.dtype:
+        rp = _ptr(rows, (n, D), "rows", dtype, dev)
+        dw = torch.empty_like(pos, dtype=_F32)
+    elif dt != dyt:
         raise ValueError(f"out has dtype {dtype}: without rows it is dy's, {dy.dtype}")
-    drows = _out(out, dy, (n, D), dtype, "out", made)
-    dw = None if rows is None else _out(None, dy, (T, k), torch.float32, "dweights", made)
-    _launch(lib().moe_unsort_tokens_backward, "moe_unsort_tokens_backward", dev, stream, _p(dy),
-            _float_code(dy.dtype), _p(rows), _float_code(dtype), _p(pos), _p(weights), T, D, k, n,
-            _p(drows), _p(dw))
-    _used_on(stream, *made)
+    if out is None:
+        drows = dy.new_empty((n, D), dtype=dtype)
+        op = drows.data_ptr()
+    else:
+        drows, op = out, _ptr(out, (n, D), "out", dtype, dev)
+    _launch(lib().moe_unsort_tokens_backward, "moe_unsort_tokens_backward", dev, stream, _p(dy), dyt,
+            rp, dt, pp, wp, T, D, k, n, op, None if dw is None else dw.data_ptr())
+    if stream is not None:
+        _used_on(stream, dw, drows if out is None else None)
     return drows, dw
 
 
 # --------------------------------------------------------------------------- the block's norms
 
-def _weight_code(H, dev, dtype, **ws):
-    """moe_dtype_t of the norms' weights: all of one type, float32 or bfloat16."""
-    for name, w in ws.items():
-        if w is not None:
-            _need(w, (H,), name, None, dev)
-            dtype = w.dtype
-    for name, w in ws.items():
-        if w is not None and w.dtype != dtype:
-            raise ValueError(f"{name} has dtype {w.dtype}, the other weight {dtype}")
-    return _float_code(dtype)
+def _weights(w, w_next, H, dev, dt):
+    """(moe_dtype_t of the norms' weights, their addresses): both of one type."""
+    wp = nextp = None
+    if w is not None:
+        dt = _float_code(w.dtype)
+        wp = _ptr(w, (H,), "w", w.dtype, dev)
+    if w_next is not None:
+        if w is not None and w_next.dtype is not w.dtype:
+            raise ValueError(f"w_next has dtype {w_next.dtype}, w {w.dtype}")
+        dt = _float_code(w_next.dtype)
+        nextp = _ptr(w_next, (H,), "w_next", w_next.dtype, dev)
+    return dt, wp, nextp
 
 
-def _gate_flags(gate, gate_act, shape, dtype, dev):
+def _gate(gate, gate_act, shape, dtype, dev):
+    """(flags, address) of a gate per element or per token."""
     if gate_act not in ("sigmoid", "none"):
         raise ValueError(f"gate_act {gate_act!r} is neither 'sigmoid' nor 'none'")
     if gate is None:
-        return 0
-    if gate.shape == shape and gate.dim() == 2 and not (shape[1] == 1):
-        _need(gate, shape, "gate", dtype, dev)
-        kind = GATE_ELEMENT
-    else:
-        if gate.shape != shape[:1] and gate.shape != (shape[0], 1):
-            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {tuple(shape)}, "
-                             f"({shape[0]}, 1) or ({shape[0]},)")
-        _need(gate, gate.shape, "gate", torch.float32, dev)
-        kind = GATE_TOKEN
-    return kind | (GATE_SIGMOID if gate_act == "sigmoid" else 0)
+        return 0, None
+    sigmoid = GATE_SIGMOID if gate_act == "sigmoid" else 0
+    if gate.shape == shape:
+        return GATE_ELEMENT | sigmoid, _ptr(gate, shape, "gate", dtype, dev)
+    if gate.shape != shape[:1] and gate.shape != (shape[0], 1):
+        raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {tuple(shape)}, "
+                         f"({shape[0]}, 1) or ({shape[0]},)")
+    return GATE_TOKEN | sigmoid, _ptr(gate, gate.shape, "gate", _F32, dev)
 
 
 @functools.lru_cache(maxsize=256)
@@ -174,14 +197,19 @@ def _block_workspace(T, H):
 def block_norm(x, w=None, *, eps=1e-5, out=None, stream=None):
     """h = x / sqrt(mean(x^2) + eps) * w per row of x [T, H] (float32 or bfloat16); w [H] float32
     or bfloat16, None for 1. out may be x. See moe_block_norm in moe.h."""
-    T, H = _rows_of(x, "x")
-    dev, made = x.device, []
-    dt = _float_code(x.dtype)
-    wdt = _weight_code(H, dev, x.dtype, w=w)
-    h = _out(out, x, (T, H), x.dtype, "out", made)
-    _launch(lib().moe_block_norm, "moe_block_norm", dev, stream, _p(x), _p(w), _p(h), T, H, dt, wdt,
-            eps)
-    _used_on(stream, *made)
+    T, H = _two(x, "x")
+    dev, dtype = x.device, x.dtype
+    dt = _float_code(dtype)
+    wdt, wp, _ = _weights(w, None, H, dev, dt)
+    xp = _p(x)
+    if out is None:
+        h = torch.empty_like(x)
+        hp = h.data_ptr()
+    else:
+        h, hp = out, _ptr(out, x.shape, "out", dtype, dev)
+    _launch(lib().moe_block_norm, "moe_block_norm", dev, stream, xp, wp, hp, T, H, dt, wdt, eps)
+    if stream is not None and out is None:
+        _used_on(stream, h)
     return h
 
 
@@ -189,24 +217,29 @@ def block_norm_backward(dh, x, w=None, *, dres=None, eps=1e-5, out=None, stream=
     """(dx, dw) of block_norm given dh [T, H] (x's type, or float32): dx = dres + the norm's
     gradient, of x's type (out may be dres); dw [H] float32, None without w. See
     moe_block_norm_backward in moe.h."""
-    T, H = _rows_of(x, "x")
-    dev, made = x.device, []
-    dt = _float_code(x.dtype)
-    _need(dh, (T, H), "dh", None, dev)
-    wdt = _weight_code(H, dev, x.dtype, w=w)
-    if dres is not None:
-        _need(dres, (T, H), "dres", x.dtype, dev)
-    dx = _out(out, x, (T, H), x.dtype, "out", made)
-    dw = ws = None
+    T, H = shape = _two(x, "x")
+    dev, dtype = x.device, x.dtype
+    dt = _float_code(dtype)
+    xp = _p(x)
+    dhp = _ptr(dh, shape, "dh", dh.dtype, dev)
+    wdt, wp, _ = _weights(w, None, H, dev, dt)
+    rp = None if dres is None else _ptr(dres, shape, "dres", dtype, dev)
+    if out is None:
+        dx = torch.empty_like(x)
+        dxp = dx.data_ptr()
+    else:
+        dx, dxp = out, _ptr(out, shape, "out", dtype, dev)
+    dw = ws = dwp = wsp = None
     n = 0
     if w is not None:
-        dw = _out(None, x, (H,), torch.float32, "dw", made)
+        dw = torch.empty_like(w, dtype=_F32)
         n = _block_workspace(T, H)
         ws = x.new_empty(n, dtype=torch.uint8)
-    _launch(lib().moe_block_norm_backward, "moe_block_norm_backward", dev, stream, _p(dh),
-            _float_code(dh.dtype), _p(x), _p(w), _p(dres), _p(dx), _p(dw), T, H, dt, wdt, eps,
-            _p(ws), n)
-    _used_on(stream, ws, *made)
+        dwp, wsp = dw.data_ptr(), ws.data_ptr()
+    _launch(lib().moe_block_norm_backward, "moe_block_norm_backward", dev, stream, dhp,
+            _float_code(dh.dtype), xp, wp, rp, dxp, dwp, T, H, dt, wdt, eps, wsp, n)
+    if stream is not None:
+        _used_on(stream, ws, dw, dx if out is None else None)
     return dx, dw
 
 
@@ -217,19 +250,30 @@ def block_residual(x, f, *, w=None, norm=True, gate=None, gate_act="sigmoid", sc
     [T] or [T, 1]), per element ([T, H], x's type), or None for 1. With next_norm (or h_out, or
     w_next) h is the next block's norm of y, else None. out may be x or f. See moe_block_residual
     in moe.h."""
-    T, H = _rows_of(x, "x")
-    dev, made = x.device, []
-    dt = _float_code(x.dtype)
-    _need(f, (T, H), "f", x.dtype, dev)
-    wdt = _weight_code(H, dev, x.dtype, w=w, w_next=w_next)
-    flags = _gate_flags(gate, gate_act, x.shape, x.dtype, dev) | (BLOCK_NORM if norm else 0)
-    y = _out(out, x, (T, H), x.dtype, "out", made)
-    h = None
-    if next_norm or w_next is not None or h_out is not None:
-        h = _out(h_out, x, (T, H), x.dtype, "h_out", made)
-    _launch(lib().moe_block_residual, "moe_block_residual", dev, stream, _p(x), _p(f), _p(w),
-            _p(gate), _p(w_next), _p(y), _p(h), T, H, dt, wdt, flags, scale, eps)
-    _used_on(stream, *made)
+    T, H = shape = _two(x, "x")
+    dev, dtype = x.device, x.dtype
+    dt = _float_code(dtype)
+    xp = _p(x)
+    fp = _ptr(f, shape, "f", dtype, dev)
+    wdt, wp, nextp = _weights(w, w_next, H, dev, dt)
+    flags, gp = _gate(gate, gate_act, shape, dtype, dev)
+    if norm:
+        flags |= BLOCK_NORM
+    if out is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        y, yp = out, _ptr(out, shape, "out", dtype, dev)
+    h = hp = None
+    if h_out is not None:
+        h, hp = h_out, _ptr(h_out, shape, "h_out", dtype, dev)
+    elif next_norm or w_next is not None:
+        h = torch.empty_like(x)
+        hp = h.data_ptr()
+    _launch(lib().moe_block_residual, "moe_block_residual", dev, stream, xp, fp, wp, gp, nextp, yp, hp,
+            T, H, dt, wdt, flags, scale, eps)
+    if stream is not None:
+        _used_on(stream, y if out is None else None, h if h_out is None else None)
     return y, h
 
 
@@ -239,38 +283,48 @@ def block_residual_backward(dy, f, *, w=None, norm=True, gate=None, gate_act="si
     w_next are given. dy [T, H] (f's type, or None where only h was used) reaches y; dh (f's type or
     float32), with the forward's y, reaches h. dw and dw_next are float32. See
     moe_block_residual_backward in moe.h."""
-    T, H = _rows_of(f, "f")
-    dev, made, dtype = f.device, [], f.dtype
-    dt = _float_code(dtype)
+    T, H = shape = _two(f, "f")
+    dev, dtype = f.device, f.dtype
+    dt = dh_dt = _float_code(dtype)
+    fp = _p(f)
     if dy is None and dh is None:
         raise ValueError("dy or dh is required")
-    if dy is not None:
-        _need(dy, (T, H), "dy", dtype, dev)
-    dh_dt = dt
+    dyp = None if dy is None else _ptr(dy, shape, "dy", dtype, dev)
+    yp = dhp = None
     if dh is not None:
-        _need(dh, (T, H), "dh", None, dev)
-        _need(y, (T, H), "y", dtype, dev)
         dh_dt = _float_code(dh.dtype)
+        dhp = _ptr(dh, shape, "dh", dh.dtype, dev)
+        if y is None:
+            raise ValueError("y is required with dh")
+        yp = _ptr(y, shape, "y", dtype, dev)
     elif w_next is not None:
         raise ValueError("w_next has no gradient without dh")
-    wdt = _weight_code(H, dev, dtype, w=w, w_next=w_next)
-    flags = _gate_flags(gate, gate_act, f.shape, dtype, dev) | (BLOCK_NORM if norm else 0)
-    out = {n: _out(None, f, (T, H), dtype, n, made) for n in ("dx", "df")}
+    wdt, wp, nextp = _weights(w, w_next, H, dev, dt)
+    flags, gp = _gate(gate, gate_act, shape, dtype, dev)
+    if norm:
+        flags |= BLOCK_NORM
+    dx, df = torch.empty_like(f), torch.empty_like(f)
+    out = {"dx": dx, "df": df}
+    dgp = dwp = dnp = ws = wsp = None
+    n = 0
     if gate is not None:
-        out["dgate"] = _out(None, f, gate.shape, gate.dtype, "dgate", made)
-    ws, n = None, 0
-    if w is not None or w_next is not None:
-        for name, t in (("dw", w), ("dw_next", w_next)):
-            if t is not None:
-                out[name] = _out(None, f, (H,), torch.float32, name, made)
+        out["dgate"] = dgate = torch.empty_like(gate)
+        dgp = dgate.data_ptr()
+    if w is not None:
+        out["dw"] = dw = torch.empty_like(w, dtype=_F32)
+        dwp = dw.data_ptr()
+    if w_next is not None:
+        out["dw_next"] = dw = torch.empty_like(w_next, dtype=_F32)
+        dnp = dw.data_ptr()
+    if dwp is not None or dnp is not None:
         n = _block_workspace(T, H)
         ws = f.new_empty(n, dtype=torch.uint8)
-    get = out.get
-    _launch(lib().moe_block_residual_backward, "moe_block_residual_backward", dev, stream, _p(dy),
-            _p(f), _p(w), _p(gate), _p(y), _p(dh), dh_dt, _p(w_next), _p(out["dx"]), _p(out["df"]),
-            _p(get("dw")), _p(get("dgate")), _p(get("dw_next")), T, H, dt, wdt, flags, scale, eps,
-            _p(ws), n)
-    _used_on(stream, ws, *made)
+        wsp = ws.data_ptr()
+    _launch(lib().moe_block_residual_backward, "moe_block_residual_backward", dev, stream, dyp, fp,
+            wp, gp, yp, dhp, dh_dt, nextp, dx.data_ptr(), df.data_ptr(), dwp, dgp, dnp, T, H, dt, wdt,
+            flags, scale, eps, wsp, n)
+    if stream is not None:
+        _used_on(stream, ws, *out.values())
     return out
 
 
