@@ -8,11 +8,11 @@ is its thin Python binding: torch provides device memory and streams.
 from .binding import (Backward, Layer, MoeError, alloc_routing, backward_from, bias_update,
                       dispatch, layer_forward, layer_from, lib, mx_dequantize, mx_gemm,
                       mx_quantize, route, status_str, to_device, workspace_size)
-from .block import (GradClip, block_norm, block_norm_backward, block_residual,
+from .block import (Block, GradClip, block_norm, block_norm_backward, block_residual,
                     block_residual_backward, clip_grad_norm, sort_tokens, sort_tokens_backward,
                     unsort_tokens, unsort_tokens_backward)
 
-__all__ = ["Backward", "GradClip", "Layer", "MoeError", "alloc_routing", "backward_from",
+__all__ = ["Backward", "Block", "GradClip", "Layer", "MoeError", "alloc_routing", "backward_from",
            "bias_update", "block_norm", "block_norm_backward", "block_residual",
            "block_residual_backward", "clip_grad_norm", "dispatch", "layer_forward", "layer_from",
            "lib", "mx_dequantize", "mx_gemm", "mx_quantize", "route", "sort_tokens",

@@ -367,6 +367,7 @@ class Backward:
                "moe_backward_workspace_size")
         self.ws_bytes = n.value
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=x.device)
+        self._clip = None
 
     def forward_train(self, y=None, stream=None):
         """y of the layer (grouped path), keeping what the backward pass reads in the workspace:
@@ -392,6 +393,16 @@ class Backward:
                                       _p(self.ws), self.ws_bytes, _stream(stream))
         _check(rc, "moe_layer_backward")
         return self.grads
+
+    def clip(self, max_norm, stream=None):
+        """Clips the weight gradients of the last call in place by their global norm, which is
+        returned (GradClip over self.grads without dx, made on the first call: outside a capture)."""
+        if self._clip is None:
+            from .block import GradClip
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("the first clip() makes its table: call it once before a capture")
+            self._clip = GradClip({n: g for n, g in self.grads.items() if n != "dx"}, stream=stream)
+        return self._clip(max_norm, stream)
 
 
 def backward_from(dev: dict, k: int, **kw) -> Backward:

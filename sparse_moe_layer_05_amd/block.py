@@ -9,8 +9,8 @@ import functools
 
 import torch
 
-from .binding import (MoeClip, MoeClipTensor, _check, _float_code, _launch, _need, _p, _used_on,
-                      lib)
+from .binding import (MOE_BF16, Layer, MoeClip, MoeClipTensor, _check, _float_code, _launch, _need,
+                      _p, _used_on, lib)
 
 BLOCK_NORM, GATE_TOKEN, GATE_ELEMENT, GATE_SIGMOID = 1, 2, 4, 8
 _F32, _I32 = torch.float32, torch.int32
@@ -336,7 +336,8 @@ class GradClip:
     grad * min(1, max_norm / (norm + 1e-6)) into the gradients, or into ``out`` (as many tensors of
     the same shapes and types), and returns the norm (a float32 tensor that the next call
     overwrites; ``coef`` is beside it). A norm that is not finite leaves the values as they are.
-    Calls of one GradClip must not overlap. See moe_clip_plan in moe.h."""
+    Calls of one GradClip must not overlap; one that was made while a stream was captured serves
+    that capture alone (its table is written by the graph). See moe_clip_plan in moe.h."""
 
     def __init__(self, grads, *, out=None, stream=None):
         grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
@@ -347,12 +348,20 @@ class GradClip:
             raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
         dev = grads[0].device
         table = (MoeClipTensor * len(grads))()
+        spans = []
         for i, (g, o) in enumerate(zip(grads, outs)):
-            _need(g, g.shape, f"grads[{i}]", None, dev)
-            _need(o, g.shape, f"out[{i}]", g.dtype, dev)
-            table[i].grad, table[i].out, table[i].n = _p(g), _p(o), g.numel()
-            table[i].dt = _float_code(g.dtype)
-        self._check_apart(grads, outs)
+            n, dtype = g.numel(), g.dtype
+            dt = _float_code(dtype)
+            gp = op = _ptr(g, g.shape, "a gradient", dtype, dev)
+            if o is not g:
+                op = _ptr(o, g.shape, "an output", dtype, dev)
+            table[i] = (gp, op, n, dt)
+            if n:
+                size = n * (2 if dt == MOE_BF16 else 4)
+                if op != gp:
+                    spans.append((gp, gp + size, False))
+                spans.append((op, op + size, True))
+        _check_apart(spans)
         n = C.c_size_t(0)
         _check(lib().moe_clip_plan_size(table, len(grads), C.byref(n)), "moe_clip_plan_size")
         self._keep = (grads, outs)
@@ -362,35 +371,67 @@ class GradClip:
         _launch(lib().moe_clip_plan, "moe_clip_plan", dev, stream, table, len(grads), _p(self.plan),
                 n.value, C.byref(self.clip))
         both = grads[0].new_empty(2, dtype=torch.float32)
-        _used_on(stream, self.plan, both)
+        if stream is not None:
+            _used_on(stream, self.plan, both)
         self.norm, self.coef = both[0], both[1]
         self._args = (C.byref(self.clip), both.data_ptr())
-
-    @staticmethod
-    def _check_apart(grads, outs):
-        """Every output lies apart from the others and from the other tensors' gradients."""
-        spans = []
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            for t, writes in ((o, True),) if o.data_ptr() == g.data_ptr() else ((g, False), (o, True)):
-                if t.numel():
-                    spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i, writes))
-        spans.sort()
-        end = written = 0    # ends of what was read or written, and of what was written, so far
-        for lo, hi, i, writes in spans:
-            if lo < written or (writes and lo < end):
-                raise ValueError(f"gradient or output {i} overlaps another one that is written")
-            end = max(end, hi)
-            if writes:
-                written = max(written, hi)
+        self._captured = torch.cuda.is_current_stream_capturing()
 
     def __call__(self, max_norm, stream=None):
+        if self._captured and not torch.cuda.is_current_stream_capturing():
+            raise ValueError("this GradClip was made while a stream was captured and serves that "
+                             "capture alone")
         clip, norm = self._args
         _launch(lib().moe_clip_grads, "moe_clip_grads", self.device, stream, clip, max_norm, norm)
         return self.norm
 
 
+def _check_apart(spans):
+    """spans: (begin, end, written) of every gradient and output. What is written lies apart from
+    everything else."""
+    end = written = 0    # ends of what is read or written, and of what is written, so far
+    for lo, hi, writes in sorted(spans):
+        if lo < written or (writes and lo < end):
+            raise ValueError("an output overlaps another output or another gradient")
+        end = max(end, hi)
+        if writes:
+            written = max(written, hi)
+
+
 def clip_grad_norm(grads, max_norm, *, out=None, stream=None):
     """GradClip for one use: clips grads (or into out) and returns their norm."""
     clip = GradClip(grads, out=out, stream=stream)
-    _used_on(stream, *clip._keep[0], *clip._keep[1])
-    return clip(max_norm, stream)
+    norm = clip(max_norm, stream)
+    if stream is not None:
+        _used_on(stream, *clip._keep[0], *clip._keep[1])
+    return norm
+
+
+# -------------------------------------------------------------------------------------- the block
+
+class Block:
+    """A layer in its residual block, prepared once as Layer is:
+        h = norm(x) * w_in;  f = layer(h);  y = x + scale * a * norm(f) * w_out
+    with the gate a as in block_residual (norm_out=False: f * w_out alone). ``__call__`` returns y;
+    with next_norm (or w_next) ``h_next`` holds the next block's norm of y. h: the rows as a block
+    before left them (its h_next), instead of norm(x) * w_in. Other keywords go to Layer."""
+
+    def __init__(self, x, W_r, b, W_up, W_down, k, *, w_in=None, w_out=None, norm_out=True,
+                 gate=None, gate_act="sigmoid", scale=1.0, next_norm=False, w_next=None, eps=1e-5,
+                 h=None, **layer):
+        if h is not None and w_in is not None:
+            raise ValueError("w_in and h exclude each other")
+        self.x, self.w_in, self.eps, self.own_norm = x, w_in, eps, h is None
+        self.h = torch.empty_like(x) if h is None else h
+        self.layer = Layer(self.h, W_r, b, W_up, W_down, k, **layer)
+        self.y = torch.empty_like(x)
+        self.h_next = torch.empty_like(x) if next_norm or w_next is not None else None
+        self.after = dict(w=w_out, norm=norm_out, gate=gate, gate_act=gate_act, scale=scale,
+                          w_next=w_next, eps=eps, out=self.y, h_out=self.h_next)
+
+    def __call__(self, stream=None):
+        if self.own_norm:
+            block_norm(self.x, self.w_in, eps=self.eps, out=self.h, stream=stream)
+        f = self.layer(stream)
+        block_residual(self.x, f, stream=stream, **self.after)
+        return self.y

