@@ -28,26 +28,11 @@ TokenRows token_rows_of(const int32_t* pos, const float* weights, int32_t T, int
   return r;
 }
 
-struct SortPlan {
-  size_t counts = 0, perm = 0, scratch = 0, total = 0;
-};
-int32_t make_sort_plan(int32_t T, int32_t E, int32_t k, SortPlan* out) {
+// Bytes of the chunk counts that the sort of many pairs needs; few are sorted in one launch.
+int32_t sort_workspace(int32_t T, int32_t E, int32_t k, size_t* bytes) {
   if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || (int64_t)T * k > INT32_MAX)
     return MOE_ERR_INVALID_ARG;
-  if (sort_is_small(T, k)) {   // one launch, no workspace
-    *out = SortPlan();
-    return MOE_OK;
-  }
-  size_t off = 0;
-  auto take = [&](size_t ints) {
-    const size_t at = off;
-    off += (ints * sizeof(int32_t) + kAlign - 1) / kAlign * kAlign;
-    return at;
-  };
-  out->counts = take((size_t)E);
-  out->perm = take((size_t)T * k);
-  out->scratch = take(dispatch_scratch_ints(T, E, k));
-  out->total = off;
+  *bytes = sort_is_small(T, k) ? 0 : dispatch_scratch_ints(T, E, k) / 2 * sizeof(int32_t);
   return MOE_OK;
 }
 
@@ -57,7 +42,7 @@ constexpr uint32_t kBlockFlags = MOE_BLOCK_NORM | MOE_GATE_TOKEN | MOE_GATE_ELEM
 
 int32_t block_shape(int32_t T, int32_t H, moe_dtype_t dt, moe_dtype_t w_dt, uint32_t flags,
                     float scale, float eps, BlockShape* out) {
-  if (T < 0 || T > kBlockMaxT || H < 16 || H % 16 || H > kBlockMaxH) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || T >= kBlockMaxT || H < 16 || H % 16 || H > kBlockMaxH) return MOE_ERR_INVALID_ARG;
   if (flags & ~kBlockFlags) return MOE_ERR_INVALID_ARG;
   if ((flags & MOE_GATE_TOKEN) && (flags & MOE_GATE_ELEMENT)) return MOE_ERR_INVALID_ARG;
   if (!(eps > 0.f) || !(eps < __builtin_inff()) || !(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;
@@ -107,32 +92,25 @@ int32_t clip_check(const moe_clip_tensor_t* t, int32_t count, int64_t* chunks) {
 extern "C" {
 
 int32_t moe_sort_tokens_workspace_size(int32_t T, int32_t E, int32_t k, size_t* bytes) {
-  SortPlan pl;
-  if (!bytes) return MOE_ERR_INVALID_ARG;
-  const int32_t rc = make_sort_plan(T, E, k, &pl);
-  if (rc == MOE_OK) *bytes = pl.total;
-  return rc;
+  return bytes ? sort_workspace(T, E, k, bytes) : MOE_ERR_INVALID_ARG;
 }
 
 int32_t moe_sort_tokens(const void* x, moe_dtype_t dt, const int32_t* idx, const float* weights,
                         int32_t T, int32_t D, int32_t E, int32_t k, void* rows, int32_t* offsets,
                         int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
-  SortPlan pl;
+  size_t need = 0;
   int32_t rc = rows_shape(T, D, k);
-  if (rc == MOE_OK) rc = make_sort_plan(T, E, k, &pl);
+  if (rc == MOE_OK) rc = sort_workspace(T, E, k, &need);
   if (rc) return rc;
   if (!float_type(dt)) return MOE_ERR_UNSUPPORTED;
   if (!offsets || (T && (!x || !idx || !rows || !pos)) || !absent_or_aligned(x) ||
       !absent_or_aligned(rows))
     return MOE_ERR_INVALID_ARG;
   hipStream_t s = (hipStream_t)stream;
-  if (pl.total == 0)
+  if (need == 0)
     return hip_status(launch_sort_small(idx, weights, T, D, E, k, elt_of(dt), x, rows, offsets, pos, s));
-  if (!ws || ws_bytes < pl.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
-  char* base = (char*)ws;
-  MOE_TRY(launch_dispatch(idx, T, E, k, (int32_t*)(base + pl.counts), offsets,
-                          (int32_t*)(base + pl.perm), pos, (int32_t*)(base + pl.scratch), 0, nullptr,
-                          DispatchExtras(), s));
+  if (!ws || ws_bytes < need || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  MOE_TRY(launch_positions(idx, T, E, k, (int32_t*)ws, offsets, pos, s));
   return hip_status(launch_spread_rows(token_rows_of(pos, weights, T, D, k, T * k), elt_of(dt), x,
                                        rows, s));
 }

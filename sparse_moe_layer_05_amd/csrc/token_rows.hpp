@@ -31,6 +31,11 @@ hipError_t launch_sort_small(const int32_t* idx, const float* weights, int T, in
                              Elt t, const void* in, void* out, int32_t* offsets, int32_t* pos,
                              hipStream_t s);
 
+// Positions and offsets alone, in two launches (T >= 1, E <= 1024). scratch: ceil(T / chunk) * E ints,
+// chunk as the dispatch cuts the tokens.
+hipError_t launch_positions(const int32_t* idx, int T, int E, int k, int32_t* scratch,
+                            int32_t* offsets, int32_t* pos, hipStream_t s);
+
 // out[t] = add[t] + sum_j weights[t, j] * rows[pos[t, j]], rounded once (add, of out's type, may be
 // nullptr). With dweights: dweights[t, j] = <a[t], rows[pos[t, j]]>, a of the rows' type (0 for dropped
 // pairs).

@@ -81,6 +81,98 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenRows p, const void* in
   }
 }
 
+// Positions from the dispatch's chunk counts [nch][E] (dispatch_count): a workgroup per chunk of CH
+// tokens adds up, for every expert, the chunks before its own and all of them, which takes the place
+// of a launch that scans them; the rest is a chunk's own masks.
+constexpr int kPlaceThreads = 1024;
+template <int CH>
+__global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t* __restrict__ idx, int T,
+                                                              int E, int k,
+                                                              const int32_t* __restrict__ ccount,
+                                                              int nch, int32_t* __restrict__ offsets,
+                                                              int32_t* __restrict__ pos) {
+  extern __shared__ uint32_t mask[];   // [CH / 32][E]
+  __shared__ int32_t total[1024], start[1024];   // start: pairs of lower chunks, then first row
+  __shared__ int32_t sums[kPlaceThreads / 64];
+  __shared__ uint64_t valid[CH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, chunk = blockIdx.x;
+  for (int e = tid; e < 1024; e += kPlaceThreads) total[e] = start[e] = 0;
+  for (int i = tid; i < E * (CH / 32); i += kPlaceThreads) mask[i] = 0;
+  __syncthreads();
+  // several groups of threads share an expert's chunks (whole numbers: their order is free)
+  const int lg = 32 - __clz(max(E - 1, 1));   // log2 of the experts rounded up
+  const int e0 = tid & ((1 << lg) - 1), group = tid >> lg, groups = kPlaceThreads >> lg;
+  if (e0 < E) {
+    int all = 0, before = 0;
+    for (int c0 = group; c0 < nch; c0 += 8 * groups) {
+      int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + i * groups;
+        v[i] = c < nch ? ccount[(int64_t)c * E + e0] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        all += v[i];
+        if (c0 + i * groups < chunk) before += v[i];
+      }
+    }
+    atomicAdd(&total[e0], all);
+    atomicAdd(&start[e0], before);
+  }
+  // the chunk's masks, a token a thread: a repeated expert of a token is dropped
+  if (tid < CH) {
+    const int t = chunk * CH + tid;
+    uint64_t kept = 0;
+    if (t < T) {
+      const uint32_t bit = 1u << (tid & 31);
+      for (int j0 = 0; j0 < k; j0 += 8) {
+        int ev[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ev[i] = j0 + i < k ? idx[(int64_t)t * k + j0 + i] : -1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if ((unsigned)ev[i] >= (unsigned)E) continue;
+          const uint32_t old = atomicOr(&mask[(tid >> 5) * E + ev[i]], bit);
+          if (!(old & bit)) kept |= 1ull << (j0 + i);
+        }
+      }
+    }
+    valid[tid] = kept;
+  }
+  __syncthreads();
+  // the running sum over the experts (kPlaceThreads >= 1024 >= E)
+  const int mine = total[tid];
+  int up = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(up, d);
+    if (lane >= d) up += o;
+  }
+  if (lane == 63) sums[wave] = up;
+  __syncthreads();
+  int base = up - mine;
+  for (int w = 0; w < wave; ++w) base += sums[w];
+  start[tid] += base;
+  if (chunk == 0) {
+    if (tid < E) offsets[tid] = base;
+    if (tid == E - 1) offsets[E] = base + mine;
+  }
+  __syncthreads();
+  const int pairs = min(CH, T - chunk * CH) * k;
+  for (int i = tid; i < pairs; i += kPlaceThreads) {
+    const int t = i / k, j = i - t * k;
+    const int64_t at = (int64_t)chunk * CH * k + i;
+    int row = -1;
+    if (valid[t] >> j & 1) {
+      const int e = idx[at], w = t >> 5;
+      row = start[e] + __popc(mask[w * E + e] & ((1u << (t & 31)) - 1));
+      for (int q = 0; q < w; ++q) row += __popc(mask[q * E + e]);
+    }
+    pos[at] = row;
+  }
+}
+
 // The rows of the pairs [j0, j0 + B), and acc += their weights times them.
 template <Elt ROWS, int B, bool STREAM>
 __device__ __forceinline__ void load_batch(const TokenRows& p, const Pairs& pr, const void* rows,
@@ -366,6 +458,22 @@ hipError_t launch_spread_rows(const TokenRows& p, Elt t, const void* in, void* o
   }
 #undef MOE_SPREAD_W
 #undef MOE_SPREAD
+  return hipGetLastError();
+}
+
+hipError_t launch_positions(const int32_t* idx, int T, int E, int k, int32_t* scratch,
+                            int32_t* offsets, int32_t* pos, hipStream_t s) {
+  if (T <= 0 || E > 1024 || k > 64) return hipErrorInvalidValue;
+  const int ch = dispatch_chunk(T, k), nch = (int)(((int64_t)T + ch - 1) / ch);
+  const size_t lds = (size_t)E * (ch / 32) * sizeof(uint32_t);
+  auto run = [&](auto count, auto place) {
+    hipLaunchKernelGGL(count, dim3(nch), dim3(ch), lds, s, idx, T, E, k, scratch);
+    hipLaunchKernelGGL(place, dim3(nch), dim3(kPlaceThreads), lds, s, idx, T, E, k, scratch, nch,
+                       offsets, pos);
+  };
+  if (ch == 64) run(dispatch_count<64>, place_kernel<64>);
+  else if (ch == 128) run(dispatch_count<128>, place_kernel<128>);
+  else run(dispatch_count<256>, place_kernel<256>);
   return hipGetLastError();
 }
 

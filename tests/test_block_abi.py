@@ -28,7 +28,7 @@ SHAPE = [
     (dict(E=0), BAD), (dict(E=1025), BAD), (dict(dt=B.MOE_FP8_E4M3), UNS), (dict(x=None), BAD),
     (dict(idx=None), BAD), (dict(rows=None), BAD), (dict(offsets=None), BAD), (dict(pos=None), BAD),
     (dict(x=ODD), BAD), (dict(rows=ODD), BAD), (dict(ws=None), WS), (dict(ws=ODD), WS),
-    (dict(n=64), WS),
+    (dict(n=16), WS),
 ])
 def test_sort_argument_errors(kw, code):
     a = dict(x=FAKE, dt=1, idx=ODD, w=None, T=4000, D=64, E=8, k=2, rows=FAKE, offsets=ODD, pos=ODD,
@@ -40,7 +40,7 @@ def test_sort_argument_errors(kw, code):
 def test_sort_workspace_size():
     n = C.c_size_t(0)
     L = moe.lib()
-    assert L.moe_sort_tokens_workspace_size(4000, 8, 2, C.byref(n)) == OK and n.value >= 4000 * 2 * 4
+    assert L.moe_sort_tokens_workspace_size(4000, 8, 2, C.byref(n)) == OK and n.value >= 8 * 4
     assert L.moe_sort_tokens_workspace_size(64, 8, 2, C.byref(n)) == OK and n.value == 0
     assert L.moe_sort_tokens_workspace_size(64, 2, 8, C.byref(n)) == OK   # a rank with few experts
     assert L.moe_sort_tokens_workspace_size(0, 8, 2, C.byref(n)) == OK
@@ -86,7 +86,7 @@ def test_unsort_backward_argument_errors(kw, code):
 
 INF, NAN = float("inf"), float("nan")
 BLOCK = [
-    (dict(T=0), OK), (dict(T=-1), BAD), (dict(T=(1 << 23) + 1), BAD), (dict(H=0), BAD),
+    (dict(T=0), OK), (dict(T=-1), BAD), (dict(T=1 << 23), BAD), (dict(H=0), BAD),
     (dict(H=24), BAD), (dict(H=16400), BAD), (dict(H=-16), BAD), (dict(eps=0.0), BAD),
     (dict(eps=-1.0), BAD), (dict(eps=NAN), BAD), (dict(eps=INF), BAD), (dict(dt=2), UNS),
     (dict(w_dt=3), UNS),
