@@ -194,6 +194,19 @@ def test_rows_of_zeros_and_far_values(H, dtype):
         O.check(got[n], ref[n][0], dtype, ref[n][1], GRAD + SUM, n)
 
 
+def test_rows_past_32_bits():
+    """More than 2^31 elements: the last rows are those of a call on them alone."""
+    T, H = (1 << 31) // 16384 + 9, 16384
+    x = torch.randn(64, H, device="cuda").to(BF).repeat(T // 64 + 1, 1)[:T].contiguous()
+    f = x.flip(0).contiguous()
+    y, h = moe.block_residual(x, f, next_norm=True)
+    y1, h1 = moe.block_residual(x[-20:].contiguous(), f[-20:].contiguous(), next_norm=True)
+    assert torch.equal(y[-20:], y1) and torch.equal(h[-20:], h1)
+    got = moe.block_residual_backward(x, f, y=y, dh=h)
+    part = moe.block_residual_backward(x[-20:].contiguous(), f[-20:].contiguous(), y=y1, dh=h1)
+    assert all(torch.equal(got[n][-20:], part[n]) for n in part)
+
+
 def test_gates_at_their_ends():
     """Sigmoids of far and infinite gates, and their slopes, which are small on both sides."""
     T, H = 8, 128

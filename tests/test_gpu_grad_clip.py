@@ -130,6 +130,19 @@ def test_values_whose_squares_leave_fp32():
             check(grads, outs, norm, clip.coef, limit if scale > 1 else float(torch.tensor(limit)))
 
 
+def test_a_tensor_past_32_bits():
+    n = (1 << 31) + 5
+    g = torch.full((n,), 2.0 ** -10, dtype=BF, device="cuda")
+    g[-3:] = 7.0
+    clip = moe.GradClip([g])
+    norm = clip(1.0)
+    true = math.sqrt((n - 3) * 2.0 ** -20 + 3 * 49.0)
+    assert abs(float(norm) - true) <= 1e-6 * true
+    c = float(clip.coef)
+    want = torch.tensor([2.0 ** -10, 7.0], dtype=F32) * c
+    assert bool((g[:-3] == want[0].to(BF).cuda()).all()) and bool((g[-3:] == want[1].to(BF).cuda()).all())
+
+
 def test_one_use_and_other_shapes():
     g = torch.Generator().manual_seed(24)
     grads = {"a": torch.randn(12, 40, 3, generator=g).cuda(), "b": torch.randn(64, generator=g).cuda()}

@@ -225,3 +225,13 @@ def test_rows_past_32_bits():
     assert int((dr[2:n - 2] != 0).any()) == 0
     y = moe.unsort_tokens(dr, pos)
     assert torch.equal(y, (2 * dy.float()).to(BF))
+
+
+def test_short_rows_past_32_bits():
+    n, D, T = (1 << 31) // 128 + 5, 128, 5000
+    rows = torch.zeros(n, D, dtype=BF, device="cuda")
+    pos = torch.arange(n - T, n, dtype=torch.int32, device="cuda")[:, None]
+    dy = torch.randn(T, D, device="cuda").to(BF)
+    dr, _ = moe.unsort_tokens_backward(dy, pos, out=rows)
+    assert torch.equal(dr[n - T:], dy) and int((dr[:n - T] != 0).any()) == 0
+    assert torch.equal(moe.unsort_tokens(dr, pos), dy)
