@@ -28,11 +28,30 @@ TokenRows token_rows_of(const int32_t* pos, const float* weights, int32_t T, int
   return r;
 }
 
-// Bytes of the chunk counts that the sort of many pairs needs; few are sorted in one launch.
-int32_t sort_workspace(int32_t T, int32_t E, int32_t k, size_t* bytes) {
+// The sort's scratch: none for few pairs; the chunk counts; where chunks are too many for each
+// workgroup to add them up, what the dispatch needs.
+struct SortPlan {
+  size_t counts = 0, perm = 0, scratch = 0, total = 0;
+  bool chunked = false;
+};
+int32_t make_sort_plan(int32_t T, int32_t E, int32_t k, SortPlan* out) {
   if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || (int64_t)T * k > INT32_MAX)
     return MOE_ERR_INVALID_ARG;
-  *bytes = sort_is_small(T, k) ? 0 : dispatch_scratch_ints(T, E, k) / 2 * sizeof(int32_t);
+  SortPlan pl;
+  auto take = [&](size_t ints) {
+    const size_t at = pl.total;
+    pl.total += (ints * sizeof(int32_t) + kAlign - 1) / kAlign * kAlign;
+    return at;
+  };
+  if (!sort_is_small(T, k)) {
+    pl.chunked = positions_by_chunks(T, E, k);
+    pl.scratch = take(dispatch_scratch_ints(T, E, k) / (pl.chunked ? 2 : 1));
+    if (!pl.chunked) {
+      pl.counts = take((size_t)E);
+      pl.perm = take((size_t)T * k);
+    }
+  }
+  *out = pl;
   return MOE_OK;
 }
 
@@ -45,7 +64,7 @@ int32_t block_shape(int32_t T, int32_t H, moe_dtype_t dt, moe_dtype_t w_dt, uint
   if (T < 0 || T >= kBlockMaxT || H < 16 || H % 16 || H > kBlockMaxH) return MOE_ERR_INVALID_ARG;
   if (flags & ~kBlockFlags) return MOE_ERR_INVALID_ARG;
   if ((flags & MOE_GATE_TOKEN) && (flags & MOE_GATE_ELEMENT)) return MOE_ERR_INVALID_ARG;
-  if (!(eps > 0.f) || !(eps < __builtin_inff()) || !(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 1e-30f) || !(eps < __builtin_inff()) || !(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;
   if (!float_type(dt) || !float_type(w_dt)) return MOE_ERR_UNSUPPORTED;
   BlockShape b;
   b.T = T; b.H = H; b.t = elt_of(dt); b.w_t = elt_of(w_dt);
@@ -92,25 +111,35 @@ int32_t clip_check(const moe_clip_tensor_t* t, int32_t count, int64_t* chunks) {
 extern "C" {
 
 int32_t moe_sort_tokens_workspace_size(int32_t T, int32_t E, int32_t k, size_t* bytes) {
-  return bytes ? sort_workspace(T, E, k, bytes) : MOE_ERR_INVALID_ARG;
+  SortPlan pl;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const int32_t rc = make_sort_plan(T, E, k, &pl);
+  if (rc == MOE_OK) *bytes = pl.total;
+  return rc;
 }
 
 int32_t moe_sort_tokens(const void* x, moe_dtype_t dt, const int32_t* idx, const float* weights,
                         int32_t T, int32_t D, int32_t E, int32_t k, void* rows, int32_t* offsets,
                         int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
-  size_t need = 0;
+  SortPlan pl;
   int32_t rc = rows_shape(T, D, k);
-  if (rc == MOE_OK) rc = sort_workspace(T, E, k, &need);
+  if (rc == MOE_OK) rc = make_sort_plan(T, E, k, &pl);
   if (rc) return rc;
   if (!float_type(dt)) return MOE_ERR_UNSUPPORTED;
   if (!offsets || (T && (!x || !idx || !rows || !pos)) || !absent_or_aligned(x) ||
       !absent_or_aligned(rows))
     return MOE_ERR_INVALID_ARG;
   hipStream_t s = (hipStream_t)stream;
-  if (need == 0)
+  if (pl.total == 0)
     return hip_status(launch_sort_small(idx, weights, T, D, E, k, elt_of(dt), x, rows, offsets, pos, s));
-  if (!ws || ws_bytes < need || !aligned16(ws)) return MOE_ERR_WORKSPACE;
-  MOE_TRY(launch_positions(idx, T, E, k, (int32_t*)ws, offsets, pos, s));
+  if (!ws || ws_bytes < pl.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  int32_t* const scratch = (int32_t*)((char*)ws + pl.scratch);
+  if (pl.chunked)
+    MOE_TRY(launch_positions(idx, T, E, k, scratch, offsets, pos, s));
+  else
+    MOE_TRY(launch_dispatch(idx, T, E, k, (int32_t*)((char*)ws + pl.counts), offsets,
+                            (int32_t*)((char*)ws + pl.perm), pos, scratch, 0, nullptr,
+                            DispatchExtras(), s));
   return hip_status(launch_spread_rows(token_rows_of(pos, weights, T, D, k, T * k), elt_of(dt), x,
                                        rows, s));
 }

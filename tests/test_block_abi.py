@@ -41,6 +41,7 @@ def test_sort_workspace_size():
     n = C.c_size_t(0)
     L = moe.lib()
     assert L.moe_sort_tokens_workspace_size(4000, 8, 2, C.byref(n)) == OK and n.value >= 8 * 4
+    assert L.moe_sort_tokens_workspace_size(1 << 18, 1024, 2, C.byref(n)) == OK and n.value >= 8 << 18
     assert L.moe_sort_tokens_workspace_size(64, 8, 2, C.byref(n)) == OK and n.value == 0
     assert L.moe_sort_tokens_workspace_size(64, 2, 8, C.byref(n)) == OK   # a rank with few experts
     assert L.moe_sort_tokens_workspace_size(0, 8, 2, C.byref(n)) == OK
@@ -87,7 +88,7 @@ def test_unsort_backward_argument_errors(kw, code):
 INF, NAN = float("inf"), float("nan")
 BLOCK = [
     (dict(T=0), OK), (dict(T=-1), BAD), (dict(T=1 << 23), BAD), (dict(H=0), BAD),
-    (dict(H=24), BAD), (dict(H=16400), BAD), (dict(H=-16), BAD), (dict(eps=0.0), BAD),
+    (dict(H=24), BAD), (dict(H=16400), BAD), (dict(H=-16), BAD), (dict(eps=0.0), BAD), (dict(eps=1e-31), BAD),
     (dict(eps=-1.0), BAD), (dict(eps=NAN), BAD), (dict(eps=INF), BAD), (dict(dt=2), UNS),
     (dict(w_dt=3), UNS),
 ]

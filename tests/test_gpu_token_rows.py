@@ -114,6 +114,25 @@ def test_sort_and_back(T, k, E, D, stray, dtype):
             assert none is None and torch.equal(O.f64(dr3), O.spread(O.f64(dy), pos, None, O.f64(mark)))
 
 
+@pytest.mark.parametrize("T,k,E", [(2000, 2, 1), (70000, 3, 1024), (262144, 2, 1024), (300000, 1, 2)])
+def test_many_tokens(T, k, E):
+    """Every way the sort finds its positions, against a stable sort; some choices of no expert here
+    (the first slot's are distinct from the second's by their parity)."""
+    g = torch.Generator().manual_seed(T)
+    idx = torch.randint(0, max(1, E // k), (T, k), generator=g) * k + torch.arange(k)
+    idx = torch.where(torch.rand(T, k, generator=g) < 0.1, E + 3, idx).int().cuda()
+    x = rand(g, T, 16)
+    rows, offsets, pos = moe.sort_tokens(x, idx, E)
+    key = torch.where(idx < E, idx, E).flatten().long()
+    order = torch.sort(key, stable=True).indices
+    n = int((key < E).sum())
+    want = torch.full((T * k,), -1, dtype=torch.int32, device="cuda")
+    want[order[:n]] = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert torch.equal(pos.flatten(), want)
+    assert torch.equal(offsets[1:].long(), torch.bincount(key, minlength=E + 1)[:E].cumsum(0))
+    assert int(offsets[0]) == 0 and torch.equal(rows[:n], x[order[:n] // k])
+
+
 def test_no_tokens_and_no_rows():
     x = torch.empty(0, 32, device="cuda")
     idx = torch.empty(0, 2, dtype=torch.int32, device="cuda")
