@@ -6,11 +6,14 @@
 //   gradient of n at v against g:  r (g - n(v) mean(g n(v))), r = 1 / sqrt(mean(v^2) + eps)
 //
 // Bound by HBM: each row is read once and held in registers between its sums and its result, so
-// neither pass keeps statistics for the other. A row is held by 64 lanes (up to 2048 columns) or by
-// a workgroup of 128 to 512, at most 32 columns a lane. y is rounded before the next norm reads it:
-// the backward pass, which has y as it is stored, then differentiates the same function.
-// Sums run in fp32; where a sum of squares passes fp32 it is taken again of smaller values, a branch
-// that no ordinary row takes.
+// neither pass keeps statistics for the other. A row is held by 8 to 64 lanes of a wave, or by a
+// workgroup where it is long. y is rounded before the next norm reads it: the backward pass, which
+// has y as it is stored, then differentiates the same function. Sums run in fp32; where a sum of
+// squares passes fp32 it is taken again of smaller values, a branch that no ordinary row takes.
+// Measured (bf16; a copy of 4 GiB reaches 4.7 TB/s): forward with both norms and a gate per token, 8192
+// x 2688, 36 us, 4.9 TB/s; one row 4.4 us; backward with both norms and a gate per element, 8192 x 4096,
+// 98 us, 5.5 TB/s of operands and results, and 5.6 us for the weights' gradients; with a gate per token,
+// 8192 x 2688, 64 and 5 us.
 // Included once, by backward.hip.
 #pragma once
 
@@ -146,6 +149,7 @@ struct Place {
   __device__ __forceinline__ static int rows(int row, int T) { return min(T - row, kRowsOfWave<TPR>); }
 };
 
+// RES: y and, where p.h is given, the next norm of it; else h alone, the norm of x.
 template <Elt T, int TPR, int NC, bool RES>
 __global__ __launch_bounds__(kThreadsOf<TPR>) void block_forward_kernel(BlockShape b,
                                                                         BlockForward p) {
@@ -505,7 +509,10 @@ __global__ __launch_bounds__(kRedThreads) void block_reduce_kernel(const float* 
   }
 }
 
-// Lanes of a row and groups of eight columns a lane, forward and backward.
+// Lanes of a row and groups of eight columns a lane: the fewest lanes that leave registers for four
+// waves a SIMD, up to four groups forward, where a lane holds three operands, and two backward, where
+// it holds five, a gradient and two sums (four: 326 registers and one wave a SIMD). Microseconds with
+// two groups / one on twice the lanes: 8192 x 4096 108 / 106, 8192 x 2688 67 / 76, 16384 x 1024 44 / 51.
 template <typename Fn>
 void with_forward_shape(int H, Fn&& fn) {
   const int g = (H + 7) / 8;
@@ -543,12 +550,14 @@ void with_backward_shape(int H, Fn&& fn) {
 }
 
 // Workgroups of the backward pass: as many on each of the 256 CUs as its registers hold, since each
-// ends with a row of partial sums and a second round would leave most CUs idle.
+// ends with a row of partial sums and a second round would leave most CUs idle. Microseconds with 8 /
+// 12 / 16 waves a CU (two groups a lane): 8192 x 4096 108 / 108 / 119, 16384 x 1024 47 / 44 / 52, 16384 x
+// 4096 165 / 156 / 184; 8192 x 2688, 6 / 9 / 12 waves, 81 / 71 / 67.
 int backward_groups(int T, int H) {
   int groups = 0;
   with_backward_shape(H, [&](auto tpr, auto nc) {
     constexpr int TPR = tpr(), waves = kThreadsOf<TPR> / 64;
-    constexpr int most = TPR == 192 ? 9 : nc() == 1 ? 16 : 12;
+    constexpr int most = nc() == 1 ? 16 : 12;
     constexpr int per_cu = most / waves > 0 ? most / waves : 1;
     groups = std::min((T + kRowsOf<TPR> - 1) / kRowsOf<TPR>, 256 * per_cu);
   });
@@ -562,9 +571,9 @@ using namespace block_norm;
 
 // Operands and results that together pass the last-level cache (256 MB) are read past it, so that the
 // results, which the next call reads, stay. Microseconds with and without, the forward pass alone and
-// followed by a product that reads h: 16384 x 4096 (537 MB) 92 / 106 and 152 / 163, 8192 x 4096 52 / 55
+// followed by a product that reads h: 16384 x 4096 (537 MB) 93 / 109 and 152 / 163, 8192 x 4096 52 / 55
 // and 87 / 89, but 8192 x 2688 (176 MB) 38 / 37 and 64 / 62, 2048 x 2688 12.2 / 12.2 and 26.3 / 24.5.
-// The backward pass: 8192 x 4096 113 / 119, 4096 x 8192 100 / 105.
+// The backward pass: 8192 x 4096 108 / 122, 16384 x 4096 156 / 170, 4096 x 8192 99 / 102.
 bool past_cache(const BlockShape& b, int tensors) {
   return (int64_t)b.T * b.H * (b.t == Elt::BF16 ? 2 : 4) * tensors > (int64_t)256 << 20;
 }

@@ -10,7 +10,8 @@
 // the conversion hides under the loads, and no gradient over- or underflows on the way to the root.
 // Bound by HBM: the norm is needed before the first value can be written, so gradients are read
 // twice and written once, the second reading, last chunk first, from the last-level cache (256 MB)
-// where they fit.
+// where they fit. Measured: 2.19 GB of fp32 308 us (7.1 TB/s read) and 790 us (5.5 TB/s), 192 tensors of
+// 113 MB, bf16 and fp32, 21 and 36 us (5.4 and 6.2 TB/s); one launch on 4 MB about 3 us.
 // Included once, by backward.hip.
 #pragma once
 
@@ -134,7 +135,9 @@ __device__ __forceinline__ void scale(const Held& h, char* out, float coef) {
 
 // fn(chunk, what is held of it) for the chunks blockIdx.x, blockIdx.x + gridDim.x, .. (counted from
 // the last with BACK); the next chunk is loaded first. The second reading starts with the last chunks:
-// kKeep of them (240 MB) are read into the caches the first time, all others past them.
+// kKeep of them (240 MB) are read into the caches the first time, all others past them, as are the
+// second reading and the results. Microseconds with 0 / 128 / 192 / 240 MB kept: 268 MB of fp32 152 / 144 /
+// 138 / 135, 134 MB 77 / 70 / 71 / 70, 2.19 GB 1094 / 1091 / 1089 / 1089 (all through the caches: 166, 85 and 1172).
 constexpr int64_t kKeep = 15360;
 template <bool BACK, typename F>
 __device__ __forceinline__ void walk(const ClipChunk* table, int64_t chunks, F&& fn) {
