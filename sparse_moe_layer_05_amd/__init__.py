@@ -1,5 +1,6 @@
 """Sparse Mixture-of-Experts layer (Nemotron 3 MoE and LatentMoE) for MI355X / gfx950: the
-forward pass, and the backward pass of the plain bf16 layer.
+forward pass, the backward pass of the bf16 layer, and the operators around it (token rows in
+expert order, the residual block's norms, gradient clipping).
 
 The layer runs in hand-written HIP kernels behind the C ABI declared in include/moe.h
 (libmoe_mi355x.so, built in-tree by ``python -m sparse_moe_layer_05_amd.build``). This package

@@ -341,7 +341,7 @@ __global__ __launch_bounds__(256) void sort_small_kernel(const int32_t* __restri
 // What the cuts of a column add up to, and the waves' shares of a dot product, are joined through
 // LDS in wave order. Microseconds without cuts / with (24 slots, 1024 bf16 columns; gated sum, its
 // gradients, the sort's): 64 tokens 4.8 / 4.4, 7.3 / 5.5 and 7.0 / 5.4; 1001 tokens 11.8 / 12.1, 24.3 / 24.6
-// and 14.1 / 13.8.
+// and 14.1 / 13.8, the gated sum of fp32 rows with a quarter of the pairs kept 9.8 / 7.5.
 enum class Pass { Gather, GatherDot, SpreadDot, Spread };
 constexpr int kMostWaves = 16;
 // Gather, GatherDot: out[t] = add[t] + sum_j w rows[pos] (add, out: IN). SpreadDot: out[pos] = w a[t]
@@ -512,8 +512,8 @@ bool past_cache(const TokenRows& p, Elt a, Elt rows, int row_passes) {
   auto bytes = [](Elt t) { return t == Elt::BF16 ? 2 : 4; };
   return (int64_t)p.T * p.D * (bytes(a) + (int64_t)p.k * bytes(rows) * row_passes) > (int64_t)256 << 20;
 }
-// Units for every SIMD: with as many, pairs are not cut.
-constexpr int64_t kFull = 1024;
+// Units that fill the chip with eight waves a SIMD: with as many, pairs are not cut.
+constexpr int64_t kFull = 8192;
 struct Waves {
   int segs, cuts;
 };
