@@ -373,8 +373,8 @@ int32_t moe_unsort_tokens_backward(const void *dy, moe_dtype_t dy_dt, const void
  *            ([T, H] of type dt, MOE_GATE_ELEMENT), or its sigmoid (MOE_GATE_SIGMOID);
  *            h = n(y) w_next, of y as it is stored (h NULL: not wanted).
  * x, f, y, h [T, H] of type dt (MOE_BF16 or MOE_F32); w, w_next [H] of type w_dt, or NULL for 1.
- * y may be x or f, and h may be x (before). Sums run in fp32 (in fp64 where squares pass it), each
- * result is rounded once. A row that holds a NaN or an infinity reaches no other row of y and h.
+ * y may be x or f, and h may be x (before). Sums run in fp32 (where squares pass it, of smaller
+ * values), each result is rounded once. A row that holds a NaN or an infinity reaches no other row of y and h.
  * H a multiple of 16 up to 16384, T < 2^23, eps >= 1e-30. Errors: MOE_ERR_INVALID_ARG (null or
  * misaligned pointer, bad size or flags, a gate without its flag), MOE_ERR_UNSUPPORTED (types). */
 #define MOE_BLOCK_NORM 1u

@@ -27,9 +27,10 @@ def _ptr(t, shape, what, dtype, device):
 
 
 def _two(t, what):
-    if t.dim() != 2:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected two dimensions")
-    return t.shape
+    s = t.shape
+    if len(s) != 2 or max(s) > 0x7FFFFFFF:   # the library takes 32-bit sizes
+        raise ValueError(f"{what} has shape {tuple(s)}, expected two dimensions below 2^31")
+    return s
 
 
 # ------------------------------------------------------------------------------- token rows

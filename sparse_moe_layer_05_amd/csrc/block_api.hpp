@@ -272,7 +272,8 @@ int32_t moe_block_residual_backward(const void* dy, const void* f, const void* w
   if ((rc = block_workspace(b, dw || dw_next, ws, ws_bytes))) return rc;
   BlockBackward p;
   p.dy = dy; p.f = f; p.w = w; p.gate = gate; p.y = y; p.dh = dh; p.dh_t = elt_of(dh_dt);
-  p.w_next = w_next; p.dx = dx; p.df = df; p.dw = dw; p.dgate = dgate; p.dw_next = dw_next;
+  p.w_next = dh ? w_next : nullptr;   // (without dh nothing may meet it)
+  p.dx = dx; p.df = df; p.dw = dw; p.dgate = dgate; p.dw_next = dw_next;
   p.part = (float*)ws;
   return hip_status(launch_block_backward(b, p, (hipStream_t)stream));
 }

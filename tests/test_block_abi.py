@@ -221,6 +221,7 @@ def test_binding_refuses_what_does_not_fit():
             lambda: moe.unsort_tokens_backward(z(4, 32), i(4, 2), rows=z(8, 16)),
             lambda: moe.unsort_tokens_backward(z(4, 32), i(4, 2), rows=z(8, 32), out=z(9, 32)),
             lambda: moe.unsort_tokens_backward(z(4, 32), i(4, 2), out=z(8, 32, d=bf)),
+            lambda: moe.unsort_tokens(torch.empty(1, 16).expand(1 << 32, 16), i(4, 2)),
             lambda: moe.block_norm(z(4, 32)),
             lambda: moe.block_norm(z(32)),
             lambda: moe.block_norm(z(4, 32), z(16)),

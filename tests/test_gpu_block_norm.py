@@ -150,6 +150,21 @@ def test_only_the_next_norm_has_a_gradient():
         O.check(got[n], *ref[n][:1], F32, ref[n][1], GRAD + SUM, n)
 
 
+def test_next_weights_without_their_gradient_are_not_met():
+    """The C call takes w_next where dh is absent: nothing of it may reach dx or df."""
+    T, H = 5, 48
+    g = torch.Generator().manual_seed(15)
+    f, dy = rand(g, T, H), rand(g, T, H)
+    wn = torch.full((H,), float("inf"), device="cuda")
+    dx, df = torch.empty_like(f), torch.empty_like(f)
+    rc = moe.lib().moe_block_residual_backward(
+        dy.data_ptr(), f.data_ptr(), None, None, None, None, 0, wn.data_ptr(), dx.data_ptr(),
+        df.data_ptr(), None, None, None, T, H, 0, 0, 1, 1.0, EPS, None, 0, None)
+    torch.cuda.synchronize()
+    want = moe.block_residual_backward(dy, f)
+    assert rc == 0 and torch.equal(dx, want["dx"]) and torch.equal(df, want["df"])
+
+
 def test_no_tokens():
     x = torch.empty(0, 64, dtype=BF, device="cuda")
     w = torch.ones(64, device="cuda")
