@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+from array import array
 
 import torch
 
@@ -348,21 +349,23 @@ class GradClip:
         if len(outs) != len(grads):
             raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
         dev = grads[0].device
-        table = (MoeClipTensor * len(grads))()
-        spans = []
-        for i, (g, o) in enumerate(zip(grads, outs)):
+        flat, spans = array("q"), []     # MoeClipTensor: three 64-bit words and the type, padded
+        for g, o in zip(grads, outs):
             n, dtype = g.numel(), g.dtype
             dt = _float_code(dtype)
-            gp = op = _ptr(g, g.shape, "a gradient", dtype, dev)
+            if g.device != dev:
+                raise ValueError(f"a gradient is on {g.device}, another on {dev}")
+            gp = op = _p(g)
             if o is not g:
                 op = _ptr(o, g.shape, "an output", dtype, dev)
-            table[i] = (gp, op, n, dt)
+            flat.extend((gp, op, n, dt))
             if n:
                 size = n * (2 if dt == MOE_BF16 else 4)
                 if op != gp:
                     spans.append((gp, gp + size, False))
                 spans.append((op, op + size, True))
         _check_apart(spans)
+        table = (MoeClipTensor * len(grads)).from_buffer(flat)
         n = C.c_size_t(0)
         _check(lib().moe_clip_plan_size(table, len(grads), C.byref(n)), "moe_clip_plan_size")
         self._keep = (grads, outs)
