@@ -393,7 +393,8 @@ int32_t moe_block_residual(const void *x, const void *f, const void *w, const vo
  * was no next norm. dh has type dh_dt: dt, or MOE_F32 (what moe_layer_backward makes of the layer's
  * input). dw, dw_next [H] fp32, dgate: NULL where not wanted. The weights' gradients are summed over
  * the rows in fp32 in a fixed order (deterministic), through the workspace
- * (moe_block_backward_workspace_size bytes; only needed for them); T == 0 makes them 0. */
+ * (moe_block_backward_workspace_size bytes; only needed for them); T == 0 makes them 0. Rows may be of
+ * any finite size; sqrt(H) times dh w_next must stay in fp32. */
 int32_t moe_block_backward_workspace_size(int32_t T, int32_t H, size_t *bytes);
 int32_t moe_block_norm_backward(const void *dh, moe_dtype_t dh_dt, const void *x, const void *w,
                                 const void *dres, void *dx, float *dw, int32_t T, int32_t H,

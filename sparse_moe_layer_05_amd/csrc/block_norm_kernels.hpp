@@ -121,6 +121,29 @@ __device__ __forceinline__ float row_inv_rms(Raw8<T> (&v)[NC], float ss, int H, 
   return inv_rms(ss, H, eps);
 }
 
+// The gradient's mean(g n(v)) is taken as sum(g v) r / H, in the same reduction as sum(v^2). Where that
+// leaves fp32, though the mean does not, or is so small that products of it may have been subnormal
+// (16384 of them lose 2^-136 in all, 2^-36 of kLeastDot), or zero, as in a row without a gradient, it is
+// taken again of the normalised row: sum(g n) / H, or sum(g (n / H)) unless the sum is small.
+constexpr float kLeastDot = 0x1p-100f;
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
+template <int TPR, Elt T, int NC>
+__device__ __forceinline__ float far_mean(const float (&g)[NC][8], Raw8<T> (&v)[NC], float r, bool small,
+                                          float inv_h, RowSum<TPR>& sum) {
+  const float part = small ? 1.f : inv_h;
+  float q[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    float u[8];
+    forget(v[i]);
+    unpack8<T>(v[i], u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[0] = fmaf(g[i][e], u[e] * r * part, q[0]);
+  }
+  sum(q);
+  return small ? q[0] * inv_h : q[0];
+}
+
 // Where a lane works: rows of TPR lanes each, several of them side by side in a wave where they are
 // short, and four waves a workgroup unless a row needs a workgroup of its own.
 template <int TPR> constexpr int kThreadsOf = TPR <= 64 ? 256 : TPR;
@@ -322,23 +345,9 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
     sum(s);
     if (p.dh) {
       float r = inv_rms(s[0], b.H, b.eps), m = s[1] * r * inv_h;
-      if (__builtin_expect(too_big(s[0]), 0)) {
-        float q[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          float y[8];
-          forget(yr[i]);
-          unpack8<T>(yr[i], y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            q[0] = fmaf(y[e] * kFar, y[e] * kFar, q[0]);
-            q[1] = fmaf(d[i][e], y[e] * kFar, q[1]);
-          }
-        }
-        sum(q);
-        const float far = inv_rms_far(q[0], b.H, b.eps);
-        r = far * kFar;
-        m = q[1] * far * inv_h;
+      if (__builtin_expect(too_big(s[0]) || !(fabsf(s[1]) >= kLeastDot) || !finite(m), 0)) {
+        r = row_inv_rms<TPR, T, NC>(yr, s[0], b.H, b.eps, sum);
+        m = far_mean<TPR, T, NC>(d, yr, r, fabsf(s[1]) * r < 1.f, inv_h, sum);
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
