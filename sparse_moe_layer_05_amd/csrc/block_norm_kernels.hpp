@@ -124,7 +124,8 @@ __device__ __forceinline__ float row_inv_rms(Raw8<T> (&v)[NC], float ss, int H, 
 // The gradient's mean(g n(v)) is taken as sum(g v) r / H, in the same reduction as sum(v^2). Where that
 // leaves fp32, though the mean does not, or is so small that products of it may have been subnormal
 // (16384 of them lose 2^-136 in all, 2^-36 of kLeastDot), or zero, as in a row without a gradient, it is
-// taken again of the normalised row: sum(g n) / H, or sum(g (n / H)) unless the sum is small.
+// taken again of the normalised row: sum(g n) / H, or sum(g (n / H)) unless the sum is small. (The norm of
+// f sums g n(f) at once, which only large gradients take out of fp32.)
 constexpr float kLeastDot = 0x1p-100f;
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
 template <int TPR, Elt T, int NC>
@@ -423,7 +424,8 @@ __global__ __launch_bounds__(kThreadsOf<TPR>) void block_backward_kernel(BlockSh
       if (b.norm || token) sum(q);
       if (token && me.lane == 0 && row < b.T && p.dgate)
         ((float*)p.dgate)[row] = q[0] * gt.rest * (b.sigmoid ? gt.a : 1.f);
-      const float m = b.norm ? q[0] * gt.a * inv_h : 0.f;   // (gt.a is 1 but for a token's gate)
+      float m = b.norm ? q[0] * gt.a * inv_h : 0.f;   // (gt.a is 1 but for a token's gate)
+      if (__builtin_expect(!finite(m), 0)) m = far_mean<TPR, T, NC>(d, fr, rf, false, inv_h, sum);
       const RowBuffer<T> fo(p.df, row0, rows, b.H);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {

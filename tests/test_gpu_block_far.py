@@ -61,6 +61,23 @@ def test_gradients_along_their_row(H, dtype):
                 O.norm_grad(O.f64(dh), O.f64(x), 1e-12, mag=True), GRAD, size)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", WIDTHS)
+def test_residual_gradients_along_their_row(H, dtype):
+    """The same of the output's norm: dy along f. A gate per token scales the sum after it is taken."""
+    g = torch.Generator().manual_seed(H + 3)
+    f, dy = near(g, 4, H, 1.0, dtype), near(g, 4, H, 1e39 / H, dtype)
+    tiny = torch.tensor([0.0, 1e-30, 1e-3, 0.5]).cuda()
+    for gate in (None, near(g, 4, H, 1.0, dtype), tiny):
+        got = moe.block_residual_backward(dy, f, gate=gate, gate_act="none")
+        ref = O.residual_grad(O.f64(dy), O.f64(f), None, True, O.f64(gate), "none", 1.0, None, None, None, 1e-5)
+        for n in got:
+            if n == "dgate" and gate is tiny:       # H times dy: past fp32 by itself
+                assert bool(torch.isinf(got[n]).all())
+                continue
+            O.check(got[n], ref[n][0], dtype, ref[n][1], GRAD + SUM, n)
+
+
 @pytest.mark.parametrize("dtype,dh_dtype", [(BF, BF), (BF, F32), (F32, F32)])
 @pytest.mark.parametrize("H", [64, 304, 2704])
 def test_residual_gradients_of_far_rows(H, dtype, dh_dtype):
