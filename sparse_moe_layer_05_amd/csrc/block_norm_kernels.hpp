@@ -79,14 +79,15 @@ struct GateValue {
 };
 __device__ __forceinline__ GateValue gate_value(float q, bool sigmoid) {
   if (!sigmoid) return {q, 1.f};
-  // exp(-|q|) = 2^t (1 + r ln 2), t + r = -|q| log2(e) to 48 bits; below 2^-149 it is 0 (a NaN stays)
-  const float x = q < -104.f || q > 104.f ? -104.f : -fabsf(q);
-  const float t = x * 1.44269502f;
-  const float r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));
-  const float p2 = __builtin_amdgcn_exp2f(t), e = fmaf(p2 * r, 0.693147182f, p2);
-  // 1 / (1 + e), 1 + e in [1, 2]: the hardware's reciprocal and one Newton step
-  const float u = 1.f + e, v = __builtin_amdgcn_rcpf(u), inv = fmaf(v, fmaf(-u, v, 1.f), v);
-  return q < 0.f ? GateValue{e * inv, inv} : GateValue{inv, e * inv};
+  // p = exp(-|q| / 2) = 2^t (1 + r ln 2), t + r = -|q| log2(e) / 2 to 48 bits, and exp(-|q|) = p p: the
+  // hardware's 2^t has no subnormal results, a product has. From 104 on p p rounds to 0 (a NaN stays).
+  const float x = fabsf(q) > 104.f ? -104.f : -fabsf(q);
+  const float t = x * 0.72134751f;
+  const float r = fmaf(x, 9.62981515e-9f, fmaf(x, 0.72134751f, -t));
+  const float p2 = __builtin_amdgcn_exp2f(t), p = fmaf(p2 * r, 0.693147182f, p2);
+  // 1 / (1 + p p), 1 + p p in [1, 2]: the hardware's reciprocal and one Newton step
+  const float u = fmaf(p, p, 1.f), v = __builtin_amdgcn_rcpf(u), inv = fmaf(v, fmaf(-u, v, 1.f), v);
+  return q < 0.f ? GateValue{p * (p * inv), inv} : GateValue{inv, p * (p * inv)};
 }
 
 __device__ __forceinline__ float inv_rms(float ss, int H, float eps) {
