@@ -135,8 +135,16 @@ def unsort_tokens_backward(dy, pos, *, rows=None, weights=None, n_rows=None, out
     dev = dy.device
     dyt = _float_code(dy.dtype)
     k, pp, wp = _pairs(pos, weights, T, dev)
-    like = rows if rows is not None else out
-    n = n_rows if n_rows is not None else like.shape[0] if like is not None else T * k
+    if rows is not None:
+        like, n = rows, _two(rows, "rows")[0]
+    elif out is not None:
+        like, n = out, _two(out, "out")[0]
+    else:
+        like, n = None, T * k
+    if n_rows is not None:
+        n = n_rows
+    if not 0 <= n <= 0x7FFFFFFF:             # as _two
+        raise ValueError(f"n_rows is {n}, expected 0 to 2^31 - 1")
     dtype = like.dtype if like is not None else dy.dtype
     dt = _float_code(dtype)
     rp = dw = None

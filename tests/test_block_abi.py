@@ -329,3 +329,22 @@ def test_row_gradients_against_differences():
     back = lambda rows, w: float((cy * O.gather(rows, pos, w, x, T, D)).sum())  # noqa: E731
     assert torch.allclose(differences(lambda t: back(t, w), rows), O.spread(cy, pos, w, zero), atol=1e-7)
     assert torch.allclose(differences(lambda t: back(rows, t), w), O.dots(cy, rows, pos), atol=1e-7)
+
+
+# ------------------------------------------- sizes that the library's 32-bit arguments do not hold
+
+def test_rows_past_32_bits_are_refused():
+    """A size is passed as 32 bits: 2^32 + 8 must not arrive as 8."""
+    f32 = torch.float32
+    z = lambda *s: torch.zeros(s, dtype=f32)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    long = torch.empty(1, 16).expand((1 << 32) + 8, 16)
+    for call, word in (
+            (lambda: moe.unsort_tokens_backward(z(4, 16), i(4, 2), rows=long), "2^31"),
+            (lambda: moe.unsort_tokens_backward(z(4, 16), i(4, 2), out=long), "2^31"),
+            (lambda: moe.unsort_tokens_backward(z(4, 16), i(4, 2), n_rows=(1 << 32) + 8), "n_rows"),
+            (lambda: moe.unsort_tokens_backward(z(4, 16), i(4, 2), n_rows=-1), "n_rows"),
+            (lambda: moe.unsort_tokens_backward(z(4, 16), i(4, 2), rows=z(8, 16), n_rows=9), "expected"),
+            (lambda: moe.unsort_tokens_backward(z(4, 16), i(4, 2), rows=z(8)), "two dimensions")):
+        with pytest.raises(ValueError, match=word.replace("^", r"\^")):
+            call()
