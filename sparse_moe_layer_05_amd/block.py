@@ -62,6 +62,9 @@ def sort_tokens(x, idx, E, *, weights=None, out=None, stream=None):
     dev, dtype = x.device, x.dtype
     dt = _float_code(dtype)
     k, ip, wp = _pairs(idx, weights, T, dev, "idx")
+    if not -1 < E < 0x80000000:              # as _two
+        raise ValueError(f"E is {E}, expected the number of experts")
+    n = _sort_workspace(T, E, k)
     if out is None:
         rows = x.new_empty((T * k, D))
         rp = rows.data_ptr()
@@ -69,7 +72,6 @@ def sort_tokens(x, idx, E, *, weights=None, out=None, stream=None):
         rows, rp = out, _ptr(out, (T * k, D), "out", dtype, dev)
     offsets = idx.new_empty(E + 1)
     pos = torch.empty_like(idx)
-    n = _sort_workspace(T, E, k)
     ws = x.new_empty(n, dtype=torch.uint8) if n else None
     _launch(lib().moe_sort_tokens, "moe_sort_tokens", dev, stream, _p(x), dt, ip, wp, T, D, E, k, rp,
             offsets.data_ptr(), pos.data_ptr(), ws.data_ptr() if n else None, n)

@@ -348,3 +348,14 @@ def test_rows_past_32_bits_are_refused():
             (lambda: moe.unsort_tokens_backward(z(4, 16), i(4, 2), rows=z(8)), "two dimensions")):
         with pytest.raises(ValueError, match=word.replace("^", r"\^")):
             call()
+
+
+def test_numbers_of_experts_that_there_cannot_be_are_refused_first():
+    """Before anything of that size is allocated, and none arrives as another one."""
+    x, idx = torch.zeros(4, 32), torch.zeros(4, 2, dtype=torch.int32)
+    for E in ((1 << 32) + 8, (1 << 31) + 1, -5):
+        with pytest.raises(ValueError, match="E is"):
+            moe.sort_tokens(x, idx, E)
+    for E in (0, 1025, (1 << 31) - 1):
+        with pytest.raises(moe.MoeError):
+            moe.sort_tokens(x, idx, E)
