@@ -396,7 +396,8 @@ class Backward:
 
     def clip(self, max_norm, stream=None):
         """Clips the weight gradients of the last call in place by their global norm, which is
-        returned (GradClip over self.grads without dx, made on the first call: outside a capture)."""
+        returned (GradClip over self.grads without dx, made on the first call: outside a capture; see
+        there for calls on other streams)."""
         if self._clip is None:
             from .block import GradClip
             if torch.cuda.is_current_stream_capturing():

@@ -27,6 +27,25 @@ def _ptr(t, shape, what, dtype, device):
     return _p(t)
 
 
+def _raw(stream, device):
+    """Raw handle of the stream that _launch takes."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _torch_stream(stream, device):
+    """The same as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
+def _is_capturing(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _two(t, what):
     s = t.shape
     if len(s) != 2 or max(s) > 0x7FFFFFFF:   # the library takes 32-bit sizes
@@ -348,6 +367,8 @@ class GradClip:
     grad * min(1, max_norm / (norm + 1e-6)) into the gradients, or into ``out`` (as many tensors of
     the same shapes and types), and returns the norm (a float32 tensor that the next call
     overwrites; ``coef`` is beside it). A norm that is not finite leaves the values as they are.
+    A call on another stream than the constructor's waits for the constructor's work, unless that
+    stream is captured: a graph is then replayed after it, and the object kept as long as the graph.
     Calls of one GradClip must not overlap; one that was made while a stream was captured serves
     that capture alone (its table is written by the graph). See moe_clip_plan in moe.h."""
 
@@ -384,19 +405,30 @@ class GradClip:
         self.clip = MoeClip()
         _launch(lib().moe_clip_plan, "moe_clip_plan", dev, stream, table, len(grads), _p(self.plan),
                 n.value, C.byref(self.clip))
-        both = grads[0].new_empty(2, dtype=torch.float32)
+        self._both = both = grads[0].new_empty(2, dtype=torch.float32)
         if stream is not None:
             _used_on(stream, self.plan, both)
         self.norm, self.coef = both[0], both[1]
         self._args = (C.byref(self.clip), both.data_ptr())
         self._captured = torch.cuda.is_current_stream_capturing()
+        self._made_on, self._ready = _raw(stream, dev), None
+        if not self._captured:
+            self._ready = torch.cuda.Event()
+            self._ready.record(_torch_stream(stream, dev))
 
     def __call__(self, max_norm, stream=None):
         if self._captured and not torch.cuda.is_current_stream_capturing():
             raise ValueError("this GradClip was made while a stream was captured and serves that "
                              "capture alone")
         clip, norm = self._args
+        other = _raw(stream, self.device) != self._made_on
+        if other:
+            stream = _torch_stream(stream, self.device)
+            if self._ready is not None and not _is_capturing(stream):
+                stream.wait_event(self._ready)
         _launch(lib().moe_clip_grads, "moe_clip_grads", self.device, stream, clip, max_norm, norm)
+        if other:      # the plan holds addresses that the kernels write through
+            _used_on(stream, self.plan, self._both)
         return self.norm
 
 
