@@ -420,9 +420,10 @@ int32_t moe_block_residual_backward(const void *dy, const void *f, const void *w
  * moe_clip_plan writes their table into `plan` (device, moe_clip_plan_size bytes, 32-byte aligned)
  * by kernels on `stream` and fills `clip` (host). moe_clip_grads, on that stream or ordered behind
  * it, may then be called any number of times while the tensors and the plan stay in place; calls
- * that share a plan must not overlap. It reads `plan` for scratch too. Errors: MOE_ERR_INVALID_ARG
- * (null or misaligned pointer, bad size, max_norm < 0 or NaN), MOE_ERR_UNSUPPORTED (types),
- * MOE_ERR_WORKSPACE (plan missing, misaligned or too small). */
+ * that share a plan must not overlap. A plan made on a stream that is captured is written by the
+ * graph's replays alone: calls outside of that capture are refused. It uses `plan` for scratch too. Errors: MOE_ERR_INVALID_ARG
+ * (null or misaligned pointer, bad size, max_norm < 0 or NaN, another capture's plan),
+ * MOE_ERR_UNSUPPORTED (types), MOE_ERR_WORKSPACE (plan missing, misaligned or too small). */
 typedef struct {
   void *grad;        /* device */
   void *out;         /* device; NULL: grad */
@@ -433,7 +434,7 @@ typedef struct {     /* filled by moe_clip_plan */
   void *plan;
   int64_t chunks;
   int32_t in_place;
-  int32_t reserved;
+  int32_t capture;   /* 0, or which stream capture the table is written by */
 } moe_clip_t;
 int32_t moe_clip_plan_size(const moe_clip_tensor_t *tensors, int32_t count, size_t *bytes);
 int32_t moe_clip_plan(const moe_clip_tensor_t *tensors, int32_t count, void *plan,

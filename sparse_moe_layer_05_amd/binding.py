@@ -70,7 +70,7 @@ class MoeClipTensor(C.Structure):
 
 class MoeClip(C.Structure):
     _fields_ = [("plan", C.c_void_p), ("chunks", C.c_int64), ("in_place", C.c_int32),
-                ("reserved", C.c_int32)]
+                ("capture", C.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -399,8 +399,8 @@ class Backward:
         returned (GradClip over self.grads without dx, made on the first call: outside a capture; see
         there for calls on other streams)."""
         if self._clip is None:
-            from .block import GradClip
-            if torch.cuda.is_current_stream_capturing():
+            from .block import GradClip, _is_capturing, _torch_stream
+            if _is_capturing(_torch_stream(stream, self.ws.device)):
                 raise ValueError("the first clip() makes its table: call it once before a capture")
             self._clip = GradClip({n: g for n, g in self.grads.items() if n != "dx"}, stream=stream)
         return self._clip(max_norm, stream)

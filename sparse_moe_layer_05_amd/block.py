@@ -10,8 +10,8 @@ from array import array
 
 import torch
 
-from .binding import (MOE_BF16, Layer, MoeClip, MoeClipTensor, _check, _float_code, _launch, _need,
-                      _p, _used_on, lib)
+from .binding import (MOE_BF16, Layer, MoeClip, MoeClipTensor, MoeError, _check, _float_code,
+                      _launch, _need, _p, _used_on, lib)
 
 BLOCK_NORM, GATE_TOKEN, GATE_ELEMENT, GATE_SIGMOID = 1, 2, 4, 8
 _F32, _I32 = torch.float32, torch.int32
@@ -410,23 +410,25 @@ class GradClip:
             _used_on(stream, self.plan, both)
         self.norm, self.coef = both[0], both[1]
         self._args = (C.byref(self.clip), both.data_ptr())
-        self._captured = torch.cuda.is_current_stream_capturing()
         self._made_on, self._ready = _raw(stream, dev), None
-        if not self._captured:
+        if not self.clip.capture:
             self._ready = torch.cuda.Event()
             self._ready.record(_torch_stream(stream, dev))
 
     def __call__(self, max_norm, stream=None):
-        if self._captured and not torch.cuda.is_current_stream_capturing():
-            raise ValueError("this GradClip was made while a stream was captured and serves that "
-                             "capture alone")
         clip, norm = self._args
         other = _raw(stream, self.device) != self._made_on
         if other:
             stream = _torch_stream(stream, self.device)
             if self._ready is not None and not _is_capturing(stream):
                 stream.wait_event(self._ready)
-        _launch(lib().moe_clip_grads, "moe_clip_grads", self.device, stream, clip, max_norm, norm)
+        try:
+            _launch(lib().moe_clip_grads, "moe_clip_grads", self.device, stream, clip, max_norm, norm)
+        except MoeError as e:
+            if self.clip.capture and max_norm >= 0:
+                raise ValueError("this GradClip was made while a stream was captured and serves that "
+                                 "capture alone") from e
+            raise
         if other:      # the plan holds addresses that the kernels write through
             _used_on(stream, self.plan, self._both)
         return self.norm

@@ -106,6 +106,18 @@ int32_t clip_check(const moe_clip_tensor_t* t, int32_t count, int64_t* chunks) {
   return MOE_OK;
 }
 
+// Which capture the stream is in: 0 for none, else its number with the sign bit set.
+int32_t capture_of(hipStream_t s, int32_t* capture) {
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (hipStreamGetCaptureInfo(s, &status, &id) != hipSuccess) {
+    (void)hipGetLastError();
+    return MOE_ERR_HIP;
+  }
+  *capture = status == hipStreamCaptureStatusActive ? (int32_t)((uint32_t)id | 0x80000000u) : 0;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -294,6 +306,9 @@ int32_t moe_clip_plan(const moe_clip_tensor_t* tensors, int32_t count, void* pla
   if (!clip) return MOE_ERR_INVALID_ARG;
   if (!plan || !aligned32(plan) || plan_bytes < kClipPartial + (size_t)chunks * sizeof(ClipChunk))
     return MOE_ERR_WORKSPACE;
+  int32_t capture = 0;
+  const int32_t e = capture_of((hipStream_t)stream, &capture);
+  if (e && chunks) return e;   // (nothing to write: nothing that a GPU is needed for)
   ClipChunk* table = (ClipChunk*)((char*)plan + kClipPartial);
   ClipBatch batch;
   memset(&batch, 0, sizeof(batch));
@@ -318,7 +333,7 @@ int32_t moe_clip_plan(const moe_clip_tensor_t* tensors, int32_t count, void* pla
   clip->plan = plan;
   clip->chunks = chunks;
   clip->in_place = in_place;
-  clip->reserved = 0;
+  clip->capture = capture;
   return MOE_OK;
 }
 
@@ -326,6 +341,12 @@ int32_t moe_clip_grads(const moe_clip_t* clip, float max_norm, float* norm, void
   if (!clip || !clip->plan || !aligned32(clip->plan) || clip->chunks < 0 ||
       clip->chunks > kClipMaxChunks || !norm || ((uintptr_t)norm & 3) || !(max_norm >= 0.f))
     return MOE_ERR_INVALID_ARG;
+  if (clip->capture) {
+    int32_t now = 0;
+    const int32_t e = capture_of((hipStream_t)stream, &now);
+    if (e) return e;
+    if (now != clip->capture) return MOE_ERR_INVALID_ARG;
+  }
   return hip_status(launch_clip((const ClipChunk*)((const char*)clip->plan + kClipPartial),
                                 clip->chunks, clip->in_place != 0, max_norm, (double*)clip->plan,
                                 norm, (hipStream_t)stream));

@@ -3,8 +3,8 @@ kernels follow addresses in stays theirs. The first tests replace the GPU by a r
 import pytest
 import torch
 
+import moe_inputs as mi
 import sparse_moe_layer_05_amd as moe
-from sparse_moe_layer_05_amd import binding as B
 from sparse_moe_layer_05_amd import block as K
 
 
@@ -139,7 +139,6 @@ def test_a_call_waits_for_a_table_made_on_another_stream(side, how):
 
 @pytest.mark.gpu
 def test_clip_of_a_backward_on_other_streams(side):
-    import moe_inputs as mi
     dev = moe.to_device(mi.make_layer(mi.LayerConfig("c", T=8, H=32, E=4, k=2, I=16), seed=0))
     back = moe.backward_from(dev, 2)
     dy = torch.randn(8, 32, device="cuda").to(torch.bfloat16)
@@ -166,3 +165,50 @@ def test_a_captured_call_of_a_table_made_before(side):
         true = (3.0 + turn) * 300 ** 0.5
         assert abs(float(norm) - true) <= 1e-6 * true
         assert abs(float(grads[0].double().norm()) - 1.0) <= 1e-5
+
+
+@pytest.mark.gpu
+def test_a_table_made_in_a_capture_is_refused_in_another(side):
+    """Only replays of the first graph write the table: in the second one it may be anything."""
+    grads = [torch.randn(200, device="cuda")]
+    first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        clip = moe.GradClip(grads)
+        clip(1.0)
+    with torch.cuda.graph(second):
+        grads[0].mul_(2.0)
+        with pytest.raises(ValueError, match="capture"):
+            clip(1.0)
+    with pytest.raises(ValueError, match="capture"):
+        clip(1.0)
+    with pytest.raises(moe.MoeError):
+        clip(-1.0)
+    for g in (first, second, first):
+        g.replay()
+    torch.cuda.synchronize()
+    assert abs(float(grads[0].double().norm()) - 1.0) <= 1e-5
+
+
+@pytest.mark.gpu
+def test_a_captured_stream_that_is_not_the_current_one(side):
+    """The stream that is given decides, not the current one."""
+    grads = [torch.randn(200, device="cuda")]
+    dev = moe.to_device(mi.make_layer(mi.LayerConfig("c", T=8, H=32, E=4, k=2, I=16), seed=0))
+    back = moe.backward_from(dev, 2)
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(other):                   # memory of that stream, which a capture cannot get
+        held = torch.zeros(1000, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        grads[0].mul_(1.0)
+        with torch.cuda.stream(other):
+            with pytest.raises(ValueError, match="capture"):
+                back.clip(1.0, stream=side)
+            clip = moe.GradClip(grads, stream=side)
+            clip(1.0, stream=side)
+    with pytest.raises(ValueError, match="capture"):
+        clip(1.0)
+    grads[0].fill_(1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert abs(float(grads[0].double().norm()) - 1.0) <= 1e-5 and held.numel() == 1000
