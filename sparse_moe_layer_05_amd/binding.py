@@ -185,6 +185,35 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
+def _raw(stream, device):
+    """Raw handle of the stream that _launch takes."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if device.type == "cuda" else 0
+
+
+def _torch_stream(stream, device):
+    """The same as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
+class _Own:
+    """What a prepared call has allocated. Marked as in use on every other stream that the call runs
+    on, it is not handed out again before that stream's work ends, though the object be dropped."""
+
+    def __init__(self, device, *tensors):
+        self.device, self.tensors = device, tensors
+        self.made_on = _raw(None, device)
+
+    def used_on(self, stream):
+        if _raw(stream, self.device) != self.made_on:
+            _used_on(_torch_stream(stream, self.device), *self.tensors)
+
+
 def _stream(stream):
     s = stream if stream is not None else torch.cuda.current_stream()
     return C.c_void_p(s.cuda_stream)
@@ -318,6 +347,7 @@ class Layer:
         self.fn_name = "moe_few_forward" if few else \
             "latent_moe_forward" if self.desc.latent else "moe_layer_forward"
         self.fn = getattr(lib(), self.fn_name)
+        self._own = _Own(x.device, self.ws, self.y if out is None else None)
 
     def __call__(self, stream=None):
         r = C.byref(self.r) if self.r is not None else None
@@ -325,9 +355,10 @@ class Layer:
             rc = lib().moe_layer_forward_static(C.byref(self.desc), C.byref(self.w), _p(self.y),
                                                 r, _stream(stream))
             _check(rc, "moe_layer_forward_static")
-            return self.y
-        _launch(self.fn, self.fn_name, self.y.device, stream, C.byref(self.desc), C.byref(self.w),
-                _p(self.y), _p(self.ws), self.ws_bytes, r)
+        else:
+            _launch(self.fn, self.fn_name, self.y.device, stream, C.byref(self.desc),
+                    C.byref(self.w), _p(self.y), _p(self.ws), self.ws_bytes, r)
+        self._own.used_on(stream)
         return self.y
 
 
@@ -367,18 +398,23 @@ class Backward:
                "moe_backward_workspace_size")
         self.ws_bytes = n.value
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=x.device)
+        self._own = _Own(x.device, self.ws, *self.grads.values())
         self._clip = None
 
     def forward_train(self, y=None, stream=None):
         """y of the layer (grouped path), keeping what the backward pass reads in the workspace:
         later calls with ``saved=True`` skip the recompute."""
         x = self._keep[0]
-        if y is None:
+        own = y is None
+        if own:
             y = torch.empty_like(x)
         _need(y, x.shape, "y", x.dtype, x.device)
         rc = lib().moe_layer_forward_train(C.byref(self.desc), C.byref(self.w), _p(y),
                                            _p(self.ws), self.ws_bytes, _stream(stream))
         _check(rc, "moe_layer_forward_train")
+        self._own.used_on(stream)
+        if own:
+            _used_on(stream, y)
         return y
 
     def __call__(self, dy, stream=None, saved=False):
@@ -392,6 +428,7 @@ class Backward:
         rc = lib().moe_layer_backward(C.byref(d), C.byref(self.w), _p(dy), C.byref(self.g),
                                       _p(self.ws), self.ws_bytes, _stream(stream))
         _check(rc, "moe_layer_backward")
+        self._own.used_on(stream)
         return self.grads
 
     def clip(self, max_norm, stream=None):
@@ -399,7 +436,7 @@ class Backward:
         returned (GradClip over self.grads without dx, made on the first call: outside a capture; see
         there for calls on other streams)."""
         if self._clip is None:
-            from .block import GradClip, _is_capturing, _torch_stream
+            from .block import GradClip, _is_capturing
             if _is_capturing(_torch_stream(stream, self.ws.device)):
                 raise ValueError("the first clip() makes its table: call it once before a capture")
             self._clip = GradClip({n: g for n, g in self.grads.items() if n != "dx"}, stream=stream)

@@ -11,7 +11,7 @@ from array import array
 import torch
 
 from .binding import (MOE_BF16, Layer, MoeClip, MoeClipTensor, MoeError, _check, _float_code,
-                      _launch, _need, _p, _used_on, lib)
+                      _launch, _need, _Own, _p, _raw, _torch_stream, _used_on, lib)
 
 BLOCK_NORM, GATE_TOKEN, GATE_ELEMENT, GATE_SIGMOID = 1, 2, 4, 8
 _F32, _I32 = torch.float32, torch.int32
@@ -25,20 +25,6 @@ def _ptr(t, shape, what, dtype, device):
     if t.shape != shape or t.dtype is not dtype or t.device != device:
         _need(t, shape, what, dtype, device)
     return _p(t)
-
-
-def _raw(stream, device):
-    """Raw handle of the stream that _launch takes."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-
-
-def _torch_stream(stream, device):
-    """The same as a torch stream."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if isinstance(stream, torch.Stream):
-        return stream
-    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
 
 
 def _is_capturing(stream):
@@ -476,10 +462,12 @@ class Block:
         self.h_next = torch.empty_like(x) if next_norm or w_next is not None else None
         self.after = dict(w=w_out, norm=norm_out, gate=gate, gate_act=gate_act, scale=scale,
                           w_next=w_next, eps=eps, out=self.y, h_out=self.h_next)
+        self._own = _Own(x.device, self.h if h is None else None, self.y, self.h_next)
 
     def __call__(self, stream=None):
         if self.own_norm:
             block_norm(self.x, self.w_in, eps=self.eps, out=self.h, stream=stream)
         f = self.layer(stream)
         block_residual(self.x, f, stream=stream, **self.after)
+        self._own.used_on(stream)
         return self.y
