@@ -180,3 +180,16 @@ def test_captured():
         torch.cuda.synchronize()
         true = norm_of(fresh[turn])
         assert abs(float(norm) - true) <= 1e-6 * true
+
+
+@pytest.mark.parametrize("dtype,chunk", [(F32, 4096), (BF, 8192)])
+def test_one_chunk_and_its_neighbours(dtype, chunk):
+    """A chunk is 16 KB: one element less, whole, one more, and the same of two chunks."""
+    g = torch.Generator().manual_seed(chunk)
+    for n in (chunk - 1, chunk, chunk + 1, 2 * chunk - 1, 2 * chunk, 2 * chunk + 1):
+        grads = tensors(g, [(n, dtype)])
+        before, outs = grads[0].clone(), [torch.empty_like(grads[0])]
+        clip = moe.GradClip(grads, out=outs)
+        check([before], outs, clip(1.0), clip.coef, 1.0)
+        clip = moe.GradClip(grads)
+        check([before], grads, clip(1.0), clip.coef, 1.0)

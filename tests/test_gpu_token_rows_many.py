@@ -150,3 +150,19 @@ def test_past_the_last_level_cache(T, D, k, dtype, other):
     """More than 256 MB of operands and results in each of the passes."""
     assert T * D * (2 + 2 * k) > 256 << 20
     run(T, D, k, 64, dtype, other, 0.0)
+
+
+@pytest.mark.parametrize("T,k,E", [(5000, 4, 3), (3000, 24, 512), (262144, 2, 1024)])
+def test_repeated_experts_of_many_tokens(T, k, E):
+    """The first of a token's pairs with an expert is kept, on every way to the positions."""
+    g = torch.Generator("cuda").manual_seed(T)
+    idx = torch.randint(-2, E + 2, (T, k), generator=g, device="cuda").int()
+    first = idx.clone()
+    for j in range(1, k):
+        first[:, j] = torch.where((idx[:, :j] == idx[:, j:j + 1]).any(1), -1, idx[:, j])
+    ends, want = positions(first, E)
+    x = make(g, T, 16)
+    rows, off, pos = moe.sort_tokens(x, idx, E)
+    assert torch.equal(pos, want) and torch.equal(off[1:].long(), ends)
+    n = int(ends[-1])
+    assert torch.equal(rows[:n], spread(x, want, None, torch.zeros_like(rows))[:n])
