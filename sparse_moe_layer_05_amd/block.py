@@ -358,6 +358,8 @@ class GradClip:
     Calls of one GradClip must not overlap; one that was made while a stream was captured serves
     that capture alone (its table is written by the graph). See moe_clip_plan in moe.h."""
 
+    _one_use = False
+
     def __init__(self, grads, *, out=None, stream=None):
         grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
         outs = grads if out is None else list(out.values()) if isinstance(out, dict) else list(out)
@@ -397,7 +399,7 @@ class GradClip:
         self.norm, self.coef = both[0], both[1]
         self._args = (C.byref(self.clip), both.data_ptr())
         self._made_on, self._ready = _raw(stream, dev), None
-        if not self.clip.capture:
+        if not (self.clip.capture or self._one_use):
             self._ready = torch.cuda.Event()
             self._ready.record(_torch_stream(stream, dev))
 
@@ -432,9 +434,14 @@ def _check_apart(spans):
             written = max(written, hi)
 
 
+class _OneUse(GradClip):
+    """Called on its constructor's stream alone, which needs no event."""
+    _one_use = True
+
+
 def clip_grad_norm(grads, max_norm, *, out=None, stream=None):
     """GradClip for one use: clips grads (or into out) and returns their norm."""
-    clip = GradClip(grads, out=out, stream=stream)
+    clip = _OneUse(grads, out=out, stream=stream)
     norm = clip(max_norm, stream)
     if stream is not None:
         _used_on(stream, *clip._keep[0], *clip._keep[1])
