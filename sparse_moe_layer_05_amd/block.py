@@ -440,7 +440,8 @@ class _OneUse(GradClip):
 
 
 def clip_grad_norm(grads, max_norm, *, out=None, stream=None):
-    """GradClip for one use: clips grads (or into out) and returns their norm."""
+    """GradClip for one use: clips grads (or into out) and returns their norm. The table is made anew
+    in every call, about 1.4 us of host time a tensor: where the tensors stay, keep a GradClip."""
     clip = _OneUse(grads, out=out, stream=stream)
     norm = clip(max_norm, stream)
     if stream is not None:

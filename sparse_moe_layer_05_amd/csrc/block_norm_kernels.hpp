@@ -5,15 +5,17 @@
 //   y = x + scale a z, z = n(f) w or f w, a = gate or sigmoid(gate) or 1;  h = n(y) w_next
 //   gradient of n at v against g:  r (g - n(v) mean(g n(v))), r = 1 / sqrt(mean(v^2) + eps)
 //
-// Bound by HBM: each row is read once and held in registers between its sums and its result, so
-// neither pass keeps statistics for the other. A row is held by 8 to 64 lanes of a wave, or by a
-// workgroup where it is long. y is rounded before the next norm reads it: the backward pass, which
+// Bound by HBM: each row is read once and held in registers between its sums and its result (but for the
+// longest ones' gradients, see with_backward_shape), so neither pass keeps statistics for the other. A row
+// is held by 8 to 64 lanes of a wave, or by a workgroup where it is long. The forward pass reads weights
+// after the row's sum, a group of columns at a time: at 2688 columns one row with both norms waits for
+// eight loads in turn. y is rounded before the next norm reads it: the backward pass, which
 // has y as it is stored, then differentiates the same function. Sums run in fp32; where a sum of
 // squares passes fp32 it is taken again of smaller values, a branch that no ordinary row takes.
 // Measured (bf16; a copy of 4 GiB reaches 4.7 TB/s): forward with both norms and a gate per token, 8192
-// x 2688, 36 us, 4.9 TB/s; one row 4.4 us; backward with both norms and a gate per element, 8192 x 4096,
-// 98 us, 5.5 TB/s of operands and results, and 5.6 us for the weights' gradients; with a gate per token,
-// 8192 x 2688, 64 and 5 us.
+// x 2688, 32 to 36 us, 4.9 to 5.6 TB/s; one row 4.6 us, of one norm alone 2.5; backward with both norms and
+// a gate per element, 8192 x 4096, 95 us, 5.9 TB/s, and 6 us for the weights' gradients; with a gate per
+// token, 8192 x 2688, 58 and 5 us. Rows none of which has a gradient from the next norm: up to 5% more.
 // Included once, by backward.hip.
 #pragma once
 
@@ -521,10 +523,15 @@ __global__ __launch_bounds__(kRedThreads) void block_reduce_kernel(const float* 
   }
 }
 
-// Lanes of a row and groups of eight columns a lane: the fewest lanes that leave registers for four
-// waves a SIMD, up to four groups forward, where a lane holds three operands, and two backward, where
-// it holds five, a gradient and two sums (four: 326 registers and one wave a SIMD). Microseconds with
-// two groups / one on twice the lanes: 8192 x 4096 108 / 106, 8192 x 2688 67 / 76, 16384 x 1024 44 / 51.
+// Lanes of a row and groups of eight columns a lane. Forward up to four groups: a lane holds three
+// operands, at most 115 registers, four waves a SIMD. Backward up to two: it holds five operands, a gradient
+// and two sums, 146 registers for bf16 (three waves a SIMD), 186 for fp32 (two), 87 to 111 for the norm
+// alone; four groups took 326 and one wave a SIMD. Microseconds with two groups / one on twice the lanes:
+// 8192 x 4096 108 / 106, 8192 x 2688 67 / 76, 16384 x 1024 44 / 51.
+// A workgroup of 1024 lanes has 128 registers a lane, one of 768 has 168, so the residual's gradient spills
+// inside the walk: past 12288 columns 44 bytes a lane (bf16), 100 (bf16 with fp32 dh) or 196 (fp32), fp32
+// past 8192 36. As many elements, 8192 x 4096 / 2048 x 16384: bf16 95 / 114 us, fp32 212 / 329, of whose 819
+// MB written 390 are spilled.
 template <typename Fn>
 void with_forward_shape(int H, Fn&& fn) {
   const int g = (H + 7) / 8;
@@ -561,10 +568,13 @@ void with_backward_shape(int H, Fn&& fn) {
 #undef MOE_SHAPE
 }
 
-// Workgroups of the backward pass: as many on each of the 256 CUs as its registers hold, since each
-// ends with a row of partial sums and a second round would leave most CUs idle. Microseconds with 8 /
-// 12 / 16 waves a CU (two groups a lane): 8192 x 4096 108 / 108 / 119, 16384 x 1024 47 / 44 / 52, 16384 x
-// 4096 165 / 156 / 184; 8192 x 2688, 6 / 9 / 12 waves, 81 / 71 / 67.
+// Workgroups of the backward pass: 16 waves on each of the 256 CUs, at most 12 where a lane has two groups,
+// which is what the registers of the residual's bf16 gradient hold: each ends with a row of partial sums,
+// and a second round leaves most CUs idle. Other forms get the same number: fp32 with a residual holds
+// eight, so a third of its workgroups run in a second round (8192 x 4096 212 us, 5.2 TB/s); the norm alone
+// would hold 16 to 20. Microseconds of bf16 with a residual, 8 / 12 / 16 waves a CU (two groups a lane):
+// 8192 x 4096 108 / 108 / 119, 16384 x 1024 47 / 44 / 52, 16384 x 4096 165 / 156 / 184; 8192 x 2688, 6 / 9 / 12
+// waves, 81 / 71 / 67.
 int backward_groups(int T, int H) {
   int groups = 0;
   with_backward_shape(H, [&](auto tpr, auto nc) {

@@ -10,8 +10,9 @@
 // the conversion hides under the loads, and no gradient over- or underflows on the way to the root.
 // Bound by HBM: the norm is needed before the first value can be written, so gradients are read
 // twice and written once, the second reading, last chunk first, from the last-level cache (256 MB)
-// where they fit. Measured: 2.19 GB of fp32 308 us (7.1 TB/s read) and 790 us (5.5 TB/s), 192 tensors of
-// 113 MB, bf16 and fp32, 21 and 36 us (5.4 and 6.2 TB/s); one launch on 4 MB about 3 us.
+// where they fit. Measured: 2.19 GB of fp32 312 us (7.1 TB/s read) and 793 us (5.5 TB/s), 192 tensors of
+// 113 MB, bf16 and fp32, 21 and 36 us (5.5 and 6.2 TB/s); one launch on 4 MB about 3 us. The table costs
+// the caller's host time, about 1.4 us a tensor, once for all calls.
 // Included once, by backward.hip.
 #pragma once
 

@@ -5,11 +5,12 @@
 //   dots        dw[t, j] = <a[t], b[pos[t, j]]>                (gradient of the weights, with either)
 //
 // All are bound by HBM: a token's row is read or written once, its k rows once each. A wave takes
-// 512 columns of one token, eight elements a lane, and walks the token's k rows, eight in flight. Rows
-// are buffers of their own (RowBuffer): a dropped pair's has no size, so no lane branches.
+// 512 columns of one token, eight elements a lane, and walks the token's k rows in batches of up to eight,
+// of whose loads the compiler keeps some or all in flight (gather_kernel, token_kernel). Rows are buffers
+// of their own (RowBuffer): a dropped pair's has no size, so no lane branches.
 // Measured (a copy of 4 GiB reaches 4.7 TB/s): spread of 8192 tokens to 6 experts, 2688 bf16 columns,
-// 50 us, 6.2 TB/s; gated sum of 1001 tokens, 24 slots a quarter of them kept, 1024 fp32 columns, 7.5 us,
-// 4.1 TB/s; gradients of the gated sum, 4096 tokens, 24 slots, 1024 bf16 columns, 86 us, 4.8 TB/s.
+// 51 us, 6.1 TB/s; gated sum of 1001 tokens, 24 slots a quarter of them kept, 1024 fp32 columns, 7.2 us,
+// 4.3 TB/s; gradients of the gated sum, 4096 tokens, 24 slots, 1024 bf16 columns, 86 us, 4.8 TB/s.
 // Included once, by routing.hip.
 #pragma once
 
@@ -203,8 +204,12 @@ __device__ __forceinline__ void add_rows(const Pairs& pr, int j0, const Raw8<ROW
   }
 }
 
-// The gated sum where units fill the chip: B rows of a token in flight, fp32 sums in slot order, one
-// rounding (8192 tokens, 6 slots, 2688 bf16 columns: 55 to 59 us, 5.2 to 5.6 TB/s).
+// The gated sum where units fill the chip: batches of B rows, fp32 sums in slot order, one rounding. As
+// compiled a batch's loads are in flight together where the result is fp32 and for eight bf16 rows to
+// bf16; two or four of them, and fp32 rows to bf16 (22 registers for any B), are waited for one row after
+// another, which the eight waves of a SIMD hide where tokens are many. Microseconds (TB/s), bf16, 2688
+// columns: 8192 tokens, 6 slots 52 (6.0), 12288, 4 59 (5.7), 16384, 2 50 (5.4); fp32 rows to bf16, 4096, 24,
+// 1024 columns 73 (5.8).
 template <Elt IN, Elt OUT, int B, bool STREAM>
 __global__ __launch_bounds__(256) void gather_kernel(TokenRows p, const void* in, const void* add,
                                                      void* out) {
@@ -339,9 +344,15 @@ __global__ __launch_bounds__(256) void sort_small_kernel(const int32_t* __restri
 // A workgroup per token: `segs` waves share its columns (wave v takes v * 512 + n * segs * 512), and
 // `cuts` of each share its pairs (eight at a time in turn), where tokens are too few to fill the chip.
 // What the cuts of a column add up to, and the waves' shares of a dot product, are joined through
-// LDS in wave order. Microseconds without cuts / with (24 slots, 1024 bf16 columns; gated sum, its
-// gradients, the sort's): 64 tokens 4.8 / 4.4, 7.3 / 5.5 and 7.0 / 5.4; 1001 tokens 11.8 / 12.1, 24.3 / 24.6
-// and 14.1 / 13.8, the gated sum of fp32 rows with a quarter of the pairs kept 9.8 / 7.5.
+// LDS in wave order. As compiled Gather and SpreadDot have a batch's loads in flight; GatherDot, whose
+// dot products are reduced meanwhile, two or three of eight bf16 rows and four of six, fp32 rows two or
+// three.
+// Microseconds with cuts / without (24 slots, 1024 columns, two units a token; gated sum, the sort's
+// gradients, its own): bf16, 250 tokens 3.5 / 4.1, 4.5 / 5.7, 6.1 / 7.4; 500 4.6 / 4.4, 6.0 / 7.9,
+// 9.3 / 10.0; 1001 9.8 / 9.2, 10.8 / 10.5, 16.9 / 17.1; 2000 17.4 / 17.4, 19.6 / 18.1, 32.5 / 31.7; 4000
+// 32.5 / 33.0, 33.4 / 34.4, 65 / 66. A quarter of the pairs kept: bf16, 1001 5.6 / 5.0, 7.1 / 7.5, 8.0 / 8.9;
+// 4000 15.6 / 11.8, 21.9 / 18.2, 28.3 / 24.7; fp32 rows, 1001 6.4 / 6.2, 7.6 / 8.2, 11.8 / 11.3; 4000
+// 19.5 / 30.6, 34.9 / 33.0, 49 / 50.
 enum class Pass { Gather, GatherDot, SpreadDot, Spread };
 constexpr int kMostWaves = 16;
 // Gather, GatherDot: out[t] = add[t] + sum_j w rows[pos] (add, out: IN). SpreadDot: out[pos] = w a[t]
@@ -498,9 +509,10 @@ __global__ __launch_bounds__(256) void narrow_kernel(TokenRows p, const void* a,
 
 int64_t units_of(const TokenRows& p) { return (int64_t)p.T * ((p.D + kSeg - 1) / kSeg); }
 dim3 seg_grid(const TokenRows& p) { return dim3((unsigned)((units_of(p) + 3) / 4)); }
-// Rows loaded together: absent ones cost their instructions, so few slots take a smaller batch.
-// Microseconds (2688 columns; gated sum, the sort's gradients, the gated sum's): 2 slots, 16384 tokens,
-// eight / two 62 / 53, 103 / 77 and 107 / 76; 6 slots, 8192 tokens, eight / six 55 / 59, 65 / 60 and 115 / 118.
+// Rows of a batch: absent ones cost their instructions, so few slots take a smaller one.
+// Microseconds of the code as compiled (2688 columns; gated sum, the sort's gradients, the gated sum's): 2
+// slots, 16384 tokens, eight / two 62 / 53, 103 / 77 and 107 / 76; 6 slots, 8192 tokens, eight / six 55 / 59,
+// 62 / 58 and 115 / 118; the sort's gradients of 5 slots 62 / 59, of fp32 113 / 111.
 int batch_of(int k, Pass pass) {
   if (pass == Pass::GatherDot && (k == 5 || k == 6)) return 6;
   return k <= 2 ? 2 : k <= 4 ? 4 : kMostBatch;
@@ -512,7 +524,9 @@ bool past_cache(const TokenRows& p, Elt a, Elt rows, int row_passes) {
   auto bytes = [](Elt t) { return t == Elt::BF16 ? 2 : 4; };
   return (int64_t)p.T * p.D * (bytes(a) + (int64_t)p.k * bytes(rows) * row_passes) > (int64_t)256 << 20;
 }
-// Units that fill the chip with eight waves a SIMD: with as many, pairs are not cut.
+// Units that fill the chip with eight waves a SIMD: with as many, pairs are not cut. From about 2000 units
+// on (token_kernel's figures) cutting pays for the gated sum of fp32 rows alone, most where few pairs are
+// kept (half as long again without), while bf16 rows then lose up to a third by it.
 constexpr int64_t kFull = 8192;
 struct Waves {
   int segs, cuts;

@@ -1,5 +1,5 @@
 """Block gradients whose workgroups walk over several rows each, against the formulas in float64 (on the
-GPU, in elementary operations), with bounds that a single lost row would pass."""
+GPU, in elementary operations), with bounds that a single lost row exceeds."""
 import pytest
 import torch
 
