@@ -3,12 +3,20 @@
 // allocates or waits. Included once, by moe_api.cpp, after its helpers.
 #pragma once
 
+#include <initializer_list>
+
 namespace {
 
 bool float_type(moe_dtype_t t) { return t == MOE_F32 || t == MOE_BF16; }
 Elt elt_of(moe_dtype_t t) { return t == MOE_F32 ? Elt::F32 : Elt::BF16; }
 bool aligned32(const void* p) { return ((uintptr_t)p & 31u) == 0; }
 bool absent_or_aligned(const void* p) { return !p || aligned16(p); }
+// Arrays of 32-bit values, or absent ones.
+bool words(std::initializer_list<const void*> all) {
+  for (const void* p : all)
+    if ((uintptr_t)p & 3u) return false;
+  return true;
+}
 
 // ---- token rows
 constexpr int kRowsMaxD = 1 << 20;
@@ -139,7 +147,7 @@ int32_t moe_sort_tokens(const void* x, moe_dtype_t dt, const int32_t* idx, const
   if (rc) return rc;
   if (!float_type(dt)) return MOE_ERR_UNSUPPORTED;
   if (!offsets || (T && (!x || !idx || !rows || !pos)) || !absent_or_aligned(x) ||
-      !absent_or_aligned(rows))
+      !absent_or_aligned(rows) || !words({idx, weights, offsets, pos}))
     return MOE_ERR_INVALID_ARG;
   hipStream_t s = (hipStream_t)stream;
   if (pl.total == 0)
@@ -166,7 +174,7 @@ int32_t moe_sort_tokens_backward(const void* drows, const void* x, moe_dtype_t d
   if (!float_type(dt) || !float_type(dx_dt)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if ((n_rows && !drows) || !pos || !dx || (dweights && !x) || !absent_or_aligned(drows) ||
-      !absent_or_aligned(x) || !aligned16(dx))
+      !absent_or_aligned(x) || !aligned16(dx) || !words({pos, weights, dweights}))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_gather_rows(token_rows_of(pos, weights, T, D, k, n_rows), elt_of(dt),
                                        drows, nullptr, elt_of(dx_dt), dx, x, dweights,
@@ -182,7 +190,7 @@ int32_t moe_unsort_tokens(const void* rows, moe_dtype_t dt, const int32_t* pos,
   if (!float_type(dt) || !float_type(y_dt)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if ((n_rows && !rows) || !pos || !y || !absent_or_aligned(rows) || !absent_or_aligned(add) ||
-      !aligned16(y))
+      !aligned16(y) || !words({pos, weights}))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_gather_rows(token_rows_of(pos, weights, T, D, k, n_rows), elt_of(dt),
                                        rows, add, elt_of(y_dt), y, nullptr, nullptr,
@@ -200,7 +208,7 @@ int32_t moe_unsort_tokens_backward(const void* dy, moe_dtype_t dy_dt, const void
   if (!dweights && dt != dy_dt) return MOE_ERR_UNSUPPORTED;   // rows of dy's type alone
   if (T == 0) return MOE_OK;
   if (!dy || !pos || (n_rows && !drows) || (dweights && n_rows && !rows) || !aligned16(dy) ||
-      !absent_or_aligned(rows) || !absent_or_aligned(drows))
+      !absent_or_aligned(rows) || !absent_or_aligned(drows) || !words({pos, weights, dweights}))
     return MOE_ERR_INVALID_ARG;
   const TokenRows r = token_rows_of(pos, weights, T, D, k, n_rows);
   hipStream_t s = (hipStream_t)stream;
@@ -255,7 +263,7 @@ int32_t moe_block_norm_backward(const void* dh, moe_dtype_t dh_dt, const void* x
   if (dh_dt != dt && dh_dt != MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (T && (!dh || !x || !dx)) return MOE_ERR_INVALID_ARG;
   if (!absent_or_aligned(dh) || !absent_or_aligned(x) || !absent_or_aligned(w) ||
-      !absent_or_aligned(dres) || !absent_or_aligned(dx))
+      !absent_or_aligned(dres) || !absent_or_aligned(dx) || !words({dw}))
     return MOE_ERR_INVALID_ARG;
   if ((rc = block_workspace(b, dw != nullptr, ws, ws_bytes))) return rc;
   BlockBackward p;
@@ -281,6 +289,7 @@ int32_t moe_block_residual_backward(const void* dy, const void* f, const void* w
   const void* all[] = {dy, f, w, gate, y, dh, w_next, dx, df, dgate};
   for (const void* q : all)
     if (!absent_or_aligned(q)) return MOE_ERR_INVALID_ARG;
+  if (!words({dw, dw_next})) return MOE_ERR_INVALID_ARG;
   if ((rc = block_workspace(b, dw || dw_next, ws, ws_bytes))) return rc;
   BlockBackward p;
   p.dy = dy; p.f = f; p.w = w; p.gate = gate; p.y = y; p.dh = dh; p.dh_t = elt_of(dh_dt);

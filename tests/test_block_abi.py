@@ -359,3 +359,29 @@ def test_numbers_of_experts_that_there_cannot_be_are_refused_first():
     for E in (0, 1025, (1 << 31) - 1):
         with pytest.raises(moe.MoeError):
             moe.sort_tokens(x, idx, E)
+
+
+# ------------------------------------------------- arrays of 32-bit values: aligned to 4 bytes
+
+HALF = C.c_void_p(0x10002)
+
+
+@pytest.mark.parametrize("fn,args,names", [
+    ("moe_sort_tokens", dict(x=FAKE, dt=1, idx=ODD, w=ODD, T=4000, D=64, E=8, k=2, rows=FAKE, offsets=ODD,
+                             pos=ODD, ws=FAKE, n=BIG), ("idx", "w", "offsets", "pos")),
+    ("moe_sort_tokens_backward", dict(drows=FAKE, x=FAKE, dt=1, pos=ODD, w=ODD, T=4, D=64, k=2, n=8, dx=FAKE,
+                                      dx_dt=0, dweights=ODD), ("pos", "w", "dweights")),
+    ("moe_unsort_tokens", dict(rows=FAKE, dt=1, pos=ODD, w=ODD, add=FAKE, T=4, D=64, k=2, n=8, y=FAKE,
+                               y_dt=0), ("pos", "w")),
+    ("moe_unsort_tokens_backward", dict(dy=FAKE, dy_dt=1, rows=FAKE, dt=1, pos=ODD, w=ODD, T=4, D=64, k=2,
+                                        n=8, drows=FAKE, dweights=ODD), ("pos", "w", "dweights")),
+    ("moe_block_norm_backward", dict(dh=FAKE, dh_dt=0, x=FAKE, w=FAKE, dres=FAKE, dx=FAKE, dw=ODD, T=4, H=64,
+                                     dt=1, w_dt=1, eps=1e-5, ws=FAKE, n=BIG), ("dw",)),
+    ("moe_block_residual_backward", dict(dy=FAKE, f=FAKE, w=FAKE, gate=FAKE, y=FAKE, dh=FAKE, dh_dt=1,
+                                         w_next=FAKE, dx=FAKE, df=FAKE, dw=ODD, dgate=FAKE, dw_next=ODD,
+                                         T=4, H=64, dt=1, w_dt=1, flags=11, scale=1.0, eps=1e-5, ws=FAKE,
+                                         n=BIG), ("dw", "dw_next")),
+])
+def test_misaligned_arrays_of_words(fn, args, names):
+    for name in names:
+        assert getattr(moe.lib(), fn)(*dict(args, **{name: HALF}).values(), None) == BAD, name
