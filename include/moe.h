@@ -332,7 +332,8 @@ int32_t moe_mx_gemm(const void *A, const uint8_t *a_scales, moe_dtype_t a_fmt, c
  * expert of another rank, so k > E is allowed here) or repeats an expert of its token, and where pos
  * is outside [0, n_rows): nothing is read or written for it, and its weight's gradient is 0. Rows
  * behind the last pair are left as they were. weights [T, k] fp32, or NULL for 1; they may be any
- * values. Sums run in fp32 in a fixed order and are rounded once; all results are deterministic.
+ * values. Sums run in fp32 in a fixed order and are rounded once; all results are deterministic. Results
+ * overlap no operand and no other result but where that is said.
  * D a multiple of 16 up to 2^20, k <= 64, T * ceil(D / 512) <= 2^25, T * k < 2^31. dt, dx_dt, y_dt,
  * dy_dt: MOE_BF16 or MOE_F32. Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size),
  * MOE_ERR_UNSUPPORTED (types), MOE_ERR_WORKSPACE. */
@@ -373,7 +374,7 @@ int32_t moe_unsort_tokens_backward(const void *dy, moe_dtype_t dy_dt, const void
  *            ([T, H] of type dt, MOE_GATE_ELEMENT), or its sigmoid (MOE_GATE_SIGMOID);
  *            h = n(y) w_next, of y as it is stored (h NULL: not wanted).
  * x, f, y, h [T, H] of type dt (MOE_BF16 or MOE_F32); w, w_next [H] of type w_dt, or NULL for 1.
- * y may be x or f, and h may be x (before). Sums run in fp32 (where squares pass it, of smaller
+ * y may be x or f, and h may be x (before) or f (after); nothing else overlaps. Sums run in fp32 (where squares pass it, of smaller
  * values), each result is rounded once. A row that holds a NaN or an infinity reaches no other row of y and h.
  * H a multiple of 16 up to 16384, T < 2^23, eps >= 1e-30. Errors: MOE_ERR_INVALID_ARG (null or
  * misaligned pointer, bad size or flags, a gate without its flag), MOE_ERR_UNSUPPORTED (types). */

@@ -95,6 +95,37 @@ def test_residual_gradients_of_far_rows(H, dtype, dh_dtype):
             O.check(got[n], ref[n][0], dtype, ref[n][1], GRAD + SUM, (n, size, grad))
 
 
+@pytest.mark.parametrize("H", [16, 64, 128, 208, 256, 304, 1040, 2704])
+def test_far_rows_leave_the_others_alone(H):
+    """Rows that are summed again, next to rows that are not, in one wave where they are short: those come
+    out bit for bit as without them, and all as they should."""
+    g = torch.Generator().manual_seed(H + 4)
+    T = 70
+    f, y = torch.randn(T, H, generator=g).cuda(), torch.randn(T, H, generator=g).cuda()
+    dy, dh = torch.randn(T, H, generator=g).cuda(), torch.randn(T, H, generator=g).cuda()
+    gate = torch.randn(T, generator=g).cuda()
+    clean = moe.block_residual_backward(dy, f, gate=gate, y=y, dh=dh)
+    far = torch.rand(T, generator=g) < 0.4
+    kind = torch.randint(0, 4, (T,), generator=g)
+    for t in torch.nonzero(far).flatten().tolist():
+        if kind[t] == 0:
+            y[t] *= 1e30
+        elif kind[t] == 1:
+            y[t] *= 1e15
+            dh[t] *= 1e23
+        elif kind[t] == 2:
+            dh[t] = 0
+        else:
+            f[t] *= 1e25
+    got = moe.block_residual_backward(dy, f, gate=gate, y=y, dh=dh)
+    ref = O.residual_grad(O.f64(dy), O.f64(f), None, True, O.f64(gate), "sigmoid", 1.0, O.f64(y), O.f64(dh), None,
+                          1e-5)
+    near_rows = ~far
+    for n in got:
+        assert torch.equal(got[n].cpu()[near_rows], clean[n].cpu()[near_rows]), n
+        O.check(got[n], ref[n][0], F32, ref[n][1], GRAD + SUM, n)
+
+
 def test_rows_without_a_gradient_pass_what_reaches_them():
     """dh of zeros, as a masked token leaves it: dx is dres bit for bit, whatever the row."""
     g = torch.Generator().manual_seed(3)
