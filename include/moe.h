@@ -374,8 +374,9 @@ int32_t moe_unsort_tokens_backward(const void *dy, moe_dtype_t dy_dt, const void
  *            ([T, H] of type dt, MOE_GATE_ELEMENT), or its sigmoid (MOE_GATE_SIGMOID);
  *            h = n(y) w_next, of y as it is stored (h NULL: not wanted).
  * x, f, y, h [T, H] of type dt (MOE_BF16 or MOE_F32); w, w_next [H] of type w_dt, or NULL for 1.
- * y may be x or f, and h may be x (before) or f (after); nothing else overlaps. Sums run in fp32 (where squares pass it, of smaller
- * values), each result is rounded once. A row that holds a NaN or an infinity reaches no other row of y and h.
+ * y may be x or f, and h may be x (before) or f (after); nothing else overlaps. Sums run in fp32
+ * (where squares pass it, of smaller values), each result is rounded once. A row that holds a NaN or
+ * an infinity reaches no other row of y and h.
  * H a multiple of 16 up to 16384, T < 2^23, eps >= 1e-30. Errors: MOE_ERR_INVALID_ARG (null or
  * misaligned pointer, bad size or flags, a gate without its flag), MOE_ERR_UNSUPPORTED (types). */
 #define MOE_BLOCK_NORM 1u
@@ -421,10 +422,11 @@ int32_t moe_block_residual_backward(const void *dy, const void *f, const void *w
  * moe_clip_plan writes their table into `plan` (device, moe_clip_plan_size bytes, 32-byte aligned)
  * by kernels on `stream` and fills `clip` (host). moe_clip_grads, on that stream or ordered behind
  * it, may then be called any number of times while the tensors and the plan stay in place; calls
- * that share a plan must not overlap. A plan made on a stream that is captured is written by the
- * graph's replays alone: calls outside of that capture are refused. It uses `plan` for scratch too. Errors: MOE_ERR_INVALID_ARG
- * (null or misaligned pointer, bad size, max_norm < 0 or NaN, another capture's plan),
- * MOE_ERR_UNSUPPORTED (types), MOE_ERR_WORKSPACE (plan missing, misaligned or too small). */
+ * that share a plan must not overlap, since it is used for scratch too. A plan made on a stream that
+ * is captured is written by the graph's replays alone: calls outside of that capture are refused.
+ * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad size, max_norm < 0 or NaN, another
+ * capture's plan), MOE_ERR_UNSUPPORTED (types), MOE_ERR_WORKSPACE (plan missing, misaligned or too
+ * small). */
 typedef struct {
   void *grad;        /* device */
   void *out;         /* device; NULL: grad */
